@@ -473,6 +473,169 @@ size_t sdm_pa_workspace(const sdm_pa_io* io);
  */
 sdm_status sdm_pa_step(const sdm_pa_io* io, int64_t ti, hipStream_t st);
 
+/* ------------------------------------------------------------------------------------------------
+ * The mixer operators beside the bank: what makes a layer's slot ids, weights, keys and queries, and
+ * the dense state that stands next to the sparse one. Same conventions as above; strides are in
+ * elements and any multiple of one element is accepted (16-byte rows take wide accesses).
+ * ------------------------------------------------------------------------------------------------ */
+
+/* RMS norm of query and key heads and the rotation by position. */
+typedef struct sdm_norm_rope_io {
+    const void* q;          /* head h of token t at q + t * q_row + h * q_head, D contiguous columns */
+    const void* k;
+    int64_t q_row, q_head, k_row, k_head;
+    void* q_out;            /* OUT, the same way; may be q itself (same strides). sdm_norm_rope_backward: the
+                               gradients of q and k */
+    void* k_out;
+    int64_t qo_row, qo_head, ko_row, ko_head;
+    const void* wq;         /* [D] norm weights of the query heads (NULL: ones) */
+    const void* wk;         /* [D] norm weights of the key heads (NULL: ones) */
+    const void* pos;        /* [N] positions, int32 or int64 (pos_bytes); only read when rot > 0. A position
+                               outside 0 .. table_rows-1 takes the nearest row of the table */
+    const float* table;     /* [table_rows, rot] float32: the cosines of a position's rot/2 angles, then the sines */
+    int64_t table_rows;     /* >= 1 when rot > 0 */
+    int64_t N;              /* tokens, >= 0 */
+    int32_t Hq, Hk;         /* query and key heads of a token, >= 0 (0: that tensor is not used) */
+    int32_t D;              /* columns of a head, 1..512 */
+    int32_t rot;            /* columns that turn: even, 0..D */
+    int32_t interleaved;    /* 0: column i turns with i + rot/2; 1: column 2i with 2i + 1 */
+    int32_t dtype;          /* sdm_dtype of the heads (inputs, outputs and gradients) */
+    int32_t w_dtype;        /* sdm_dtype of wq and wk */
+    int32_t pos_bytes;      /* 4 or 8 */
+    float eps;              /* added to the mean of squares, >= 0 */
+} sdm_norm_rope_io;
+
+/*
+ * Per head x: y = x w / sqrt(mean(x^2) + eps), its first rot columns turned by the token's angles:
+ * (y1, y2) -> (y1 c - y2 s, y2 c + y1 s). One kernel on st; float32 inside, rounded once.
+ * Requires N * (Hq + Hk) <= 2^25.
+ */
+sdm_status sdm_norm_rope(const sdm_norm_rope_io* io, hipStream_t st);
+
+typedef struct sdm_norm_rope_grad {
+    const void* dq;         /* gradients of the outputs, laid out like q and k with strides of their own */
+    const void* dk;
+    int64_t dq_row, dq_head, dk_row, dk_head;
+    float* dwq;             /* OUT [D] float32 (NULL: skipped) */
+    float* dwk;
+    void* workspace;        /* sdm_norm_rope_workspace() bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} sdm_norm_rope_grad;
+
+/* The backward of sdm_norm_rope: io as there, with q_out and k_out receiving the gradients of q and k (they
+ * must not overlap q, k, dq or dk). The weights' gradients are summed in a fixed order. Two kernels on st. */
+sdm_status sdm_norm_rope_backward(const sdm_norm_rope_io* io, const sdm_norm_rope_grad* grad, hipStream_t st);
+size_t sdm_norm_rope_workspace(const sdm_norm_rope_io* io);
+
+/* Slot ids and weights from two rows of scores per token. */
+typedef struct sdm_slot_topk_io {
+    const void* a;          /* [N, n1] scores, row t at a + t * a_row */
+    const void* b;          /* [N, n2] */
+    int64_t a_row, b_row;
+    void* idx;              /* [N, K] int32 or int64 (idx_bytes): OUT of sdm_slot_topk, input of the backward */
+    void* val;              /* OUT [N, K] float32 or bf16 (val_dtype); not used by the backward */
+    int64_t N;              /* tokens, >= 0 */
+    int32_t n1, n2;         /* 1..4096 */
+    int32_t K;              /* slots per token, 1..64, at most n1 * n2 */
+    int32_t dtype;          /* sdm_dtype of a and b */
+    int32_t val_dtype;      /* sdm_dtype of val */
+    int32_t idx_bytes;      /* 4 or 8 */
+    float scale;            /* finite, > 0 */
+    int64_t chunk_rows;     /* 0: ids are local. C > 0: tokens come in chunks of C, chunk c belongs to stream c % P
+                               and its ids are absolute, + (c % P) * stream_offset, as sdm_phase1 takes them */
+    int32_t P;              /* streams, >= 1 */
+    int64_t stream_offset;  /* >= 0 */
+} sdm_slot_topk_io;
+
+/*
+ * Per token: the min(K, n) best entries of either row, then the K best sums a[i] + b[j] of those (float32
+ * sums), best first: idx = i n2 + j, val = softmax of the K sums times scale. Larger values come first;
+ * of equal ones the lower column, of equal sums the pair whose a ranks higher, then whose b does. A NaN
+ * score or sum counts as -infinity; a sum of -infinity has weight 0 (all of them when nothing else is
+ * there). One kernel on st.
+ */
+sdm_status sdm_slot_topk(const sdm_slot_topk_io* io, hipStream_t st);
+
+typedef struct sdm_slot_topk_grad {
+    const float* dval;      /* [N, K] gradients of the weights */
+    void* da;               /* OUT [N, n1] in dtype, whole rows (NULL: skipped) */
+    void* db;               /* OUT [N, n2] */
+    int64_t da_row, db_row;
+} sdm_slot_topk_grad;
+
+/* The backward of sdm_slot_topk at the selection idx: the weights are recomputed from a, b and idx (ids out of
+ * range are taken to the nearest slot). A slot of weight 0 has gradient 0. One kernel on st, no atomics. */
+sdm_status sdm_slot_topk_backward(const sdm_slot_topk_io* io, const sdm_slot_topk_grad* grad, hipStream_t st);
+
+/* The gated linear recurrence: a dense state per stream and head. */
+typedef struct sdm_glr_io {
+    const void* q;          /* [B, T, Hk, dk]: element (b, t, h) at q + b q_b + t q_t + h q_h, dk contiguous columns */
+    const void* k;          /* [B, T, Hk, dk] */
+    const void* v;          /* [B, T, H, dv] */
+    const float* g;         /* [B, T, H] log gates (<= 0; -infinity, or anything at or below -10000, resets the state) */
+    int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, g_b, g_t, g_h;
+    const float* state;     /* [B, H, dk, dv] contiguous, the state before the first token (NULL: zero) */
+    const int32_t* lens;    /* [B] tokens of each stream (NULL: T); a value outside 0..T is taken to the nearest.
+                               Later tokens are not read, leave the state alone and get zero outputs */
+    void* o;                /* OUT of sdm_glr_forward [B, T, H, dv], strided */
+    int64_t o_b, o_t, o_h;
+    float* last;            /* OUT of sdm_glr_forward [B, H, dk, dv] contiguous: the state after the last token (NULL: skipped;
+                               must not be `state`) */
+    int32_t B, T;           /* >= 0 */
+    int32_t H, Hk;          /* value heads, and query / key heads: H a multiple of Hk; value head h uses head h / (H / Hk) */
+    int32_t dk, dv;         /* 1..128 */
+    int32_t dtype;          /* sdm_dtype of q, k, v, o and their gradients */
+    float scale;
+    void* workspace;        /* sdm_glr_workspace() bytes, 256-byte aligned (may be NULL when that is 0) */
+    size_t workspace_bytes;
+} sdm_glr_io;
+
+/*
+ * Per stream and head, from S = state:  S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t.
+ * States and sums are float32; of bfloat16 inputs every product is exact, and a float32 factor (a decayed
+ * score, a state) enters a matrix product as two or three bfloat16 parts. Requires B * H <= 2^20,
+ * B * T * H <= 2^31 - 1.
+ */
+sdm_status sdm_glr_forward(const sdm_glr_io* io, hipStream_t st);
+size_t sdm_glr_workspace(const sdm_glr_io* io, int32_t backward);
+
+typedef struct sdm_glr_grad {
+    const void* d_o;        /* [B, T, H, dv] gradients of o, strided */
+    int64_t do_b, do_t, do_h;
+    const float* d_last;    /* [B, H, dk, dv] contiguous gradient of the last state (NULL: zero) */
+    void* dq;               /* OUT [B, T, Hk, dk] contiguous, in dtype */
+    void* dk;               /* OUT [B, T, Hk, dk] */
+    void* dv;               /* OUT [B, T, H, dv] */
+    float* dg;              /* OUT [B, T, H] float32 */
+    float* d_state;         /* OUT [B, H, dk, dv] float32: the gradient of `state` (NULL: skipped) */
+} sdm_glr_grad;
+
+/* The backward of sdm_glr_forward (io's o and last are not used; its workspace is of the backward size). Heads that
+ * share a query and key head add their gradients in head order. No atomics: the bits are the same every run. */
+sdm_status sdm_glr_backward(const sdm_glr_io* io, const sdm_glr_grad* grad, hipStream_t st);
+
+/* One token of many requests. */
+typedef struct sdm_glr_step_io {
+    const void* q;          /* [B, Hk, dk]: element (b, h) at q + b q_b + h q_h */
+    const void* k;
+    const void* v;          /* [B, H, dv] */
+    const float* g;         /* [B, H] */
+    int64_t q_b, q_h, k_b, k_h, v_b, v_h, g_b, g_h;
+    const float* state;     /* [rows, H, dk, dv] contiguous */
+    float* new_state;       /* OUT, laid out the same; may be `state` */
+    int64_t rows;
+    const int32_t* slots;   /* [B] row of each request (NULL: row b). A request whose row is outside 0..rows-1 is left
+                               out: its output is 0 and no state is read or written. Rows must be distinct */
+    void* o;                /* OUT [B, H, dv], strided */
+    int64_t o_b, o_h;
+    int32_t B, H, Hk, dk, dv;   /* as in sdm_glr_io; dk, dv 1..128 */
+    int32_t dtype;
+    float scale;
+} sdm_glr_step_io;
+
+/* The recurrence by one token: the state is read once and written once. One kernel on st. */
+sdm_status sdm_glr_step(const sdm_glr_step_io* io, hipStream_t st);
+
 /* Static text for a status code. */
 const char* sdm_status_string(sdm_status s);
 

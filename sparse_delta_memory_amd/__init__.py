@@ -8,6 +8,13 @@ libsdm_amd.so. There is no CPU fallback: without the built library every call ra
     out = phase1(shape, k_idx, q_idx, k_val, q_val, g)          # dict of device tensors
     dw_step(bank, dv, out["krec"], shape, ti, dv_step_rows=P*C)  # bank updated in place
     read_step(bank, out, k_idx, q_idx, v, beta, dv, pred, read, shape, ti, step_rows=P*C)  # before DW
+
+Beside the bank (mixer_ops.py): the slot ids and weights a layer gives Phase 1, its query and key heads,
+and the dense state that stands next to the sparse one, each with its backward pass.
+
+    q, k = norm_rope(q, k, wq, wk, positions, rope_table(rows, rot))
+    k_idx, k_val = slot_topk(scores_a, scores_b, W)
+    o, last = glr_forward(q, k, v, g)                            # glr_step: one token of many requests
 """
 
 from __future__ import annotations
@@ -20,7 +27,8 @@ from ._lib import P1IO, P1Shape, SdmError  # noqa: F401
 __all__ = ["P1Shape", "phase1", "phase1_pairs", "phase1_workspace_bytes", "alloc_phase1_outputs", "dw_step", "dw_workspace_bytes",
            "alloc_dw_workspace", "DwPlan", "ReadPlan", "read_step", "gds_step", "gds_workspace_bytes", "alloc_gds_workspace", "gwr_step", "pa_step", "pa_workspace_bytes",
            "alloc_pa_workspace", "SdmError", "make_shape",
-           "timing_events"]
+           "timing_events", "norm_rope", "norm_rope_backward", "rope_table", "slot_topk", "slot_topk_backward", "glr_forward",
+           "glr_backward", "glr_step", "glr_workspace_bytes"]
 
 
 def make_shape(N, C, W, R, P=1, key_bits=16, stream_offset=0, first_partial=None, valid_last=None, tile_len=128,
@@ -453,3 +461,7 @@ def pa_step(grad, snap, p1, beta, d_dva, shape: P1Shape, ti: int, step_rows: int
         io.workspace_bytes = workspace.numel() * workspace.element_size()
     st = torch.cuda.current_stream(grad.device) if stream is None else stream
     _lib.check(lib.sdm_pa_step(ctypes.byref(io), int(ti), ctypes.c_void_p(st.cuda_stream)))
+
+
+from .mixer_ops import (  # noqa: E402,F401
+    glr_backward, glr_forward, glr_step, glr_workspace_bytes, norm_rope, norm_rope_backward, rope_table, slot_topk, slot_topk_backward)

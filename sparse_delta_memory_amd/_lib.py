@@ -106,8 +106,61 @@ class PaIO(ctypes.Structure):
     ]
 
 
+class NormRopeIO(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k")] + [
+        (f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head")] + [
+        ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("qo_row", "qo_head", "ko_row", "ko_head")] + [
+        (f, ctypes.c_void_p) for f in ("wq", "wk", "pos", "table")] + [
+        ("table_rows", ctypes.c_int64), ("N", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("Hq", "Hk", "D", "rot", "interleaved", "dtype", "w_dtype", "pos_bytes")] + [
+        ("eps", ctypes.c_float)]
+
+
+class NormRopeGrad(ctypes.Structure):
+    _fields_ = [("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("dq_row", "dq_head", "dk_row", "dk_head")] + [
+        (f, ctypes.c_void_p) for f in ("dwq", "dwk", "workspace")] + [("workspace_bytes", ctypes.c_size_t)]
+
+
+class SlotTopkIO(ctypes.Structure):
+    _fields_ = [("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("a_row", ctypes.c_int64), ("b_row", ctypes.c_int64),
+                ("idx", ctypes.c_void_p), ("val", ctypes.c_void_p), ("N", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("n1", "n2", "K", "dtype", "val_dtype", "idx_bytes")] + [
+        ("scale", ctypes.c_float), ("chunk_rows", ctypes.c_int64), ("P", ctypes.c_int32), ("stream_offset", ctypes.c_int64)]
+
+
+class SlotTopkGrad(ctypes.Structure):
+    _fields_ = [("dval", ctypes.c_void_p), ("da", ctypes.c_void_p), ("db", ctypes.c_void_p), ("da_row", ctypes.c_int64),
+                ("db_row", ctypes.c_int64)]
+
+
+class GlrIO(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v", "g")] + [
+        (f, ctypes.c_int64) for f in ("q_b", "q_t", "q_h", "k_b", "k_t", "k_h", "v_b", "v_t", "v_h", "g_b", "g_t", "g_h")] + [
+        ("state", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("o", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("o_b", "o_t", "o_h")] + [("last", ctypes.c_void_p)] + [
+        (f, ctypes.c_int32) for f in ("B", "T", "H", "Hk", "dk", "dv", "dtype")] + [
+        ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GlrGrad(ctypes.Structure):
+    _fields_ = [("d_o", ctypes.c_void_p)] + [(f, ctypes.c_int64) for f in ("do_b", "do_t", "do_h")] + [
+        (f, ctypes.c_void_p) for f in ("d_last", "dq", "dk", "dv", "dg", "d_state")]
+
+
+class GlrStepIO(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v", "g")] + [
+        (f, ctypes.c_int64) for f in ("q_b", "q_h", "k_b", "k_h", "v_b", "v_h", "g_b", "g_h")] + [
+        ("state", ctypes.c_void_p), ("new_state", ctypes.c_void_p), ("rows", ctypes.c_int64), ("slots", ctypes.c_void_p),
+        ("o", ctypes.c_void_p), ("o_b", ctypes.c_int64), ("o_h", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("B", "H", "Hk", "dk", "dv", "dtype")] + [("scale", ctypes.c_float)]
+
+
 EXPORTS = ["sdm_phase1_workspace", "sdm_phase1", "sdm_phase1_pairs", "sdm_dw_workspace", "sdm_dw_step", "sdm_dw_step_noalloc", "sdm_read_step",
-           "sdm_gds_workspace", "sdm_gds_step", "sdm_gwr_step", "sdm_pa_workspace", "sdm_pa_step", "sdm_status_string", "sdm_last_error"]
+           "sdm_gds_workspace", "sdm_gds_step", "sdm_gwr_step", "sdm_pa_workspace", "sdm_pa_step", "sdm_norm_rope",
+           "sdm_norm_rope_workspace", "sdm_norm_rope_backward", "sdm_slot_topk", "sdm_slot_topk_backward", "sdm_glr_workspace",
+           "sdm_glr_forward", "sdm_glr_backward", "sdm_glr_step", "sdm_status_string", "sdm_last_error"]
 
 _lock = threading.Lock()
 _lib = None
@@ -152,6 +205,16 @@ def load() -> ctypes.CDLL:
         lib.sdm_pa_workspace.restype = ctypes.c_size_t
         lib.sdm_pa_step.argtypes = [ctypes.POINTER(PaIO), ctypes.c_int64, ctypes.c_void_p]
         lib.sdm_pa_step.restype = ctypes.c_int
+        for name, args in (("sdm_norm_rope", [NormRopeIO]), ("sdm_norm_rope_backward", [NormRopeIO, NormRopeGrad]),
+                           ("sdm_slot_topk", [SlotTopkIO]), ("sdm_slot_topk_backward", [SlotTopkIO, SlotTopkGrad]),
+                           ("sdm_glr_forward", [GlrIO]), ("sdm_glr_backward", [GlrIO, GlrGrad]), ("sdm_glr_step", [GlrStepIO])):
+            fn = getattr(lib, name)
+            fn.argtypes = [ctypes.POINTER(a) for a in args] + [ctypes.c_void_p]
+            fn.restype = ctypes.c_int
+        lib.sdm_norm_rope_workspace.argtypes = [ctypes.POINTER(NormRopeIO)]
+        lib.sdm_norm_rope_workspace.restype = ctypes.c_size_t
+        lib.sdm_glr_workspace.argtypes = [ctypes.POINTER(GlrIO), ctypes.c_int32]
+        lib.sdm_glr_workspace.restype = ctypes.c_size_t
         lib.sdm_status_string.argtypes = [ctypes.c_int]
         lib.sdm_status_string.restype = ctypes.c_char_p
         lib.sdm_last_error.argtypes = []

@@ -22,15 +22,31 @@ namespace {
 
 thread_local std::string g_last_error;
 
+}  // namespace
+
+namespace sdm {
+
 sdm_status fail(sdm_status s, const char* fmt, ...) {
     char buf[512];
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(buf, sizeof(buf), fmt, ap);
     va_end(ap);
-    g_last_error = buf;
+    try {
+        g_last_error = buf;
+    } catch (...) {   // no memory for the message: the status still says what failed
+        g_last_error.clear();
+    }
     return s;
 }
+
+void clear_error() { g_last_error.clear(); }
+
+}  // namespace sdm
+
+namespace {
+
+using sdm::fail;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -45,7 +61,9 @@ struct DeviceSetup {
 };
 DeviceSetup g_setup[kMaxDevices];
 
-hipError_t device_setup(int* lds_max) {
+}  // namespace
+
+hipError_t sdm::device_setup(int* lds_max) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
@@ -55,9 +73,11 @@ hipError_t device_setup(int* lds_max) {
         int lds = 0;
         d.err = hipDeviceGetAttribute(&lds, hipDeviceAttributeMaxSharedMemoryPerBlock, dev);
         if (d.err != hipSuccess) return;
-        const void* fns[128];
-        int n = sdm::p1_lds_kernels(fns, 128);
-        n += sdm::read_lds_kernels(fns + n, 128 - n);
+        const void* fns[256];
+        int n = sdm::p1_lds_kernels(fns, 256);
+        n += sdm::read_lds_kernels(fns + n, 256 - n);
+        n += sdm::slot_lds_kernels(fns + n, 256 - n);
+        n += sdm::glr_lds_kernels(fns + n, 256 - n);
         for (int i = 0; i < n && d.err == hipSuccess; ++i) {
             // The dynamic limit is what the device holds beside the kernel's static LDS.
             hipFuncAttributes fa;
@@ -72,6 +92,10 @@ hipError_t device_setup(int* lds_max) {
     if (lds_max != nullptr) *lds_max = d.lds_max;
     return d.err;
 }
+
+namespace {
+
+using sdm::device_setup;
 
 sdm_status check_p1_shape(const sdm_p1_shape* s) {
     if (s == nullptr) return fail(SDM_EINVAL, "sdm_phase1: shape is NULL");

@@ -135,4 +135,28 @@ struct PaWorkspace {
 };
 PaWorkspace pa_workspace_layout(const sdm_pa_io* io);
 
+// The message of a refused call (sdm_last_error) and its status; clear_error starts an entry point.
+sdm_status fail(sdm_status s, const char* fmt, ...);
+void clear_error();
+// Once per device, before the first launch there: the dynamic-LDS limits (see api.cpp).
+hipError_t device_setup(int* lds_max);
+
+// Head norms with rotation (validated by sdm_norm_rope and sdm_norm_rope_backward). workspace: bytes of the
+// backward's partial weight gradients.
+hipError_t norm_rope_launch(const sdm_norm_rope_io* io, hipStream_t st);
+hipError_t norm_rope_back_launch(const sdm_norm_rope_io* io, const sdm_norm_rope_grad* g, hipStream_t st);
+size_t norm_rope_back_workspace(int64_t N, int H, int D);
+
+// Slot selection (validated by sdm_slot_topk and sdm_slot_topk_backward).
+hipError_t slot_topk_launch(const sdm_slot_topk_io* io, hipStream_t st);
+hipError_t slot_topk_back_launch(const sdm_slot_topk_io* io, const sdm_slot_topk_grad* g, hipStream_t st);
+int slot_lds_kernels(const void** fns, int cap);
+
+// The gated linear recurrence (validated by its entry points).
+hipError_t glr_forward_launch(const sdm_glr_io* io, hipStream_t st);
+hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipStream_t st);
+hipError_t glr_step_launch(const sdm_glr_step_io* io, hipStream_t st);
+size_t glr_workspace_bytes(const sdm_glr_io* io, bool backward);
+int glr_lds_kernels(const void** fns, int cap);
+
 }  // namespace sdm

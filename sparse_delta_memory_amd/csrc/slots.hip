@@ -1,0 +1,459 @@
+// Slot selection: the slot ids and weights of a bank of n1 x n2 slots from two rows of scores per token,
+// and the backward pass.
+//
+// A slot's score is a[i] + b[j], its id i n2 + j. The K best slots lie among the pairs of the K best a
+// and the K best b, so the K best of each row are taken, and of the pairs (i-th best a, j-th best b)
+// only those with (i + 1)(j + 1) <= K can be among the K best: all (i' <= i, j' <= j) are at least as
+// good. Order, everywhere: the larger value first, of equal ones the lower place (column; for pairs the
+// better a, then the better b). A NaN score counts as -infinity. The weights are the softmax of the K
+// sums times `scale`; a sum of -infinity weighs 0, and so does every one when all are.
+//
+// One wave per token. The row sits in registers as ordered keys (the unsigned order is the float
+// order); the K-th best of the 64 lanes' own maxima is a bound that at least K entries meet and few
+// others do, so one sweep of ballots moves the few entries at or above it to LDS, and sorting networks
+// over the 64 lanes (compare-exchange across lanes, no LDS for most steps) order them. Reading the
+// scores bounds it from below; the networks' vector instructions are what it spends its time on.
+#include <hip/hip_runtime.h>
+
+#include "mixer_device.hpp"
+#include "sdm_launch.hpp"
+
+namespace sdm {
+namespace {
+
+constexpr int kStThreads = 256;
+constexpr int kStWaves = kStThreads / kWave;
+
+struct StArgs {
+    sdm_slot_topk_io io;
+    int ka, kb;      // kept entries of each row: min(K, n)
+    int pairs;       // pairs (i, j) with (i + 1)(j + 1) <= K
+    int vec;         // rows take 16-byte loads
+};
+
+// Pairs (i, j) in the order of (i + 1)(j + 1), i in the high byte: the first pair_count(K) of them are
+// those that can win for K.
+constexpr int kStMaxPairs = 280;
+struct PairTable {
+    uint16_t at[kStMaxPairs];
+    uint16_t count[65];
+};
+constexpr PairTable make_pairs() {
+    PairTable t{};
+    int n = 0;
+    for (int p = 1; p <= 64; ++p) {
+        for (int i = 1; i <= p; ++i) {
+            if (p % i == 0) t.at[n++] = static_cast<uint16_t>(((i - 1) << 8) | (p / i - 1));
+        }
+        t.count[p] = static_cast<uint16_t>(n);
+    }
+    return t;
+}
+constexpr PairTable kPairsHost = make_pairs();
+static_assert(kPairsHost.count[64] == kStMaxPairs, "pairs (i, j) with (i + 1)(j + 1) <= 64");
+__constant__ PairTable kPairs = make_pairs();
+
+// Float order as unsigned order; -0 as +0, NaN as -infinity. 0 is below every float's key.
+__device__ __forceinline__ uint32_t key_of(float f) {
+    f = f != f ? -INFINITY : f + 0.0f;
+    const uint32_t u = __float_as_uint(f);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float float_of(uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+// An entry: its key, and the complement of its place, so that the larger pair is the better entry.
+struct Entry {
+    uint32_t key, inv;
+};
+__device__ __forceinline__ bool above(const Entry& a, const Entry& b) {
+    return ((static_cast<uint64_t>(a.key) << 32) | a.inv) > ((static_cast<uint64_t>(b.key) << 32) | b.inv);
+}
+__device__ __forceinline__ Entry pick(bool c, const Entry& a, const Entry& b) {
+    return Entry{c ? a.key : b.key, c ? a.inv : b.inv};
+}
+
+// Compare-exchange with lane ^ M: the lanes of `up` keep the better entry.
+template <int M>
+__device__ __forceinline__ void exchange(Entry& e, bool up) {
+    const Entry o{lane_xor<M>(e.key), lane_xor<M>(e.inv)};
+    e = pick(above(e, o) == up, e, o);
+}
+template <int M>
+__device__ __forceinline__ void exchange_key(uint32_t& k, bool up) {
+    const uint32_t o = lane_xor<M>(k);
+    k = up ? max(k, o) : min(k, o);
+}
+
+// One stage of the sorting network per merge length: best first when `up` holds for the whole length.
+template <int M, typename E, typename F>
+__device__ __forceinline__ void merge_steps(E& e, bool down, F step) {
+    step(std::integral_constant<int, M>{}, e, down);
+    if constexpr (M > 1) merge_steps<M / 2>(e, down, step);
+}
+template <int M, typename E, typename F>
+__device__ __forceinline__ void sort_steps(E& e, F step) {
+    if constexpr (M > 1) sort_steps<M / 2>(e, step);
+    merge_steps<M>(e, M < 32 && (lane_id() & (2 * M)) != 0, step);
+}
+struct EntryStep {
+    template <int M>
+    __device__ __forceinline__ void operator()(std::integral_constant<int, M>, Entry& e, bool down) const {
+        exchange<M>(e, ((lane_id() & M) == 0) != down);
+    }
+};
+struct KeyStep {
+    template <int M>
+    __device__ __forceinline__ void operator()(std::integral_constant<int, M>, uint32_t& k, bool down) const {
+        exchange_key<M>(k, ((lane_id() & M) == 0) != down);
+    }
+};
+// The wave's 64 entries (or keys), best in lane 0.
+__device__ __forceinline__ void sort64(Entry& e) { sort_steps<32>(e, EntryStep{}); }
+__device__ __forceinline__ void sort64(uint32_t& k) { sort_steps<32>(k, KeyStep{}); }
+
+// The best 64 of two sorted lists of 64, sorted: the better of lane l's entry and the other list's
+// entry from the end is one of the 64 best, and those form one rising and falling run.
+__device__ __forceinline__ void merge64(Entry& best, const Entry& other) {
+    const int from = (63 - static_cast<int>(lane_id())) << 2;
+    const Entry o{static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(other.key))),
+                  static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(from, static_cast<int>(other.inv)))};
+    best = pick(above(best, o), best, o);
+    merge_steps<32>(best, false, EntryStep{});
+}
+
+__device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
+    return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(lane << 2, static_cast<int>(x)));
+}
+
+// Place of value v of a lane's registers: runs of E elements per lane (E = 16 bytes' worth on the
+// vector path, 1 on the element path).
+template <int E>
+__device__ __forceinline__ uint32_t place(int v) {
+    return static_cast<uint32_t>((v / E) * (kWave * E) + (v % E)) + lane_id() * E;
+}
+
+// NV keys of the row per lane; entries past n have key 0.
+template <typename T, int E, int NV>
+__device__ __forceinline__ void load_keys(const T* row, int n, uint32_t (&k)[NV]) {
+    if constexpr (E == 1) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const uint32_t i = place<1>(v);
+            k[v] = i < static_cast<uint32_t>(n) ? key_of(widen(row[i])) : 0u;
+        }
+    } else {
+        static_assert(NV % E == 0, "whole vectors");
+        u32x4 w[NV / E];
+#pragma unroll
+        for (int c = 0; c < NV / E; ++c) {
+            const uint32_t i = place<E>(c * E);
+            w[c] = u32x4{0, 0, 0, 0};
+            if (i < static_cast<uint32_t>(n)) w[c] = *reinterpret_cast<const u32x4*>(row + i);   // n is a multiple of E
+        }
+#pragma unroll
+        for (int c = 0; c < NV / E; ++c) {
+            const bool in = place<E>(c * E) < static_cast<uint32_t>(n);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float f = sizeof(T) == 4 ? __uint_as_float(w[c][e % 4])
+                                               : __uint_as_float(e % 2 ? w[c][e / 2 % 4] & 0xFFFF0000u : w[c][e / 2 % 4] << 16);
+                k[c * E + e] = in ? key_of(f) : 0u;
+            }
+        }
+    }
+}
+
+// The best `kept` entries of the row whose keys the lanes hold, best in lane 0. list: 128 entries of LDS.
+template <int E, int NV>
+__device__ __forceinline__ Entry best_of(const uint32_t (&k)[NV], int kept, u32x2* list) {
+    if constexpr (NV == 1) {
+        Entry e{k[0], ~place<E>(0)};
+        sort64(e);
+        return e;
+    } else {
+        uint32_t m = k[0];
+#pragma unroll
+        for (int v = 1; v < NV; ++v) m = max(m, k[v]);
+        sort64(m);
+        // At least `kept` entries are at or above the kept-th best lane maximum. Entries past the row's
+        // end (key 0) are not taken: a row has at least `kept` entries.
+        const uint32_t bound = max(1u, static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(m), kept - 1)));
+        Entry best{0u, 0u};
+        int n = 0;   // entries in the list, below 64 between sweeps
+        bool have = false;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const bool in = k[v] >= bound;
+            const uint64_t mask = __ballot(in);
+            if (mask == 0) continue;
+            const int at = n + static_cast<int>(__builtin_amdgcn_mbcnt_hi(
+                                   static_cast<uint32_t>(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u)));
+            if (in) list[at] = u32x2{k[v], ~place<E>(v)};
+            n += __popcll(mask);
+            if (n >= 64) {   // 64 of them sorted and merged, the rest moved to the front
+                __builtin_amdgcn_wave_barrier();
+                const u32x2 x = list[lane_id()], r = list[64 + lane_id()];
+                Entry e{x[0], x[1]};
+                sort64(e);
+                if (have) merge64(best, e);
+                else best = e;
+                have = true;
+                n -= 64;
+                __builtin_amdgcn_wave_barrier();
+                list[lane_id()] = r;
+                __builtin_amdgcn_wave_barrier();
+            }
+        }
+        if (n > 0) {
+            __builtin_amdgcn_wave_barrier();
+            const u32x2 x = list[lane_id()];
+            Entry e{static_cast<int>(lane_id()) < n ? x[0] : 0u, static_cast<int>(lane_id()) < n ? x[1] : 0u};
+            sort64(e);
+            if (have) merge64(best, e);
+            else best = e;
+            __builtin_amdgcn_wave_barrier();
+        }
+        return best;
+    }
+}
+
+template <typename T, int E, int NV>
+__device__ __forceinline__ Entry best_of_row(const void* base, int64_t at, int n, int kept, u32x2* list) {
+    uint32_t k[NV];
+    load_keys<T, E, NV>(static_cast<const T*>(base) + at, n, k);
+    return best_of<E, NV>(k, kept, list);
+}
+
+__device__ __forceinline__ float wave_max_first(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x))); }
+
+// Weights of the K sums in lanes 0 .. K-1 (best in lane 0).
+__device__ __forceinline__ float slot_weight(float v, float top, float scale, bool on) {
+    const float e = on && v > -INFINITY ? expf((v - top) * scale) : 0.0f;
+    const float s = group_sum<kWave>(e);
+    return s > 0.0f ? e / s : (s != s ? s : 0.0f);
+}
+
+template <typename T, int E, int NV>
+__global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
+    const sdm_slot_topk_io& io = a.io;
+    __shared__ u32x2 lists[kStWaves][128];
+    u32x2* list = lists[threadIdx.x / kWave];
+    const int lane = static_cast<int>(lane_id());
+    const int64_t waves = static_cast<int64_t>(gridDim.x) * kStWaves;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kStWaves + threadIdx.x / kWave; t < io.N; t += waves) {
+        const Entry ea = best_of_row<T, E, NV>(io.a, t * io.a_row, io.n1, a.ka, list);
+        const Entry eb = best_of_row<T, E, NV>(io.b, t * io.b_row, io.n2, a.kb, list);
+        const float va = float_of(ea.key), vb = float_of(eb.key);
+        Entry best{0u, 0u};
+        for (int p0 = 0; p0 < a.pairs; p0 += kWave) {
+            const int p = p0 + lane;
+            const uint32_t ij = p < a.pairs ? kPairs.at[p] : 0xFFFFu;
+            const int i = static_cast<int>(ij >> 8), j = static_cast<int>(ij & 255u);
+            const float x = __uint_as_float(lane_value(__float_as_uint(va), i)) + __uint_as_float(lane_value(__float_as_uint(vb), j));
+            Entry e{key_of(x), ~ij};
+            if (i >= a.ka || j >= a.kb) e = Entry{0u, 0u};
+            sort64(e);
+            if (p0 == 0) best = e;
+            else merge64(best, e);
+        }
+        const uint32_t ij = ~best.inv;
+        const int i = static_cast<int>((ij >> 8) & 63u), j = static_cast<int>(ij & 63u);
+        const int64_t ia = static_cast<uint32_t>(lane_value(~ea.inv, i)), jb = static_cast<uint32_t>(lane_value(~eb.inv, j));
+        const float v = float_of(best.key);
+        const float w = slot_weight(v, wave_max_first(v), io.scale, lane < io.K);
+        if (lane < io.K) {
+            const int64_t off = io.chunk_rows > 0 ? (t / io.chunk_rows) % io.P * io.stream_offset : 0;
+            const int64_t id = ia * io.n2 + jb + off;
+            if (io.idx_bytes == 8) static_cast<int64_t*>(io.idx)[t * io.K + lane] = id;
+            else static_cast<int32_t*>(io.idx)[t * io.K + lane] = static_cast<int32_t>(id);
+            if (io.val_dtype == SDM_BF16) static_cast<bf16_t*>(io.val)[t * io.K + lane] = narrow<bf16_t>(w);
+            else static_cast<float*>(io.val)[t * io.K + lane] = w;
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------------------ backward
+//
+// With p the weights (recomputed from the K gathered sums in float32) and y the gradient of them,
+// d_m = scale p_m (y_m - sum p y) is the gradient of sum m; a score's gradient is the sum of the d of
+// the slots it is part of, the rest of the row 0. One wave per token: the row's gradient is collected
+// in LDS, each score's entries added by the one lane that holds the first of them, in the order of m,
+// so nothing is atomic and the bits are the same every run; then the whole row is written in wide
+// stores. Bound by writing the rows.
+struct StBack {
+    sdm_slot_topk_io io;
+    const float* dval;
+    void *da, *db;
+    int64_t da_row, db_row;
+    int vec;
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void write_row(T* out, int n, float* acc) {
+    const int lane = static_cast<int>(lane_id());
+    if constexpr (VEC && sizeof(T) == 2) {
+        for (int c = lane * 8; c < n; c += kWave * 8) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(acc + c), y = *reinterpret_cast<const f32x4*>(acc + c + 4);
+            *reinterpret_cast<u32x4*>(out + c) =
+                u32x4{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3])};
+        }
+    } else if constexpr (VEC) {
+        for (int c = lane * 4; c < n; c += kWave * 4) *reinterpret_cast<f32x4*>(out + c) = *reinterpret_cast<const f32x4*>(acc + c);
+    } else {
+        for (int c = lane; c < n; c += kWave) out[c] = narrow<T>(acc[c]);
+    }
+}
+
+// acc (zero on entry and on return) gains the entries (col, d) of lanes 0 .. K-1 and is written out.
+template <typename T, bool VEC>
+__device__ __forceinline__ void scatter_row(T* out, int n, int col, float d, int K, float* acc) {
+    const int lane = static_cast<int>(lane_id());
+    // The first lane with this column adds every lane's entry of it, in lane order.
+    bool first = lane < K;
+    float sum = 0.0f;
+    for (int m = 0; m < K; ++m) {
+        const int cm = __builtin_amdgcn_readlane(col, m);
+        const float dm = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(__float_as_int(d), m)));
+        const bool same = cm == col;
+        sum += same ? dm : 0.0f;
+        first = first && !(same && m < lane);
+    }
+    if (first) acc[col] = sum;
+    __builtin_amdgcn_wave_barrier();
+    write_row<T, VEC>(out, n, acc);
+    __builtin_amdgcn_wave_barrier();
+    if (first) acc[col] = 0.0f;
+    __builtin_amdgcn_wave_barrier();
+}
+
+template <typename T, bool VEC>
+__global__ __launch_bounds__(kStThreads) void slot_topk_back_kernel(StBack b) {
+    const sdm_slot_topk_io& io = b.io;
+    extern __shared__ float accs[];   // [waves, width]
+    const int width = (max(io.n1, io.n2) + 7) & ~7;
+    float* acc = accs + static_cast<size_t>(threadIdx.x / kWave) * width;
+    const int lane = static_cast<int>(lane_id());
+    for (int c = lane; c < width; c += kWave) acc[c] = 0.0f;
+    __builtin_amdgcn_wave_barrier();
+    const int wpb = static_cast<int>(blockDim.x) / kWave;
+    const int64_t waves = static_cast<int64_t>(gridDim.x) * wpb;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * wpb + threadIdx.x / kWave; t < io.N; t += waves) {
+        const bool on = lane < io.K;
+        int i = 0, j = 0;
+        float v = -INFINITY, y = 0.0f;
+        if (on) {
+            int64_t id = io.idx_bytes == 8 ? static_cast<const int64_t*>(io.idx)[t * io.K + lane]
+                                           : static_cast<const int32_t*>(io.idx)[t * io.K + lane];
+            if (io.chunk_rows > 0) id -= (t / io.chunk_rows) % io.P * io.stream_offset;
+            // In bounds whatever the caller passed.
+            const int64_t last = static_cast<int64_t>(io.n1) * io.n2 - 1;
+            id = id < 0 ? 0 : id > last ? last : id;
+            i = static_cast<int>(id / io.n2);
+            j = static_cast<int>(id - static_cast<int64_t>(i) * io.n2);
+            const float s = widen(static_cast<const T*>(io.a)[t * io.a_row + i]), u = widen(static_cast<const T*>(io.b)[t * io.b_row + j]);
+            const float x = s + u;
+            v = x != x ? -INFINITY : x;
+            y = b.dval[t * io.K + lane];
+        }
+        float top = v;
+        top = fmaxf(top, lane_xor_f<1>(top));
+        top = fmaxf(top, lane_xor_f<2>(top));
+        top = fmaxf(top, lane_xor_f<4>(top));
+        top = fmaxf(top, lane_xor_f<8>(top));
+        top = fmaxf(top, lane_xor_f<16>(top));
+        top = fmaxf(top, lane_xor_f<32>(top));
+        const float p = slot_weight(v, top, io.scale, on);
+        // A slot of weight 0 takes part in neither sum: its gradient is 0 whatever came in.
+        const float py = p > 0.0f ? p * y : 0.0f;
+        const float dot = group_sum<kWave>(py);
+        const float d = p > 0.0f ? p * (y - dot) * io.scale : p;
+        if (b.da != nullptr) scatter_row<T, VEC>(static_cast<T*>(b.da) + t * b.da_row, io.n1, i, d, io.K, acc);
+        if (b.db != nullptr) scatter_row<T, VEC>(static_cast<T*>(b.db) + t * b.db_row, io.n2, j, d, io.K, acc);
+    }
+}
+
+bool rows16(const void* p, int64_t row, int n, int unit) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && row % unit == 0 && n % unit == 0;
+}
+
+// Rows per launch-resident wave: enough blocks to fill the device several times, then grid-stride.
+constexpr int64_t kStBlocks = 1 << 16;
+
+template <typename T, int E>
+void st_go(const StArgs& a, hipStream_t st) {
+    const int64_t need = (a.io.N + kStWaves - 1) / kStWaves;
+    const unsigned grid = static_cast<unsigned>(need < kStBlocks ? need : kStBlocks);
+    const int nv = ((a.io.n1 > a.io.n2 ? a.io.n1 : a.io.n2) + kWave - 1) / kWave;   // keys per lane of the longer row
+    if constexpr (E == 1) {
+        if (nv <= 1) { slot_topk_kernel<T, 1, 1><<<grid, kStThreads, 0, st>>>(a); return; }
+        if (nv <= 2) { slot_topk_kernel<T, 1, 2><<<grid, kStThreads, 0, st>>>(a); return; }
+    }
+    if constexpr (E <= 4) {
+        if (nv <= 4) { slot_topk_kernel<T, E, 4><<<grid, kStThreads, 0, st>>>(a); return; }
+    }
+    if (nv <= 8) slot_topk_kernel<T, E, 8><<<grid, kStThreads, 0, st>>>(a);
+    else if (nv <= 16) slot_topk_kernel<T, E, 16><<<grid, kStThreads, 0, st>>>(a);
+    else if (nv <= 32) slot_topk_kernel<T, E, 32><<<grid, kStThreads, 0, st>>>(a);
+    else slot_topk_kernel<T, E, 64><<<grid, kStThreads, 0, st>>>(a);
+}
+
+}  // namespace
+
+hipError_t slot_topk_launch(const sdm_slot_topk_io* io, hipStream_t st) {
+    StArgs a;
+    a.io = *io;
+    a.ka = io->K < io->n1 ? io->K : io->n1;
+    a.kb = io->K < io->n2 ? io->K : io->n2;
+    a.pairs = kPairsHost.count[io->K];
+    const bool bf = io->dtype == SDM_BF16;
+    const int unit = bf ? 8 : 4;
+    // 16-byte loads pay from rows of 64 lanes' worth of them; shorter rows leave lanes idle either way.
+    const int longest = io->n1 > io->n2 ? io->n1 : io->n2;
+    a.vec = longest > 2 * kWave && rows16(io->a, io->a_row, io->n1, unit) && rows16(io->b, io->b_row, io->n2, unit);
+    if (bf) a.vec ? st_go<bf16_t, 8>(a, st) : st_go<bf16_t, 1>(a, st);
+    else a.vec ? st_go<float, 4>(a, st) : st_go<float, 1>(a, st);
+    return hipGetLastError();
+}
+
+int slot_lds_kernels(const void** fns, int cap) {
+    const void* all[] = {reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, true>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, false>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, true>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, false>)};
+    int n = 0;
+    for (const void* f : all) {
+        if (n < cap) fns[n++] = f;
+    }
+    return n;
+}
+
+hipError_t slot_topk_back_launch(const sdm_slot_topk_io* io, const sdm_slot_topk_grad* g, hipStream_t st) {
+    StBack b;
+    b.io = *io;
+    b.dval = g->dval;
+    b.da = g->da;
+    b.db = g->db;
+    b.da_row = g->da_row;
+    b.db_row = g->db_row;
+    const bool bf = io->dtype == SDM_BF16;
+    const int unit = bf ? 8 : 4;
+    b.vec = (g->da == nullptr || rows16(g->da, g->da_row, io->n1, unit)) && (g->db == nullptr || rows16(g->db, g->db_row, io->n2, unit));
+    const int width = ((io->n1 > io->n2 ? io->n1 : io->n2) + 7) & ~7;
+    const size_t lds = static_cast<size_t>(kStWaves) * width * sizeof(float);
+    const int64_t need = (io->N + kStWaves - 1) / kStWaves;
+    const int64_t most = 4096;   // grid-stride past 16 blocks per compute unit: the LDS rows are zeroed once per wave
+    const unsigned grid = static_cast<unsigned>(need < most ? need : most);
+    if (bf) {
+        if (b.vec) slot_topk_back_kernel<bf16_t, true><<<grid, kStThreads, lds, st>>>(b);
+        else slot_topk_back_kernel<bf16_t, false><<<grid, kStThreads, lds, st>>>(b);
+    } else {
+        if (b.vec) slot_topk_back_kernel<float, true><<<grid, kStThreads, lds, st>>>(b);
+        else slot_topk_back_kernel<float, false><<<grid, kStThreads, lds, st>>>(b);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace sdm
