@@ -47,7 +47,6 @@ namespace sdm {
 namespace {
 
 constexpr int kL = 64;           // tokens of a chunk
-constexpr int kGlrThreads = 256;
 constexpr float kGateMin = -10000.0f;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -109,7 +108,7 @@ __device__ __forceinline__ int twist(int row) {
     constexpr int pieces = W * static_cast<int>(sizeof(T)) / 16;
     if constexpr (pieces == 8) return 4 * ((row >> 1) & 1) + ((row >> 2) & 3);
     else if constexpr (sizeof(T) == 2) return 4 * (row & 3) + ((row >> 2) & 3);
-    else return row & 15;
+    else return row & (pieces == 32 ? 7 : 15);
 }
 template <typename T, int W>
 __device__ __forceinline__ char* piece(T* tile, int row, int c) {
@@ -177,35 +176,37 @@ struct Rows {
     const void* p;
     int64_t b, t, h;
     int width, per;
-    int wide;      // 16-byte loads: aligned rows of whole 16-byte pieces
+    int wide;      // 16-byte loads: aligned rows of whole 16-byte pieces that do not overlap, 64 of them within 2^30 bytes
 };
 
 struct GlrPass {
-    Rows x, y, z, w;          // w: the rows the results are dotted with (dot != NULL)
+    Rows x, y, z, w;          // w: the rows the results are dotted with (DOT)
     const float* g;
     int64_t g_b, g_t, g_h;
     const int32_t* lens;
     int B, T, H;
     int nseg, seg;            // segments, and tokens of each (a multiple of 64)
     float m_p, m_o, m_s;
-    // The state before a segment (in the pass's direction), [B H, nseg] states from s_in (NULL: zero), element (key, value)
-    // at key * s_k + value * s_v; the state after the last segment to s_out, [B H] states (NULL: not kept).
-    const float* s_in;
-    float* s_out;
-    int64_t s_k, s_v;
-    // out rows: [B, T, H] with strides, narrowed to the input type, or float32 (fold)
+    // States, element (key, value) at key * s_k + value * s_v. start: [B H] before the first segment in the pass's direction
+    // (NULL: zero); segs: [B H, nseg] (NULL when nseg is 1), the segments' own states with their decays [B H, nseg], or,
+    // chained, the states before the segments. last: [B H] after the last segment (NULL: not kept).
+    const float* start;
+    float* segs;
+    float* decays;
+    int chained;
+    float* last;
+    int s_k, s_v;
+    // out rows: [B, T, H] with strides, narrowed to the input type, or float32 (shared heads, added up later)
     void* out;
     int64_t o_b, o_t, o_h;
     int out_wide;             // 4-element stores
     int out_f32;
-    float* dot;               // [B H, T] row dots of w and the result
-    // <state after the segment, the gradient of it>: [B H, nseg], from r_end (indexed like s_in: the gradient at the segment's end)
-    const float* r_end;
-    int64_t r_k, r_v;
+    float* dot;               // [B H, T] row dots of w and the result (DOT)
+    // DOT: <S, R> at the segment's end to cross [B H, nseg]; R's start, segs and decays like S's, backwards in time.
     float* cross;
-    // state-only pass
-    float* seg_state;         // [B H, nseg] states [s_k, s_v]
-    float* seg_decay;         // [B H, nseg]
+    const float* r_start;
+    const float* r_segs;
+    const float* r_decays;
 };
 
 __device__ __forceinline__ int row_len(const GlrPass& p, int b) {
@@ -213,48 +214,57 @@ __device__ __forceinline__ int row_len(const GlrPass& p, int b) {
     return n < 0 ? 0 : n > p.T ? p.T : n;
 }
 
-// A chunk's tile in flight: 16-byte pieces per thread, zero past the row's length and the head's width.
-template <typename T, int W>
+// A chunk's tile of one operand, global memory to LDS. Rows that take wide loads go there directly, 16
+// bytes per lane, no registers between (the lanes' pieces lie in lane order in LDS, so the lane reads the
+// piece that belongs there by the twist); others element by element. Zero past the row's length and the
+// head's width: the loads' buffer descriptor ends with the chunk's last token, and what lies outside its
+// range reads as zero. The range check covers the register offset, which holds all of it.
+// 16 bytes per lane from the buffer's byte offset `off` to LDS at `to` (the wave's) + 16 lane.
+__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t rsrc, char* to, int off) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no such instruction
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+#endif
+}
+
+template <typename T, int W, int THREADS>
 struct Stage {
     static constexpr int kPieces = W * static_cast<int>(sizeof(T)) / 16;       // per row
-    static constexpr int kEach = kL * kPieces / kGlrThreads;                    // per thread
+    static constexpr int kEach = kL * kPieces / THREADS;                        // per thread
     static constexpr int kElems = 16 / static_cast<int>(sizeof(T));
-    u32x4 r[kEach];
+    static constexpr int kStep = THREADS / kPieces;                             // rows between a thread's pieces
+    static_assert(kStep % 16 == 0 || (kStep % 8 == 0 && kPieces == 32), "a thread's rows have one twist");
+    uint32_t off;      // of the thread's first piece from the chunk's first row, bytes; out of any range past the head's width
 
-    __device__ __forceinline__ void load(const Rows& s, const T* base, int t0, int len) {
-#pragma unroll
-        for (int n = 0; n < kEach; ++n) {
-            const int at = n * kGlrThreads + static_cast<int>(threadIdx.x), row = at / kPieces, c = at % kPieces;
-            r[n] = u32x4{0, 0, 0, 0};
-            const int left = s.width - c * kElems;
-            if (t0 + row < len && left > 0) {
-                const T* p = base + static_cast<int64_t>(t0 + row) * s.t + c * kElems;
-                if (s.wide) {
-                    r[n] = *reinterpret_cast<const u32x4*>(p);
-                } else {
-                    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int e = 0; e < kElems; ++e) {
-                        if (e < left) {
-                            if constexpr (sizeof(T) == 2) w[e / 2] |= static_cast<uint32_t>(p[e].bits) << (16 * (e & 1));
-                            else w[e] = __float_as_uint(p[e]);
-                        }
-                    }
-                    r[n] = u32x4{w[0], w[1], w[2], w[3]};
-                }
-            }
-        }
+    __device__ __forceinline__ void init(const Rows& s) {
+        const int row = static_cast<int>(threadIdx.x) / kPieces;
+        const int c = (static_cast<int>(threadIdx.x) % kPieces) ^ twist<T, W>(row);
+        off = c * kElems < s.width ? static_cast<uint32_t>(row * static_cast<int>(s.t) * static_cast<int>(sizeof(T)) + c * 16) : 0xC0000000u;
     }
-    __device__ __forceinline__ void store(T* tile) const {
+    // base: the chunk's first row; left: its tokens. Complete after a wait for vector memory and a barrier.
+    __device__ __forceinline__ void fill(const Rows& s, const T* base, int left, T* tile, int wave) const {
+        const int tok = left < kL ? left : kL;
+        if (s.wide) {
+            const int bytes = ((tok - 1) * static_cast<int>(s.t) + s.width) * static_cast<int>(sizeof(T));
+            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
+            const uint32_t step = static_cast<uint32_t>(kStep * static_cast<int>(s.t) * static_cast<int>(sizeof(T)));
+            char* to = reinterpret_cast<char*>(tile) + wave * (kWave * 16);
 #pragma unroll
-        for (int n = 0; n < kEach; ++n) {
-            const int at = n * kGlrThreads + static_cast<int>(threadIdx.x), row = at / kPieces, c = at % kPieces;
-            *reinterpret_cast<u32x4*>(piece<T, W>(tile, row, c)) = r[n];
+            for (int n = 0; n < kEach; ++n) to_lds16(rsrc, to + n * THREADS * 16, static_cast<int>(off + n * step));
+            return;
+        }
+        for (int at = static_cast<int>(threadIdx.x); at < kL * W; at += THREADS) {
+            const int t = at / W, col = at % W;
+            T v = narrow<T>(0.0f);
+            if (t < tok && col < s.width) v = base[static_cast<int64_t>(t) * s.t + col];
+            *reinterpret_cast<T*>(piece<T, W>(tile, t, col / kElems) + (col % kElems) * static_cast<int>(sizeof(T))) = v;
         }
     }
 };
 
-// A chunk's gate factors (one wave computes them, a token per lane).
+// Barrier after which every wave's tile loads are in LDS.
+__device__ __forceinline__ void tile_barrier() { __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+// A chunk's gate factors (one wave computes them, a token per lane). Sums are in units of log 2.
 struct Gates {
     float lhi[kL], llo[kL];   // the sum of gates since the start of the token's tile of 16, in two parts
     float up[kL];             // exp(G_i - G at the start of its tile)
@@ -279,10 +289,21 @@ __device__ __forceinline__ double lane_d(double x, int lane) {
     return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+// 2^x of a float64 exponent: the rounded part through the hardware exp2 (its results below 2^-126 are 0), the
+// remainder to first order.
+__device__ __forceinline__ float exp2_of(double x) {
+    const float hi = static_cast<float>(x);
+    const float lo = static_cast<float>(x - hi);
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return fmaf(e, lo * 0.69314718056f, e);
+}
+
+constexpr double kLog2E = 1.4426950408889634074;
+
 template <bool REV>
 __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gates& o) {
     const int l = static_cast<int>(lane_id());
-    double G = g < kGateMin ? kGateMin : g;   // NaN stays
+    double G = (g < kGateMin ? kGateMin : g) * kLog2E;   // NaN stays
 #pragma unroll
     for (int n = 1; n < kL; n *= 2) {
         const double below = shfl_up_d(G, n);
@@ -294,40 +315,57 @@ __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gate
     const float hi = static_cast<float>(local);
     o.lhi[l] = hi;
     o.llo[l] = static_cast<float>(local - hi);
-    o.up[l] = expf(hi);
-    o.down[l] = expf(static_cast<float>(end - G));
-    const float fwd = expf(static_cast<float>(G)), bwd = expf(static_cast<float>(last - G));
+    o.up[l] = exp2_of(local);
+    o.down[l] = exp2_of(end - G);
+    const float fwd = exp2_of(G), bwd = exp2_of(last - G);
     o.f[l] = (REV ? bwd : fwd) * m_o;
     o.u[l] = (REV ? fwd : bwd) * m_s;
     {
         const int it = (l >> 2) & 3, jt = l & 3, hi_t = it > jt ? it : jt, lo_t = it > jt ? jt : it;
-        const double a = lane_d(G, (16 * hi_t + 63) & 63), b = lane_d(G, 16 * lo_t + 15);   // starts of tile hi_t, end of lo_t
-        if (l < 16) o.tau[l] = it == jt ? 1.0f : expf(static_cast<float>(a - b));
+        const double a = lane_d(G, (16 * hi_t + 63) & 63), b = lane_d(G, 16 * lo_t + 15);   // start of tile hi_t, end of lo_t
+        if (l < 16) o.tau[l] = it == jt ? 1.0f : exp2_of(a - b);
     }
     if (l == 0) {
-        o.all = expf(static_cast<float>(last));
+        o.all = exp2_of(last);
         o.sum = last;
     }
 }
 
+// The score operands of a chunk, computed once and shared by the waves: pair n is (it, jb), the tiles of tokens
+// 16 it across and 32 jb down; its two halves are the score tiles jt = 2 jb and 2 jb + 1. Of the 16 tiles the
+// 6 pairs below hold all that the direction needs (and two that are zero).
+template <bool REV>
+struct Pairs {
+    static constexpr int kIt[6] = {REV ? 0 : 0, REV ? 0 : 1, REV ? 1 : 2, REV ? 1 : 2, REV ? 2 : 3, REV ? 3 : 3};
+    static constexpr int kJb[6] = {REV ? 0 : 0, REV ? 1 : 0, REV ? 0 : 0, REV ? 1 : 1, REV ? 1 : 0, REV ? 1 : 1};
+};
+
 // KD, VD: padded widths of x / y and of z (64 or 128). NS: parts of scores and of the state where it meets x.
-template <typename T, int KD, int VD, bool REV, bool OUT, int NS>
-__global__ __launch_bounds__(kGlrThreads) void glr_kernel(GlrPass p) {
-    constexpr int KB = KD / 32, KT = KD / 16, NT = VD / 64;
+// OUT: results (else the segments' own states alone). DOT: row dots of the results, and <S, R>. FOLD: float32 results
+// of bfloat16 inputs.
+template <typename T, int KD, int VD, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
+__global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(GlrPass p) {
+    constexpr int KB = KD / 32, KT = KD / 16, kThreads = 4 * VD, kWaves = VD / 16;
     constexpr int P2 = kParts<T, NS>, P3 = kParts<T, 3>;
-    constexpr bool kAhead = sizeof(T) == 2;   // float32 tiles are twice as wide: no registers for a chunk in flight
+    constexpr bool F32 = sizeof(T) == 4 || FOLD;
+    // Without results two chunks' tiles fit beside each other (in bfloat16) and the next chunk's loads run under a chunk's
+    // products; with them x's tile is free half way through a chunk, y's and z's at its end.
+    constexpr int kBufs = !OUT && sizeof(T) == 2 ? 2 : 1;
+    constexpr int kScoreWords = 8 * static_cast<int>(sizeof(T)) / 4;   // per lane and part
     extern __shared__ __align__(16) char lds[];
     T* xt = reinterpret_cast<T*>(lds);
     T* yt = xt + (OUT ? kL * KD : 0);
-    T* zt = yt + kL * KD;
-    Gates& gates = *reinterpret_cast<Gates*>(zt + kL * VD);
-    float* dots = reinterpret_cast<float*>(&gates + 1);   // [4][64]
+    T* zt = yt + kBufs * kL * KD;
+    uint32_t* scores = reinterpret_cast<uint32_t*>(zt + kBufs * kL * VD);   // [6][P2][64 lanes][kScoreWords]
+    Gates* gate_at = reinterpret_cast<Gates*>(scores + (OUT ? 6 * P2 * kWave * kScoreWords : 0));   // two chunks
+    float* dots = reinterpret_cast<float*>(gate_at + 2);   // [waves][64]
 
+    const int nblk = OUT ? p.nseg : p.nseg - 1;   // the last segment's own state (in the pass's direction) is not needed
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    const int si = blk % p.nseg, bh = blk / p.nseg, b = bh / p.H, h = bh - b * p.H;
-    const int lane = static_cast<int>(lane_id()), wave = static_cast<int>(threadIdx.x) / kWave;
+    const int bh = blk / nblk, si = blk - bh * nblk + (!OUT && REV ? 1 : 0), b = bh / p.H, h = bh - b * p.H;
+    const int lane = static_cast<int>(lane_id()), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
-    const int n0 = wave * 16 * NT;   // the wave's first column
+    const int n0 = wave * 16;   // the wave's first column
     const int len = row_len(p, b);
     const int t_lo = si * p.seg, t_hi = min(p.T, t_lo + p.seg);   // the segment's tokens
     const int live = min(len, t_hi);
@@ -340,266 +378,359 @@ __global__ __launch_bounds__(kGlrThreads) void glr_kernel(GlrPass p) {
     const int kd = p.y.width, vd = p.z.width;
     const int64_t one = static_cast<int64_t>(kd) * vd;
 
-    // The wave's state: tile d, rows 32 (d / 2) + 8 quarter + 4 (d % 2) + r, column n0 + 16 nt + lane % 16.
-    f32x4 S[KT][NT];
+    // The wave's state: tile d, rows 32 (d / 2) + 8 quarter + 4 (d % 2) + r, column n0 + lane % 16.
+    f32x4 S[KT];
+    // Its elements are read and written through buffer descriptors of one state's range; the lanes' offsets past the
+    // state's widths are out of it (read as zero, not written), so no branches cut the accumulators' registers apart.
+    const uint32_t at0 = 4u * static_cast<uint32_t>((n0 + i16) * p.s_v + 8 * qd * p.s_k);
+    auto state_at = [&](int d, int r) {
+        const int k = 32 * (d >> 1) + 4 * (d & 1) + r;
+        return static_cast<int>(n0 + i16 < vd && k + 8 * qd < kd ? at0 + 4u * static_cast<uint32_t>(k * p.s_k) : 0xC0000000u);
+    };
+    auto state_of = [&](const float* s) {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(s), 0, static_cast<int>(one) * 4, 0x00027000);
+    };
+    auto state_read = [&](__amdgpu_buffer_rsrc_t s, int d, int r) {
+        return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(s, state_at(d, r), 0, 0));
+    };
 #pragma unroll
-    for (int d = 0; d < KT; ++d) {
+    for (int d = 0; d < KT; ++d) S[d] = f32x4{0, 0, 0, 0};
+    if constexpr (OUT) {
+        const bool whole = p.segs != nullptr && p.chained;
+        const float* s0 = whole ? p.segs + (static_cast<int64_t>(bh) * p.nseg + si) * one : p.start != nullptr ? p.start + bh * one : nullptr;
+        if (s0 != nullptr) {
+            const auto s = state_of(s0);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            S[d][nt] = f32x4{0, 0, 0, 0};
-            if (OUT && p.s_in != nullptr) {
-                const float* s = p.s_in + (static_cast<int64_t>(bh) * p.nseg + si) * one;
-                const int n = n0 + 16 * nt + i16, k0 = 32 * (d >> 1) + 8 * qd + 4 * (d & 1);
+            for (int d = 0; d < KT; ++d) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if (n < vd && k0 + r < kd) S[d][nt][r] = s[(k0 + r) * p.s_k + n * p.s_v];
-                }
+                for (int r = 0; r < 4; ++r) S[d][r] = state_read(s, d, r);
+            }
+        }
+        // The segments before this one, in order.
+#pragma unroll 1
+        for (int n = REV ? p.nseg - 1 : 0; !whole && n != si; n += REV ? -1 : 1) {
+            const auto s = state_of(p.segs + (static_cast<int64_t>(bh) * p.nseg + n) * one);
+            const float dec = p.decays[static_cast<int64_t>(bh) * p.nseg + n];
+#pragma unroll
+            for (int d = 0; d < KT; ++d) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[d][r] = fmaf(dec, S[d][r], state_read(s, d, r));
             }
         }
     }
     double decay = 0.0;   // state-only: the sum of the segment's gates
 
-    Stage<T, KD> sx, sy;
-    Stage<T, VD> sz;
-    float gate = 0.0f;
-    auto fetch = [&](int c) {
+    Stage<T, KD, kThreads> sx, sy;
+    Stage<T, VD, kThreads> sz;
+    if (OUT) sx.init(p.x);
+    sy.init(p.y);
+    sz.init(p.z);
+    auto fill_x = [&](int c) {
         const int t0 = t_lo + c * kL;
-        if (OUT) sx.load(p.x, xb, t0, live);
-        sy.load(p.y, yb, t0, live);
-        sz.load(p.z, zb, t0, live);
-        if (wave == 0) gate = t0 + lane < live ? gb[static_cast<int64_t>(t0 + lane) * p.g_t] : 0.0f;
+        if (OUT) sx.fill(p.x, xb + t0 * p.x.t, live - t0, xt, wave);
     };
-    if (kAhead && chunks > 0) fetch(REV ? chunks - 1 : 0);
+    auto fill_yz = [&](int c, int buf) {
+        const int t0 = t_lo + c * kL;
+        sy.fill(p.y, yb + t0 * p.y.t, live - t0, yt + buf * kL * KD, wave);
+        sz.fill(p.z, zb + t0 * p.z.t, live - t0, zt + buf * kL * VD, wave);
+    };
+    // Chunk c's gates, one token per lane (c >= 0 has tokens; a lane past them loads the last one's, and drops it).
+    auto gate_load = [&](int c) { return gb[static_cast<int64_t>(min(t_lo + max(c, 0) * kL + lane, live - 1)) * p.g_t]; };
+    auto gate_of = [&](int c, float g) { return t_lo + c * kL + lane < live ? g : 0.0f; };
+    float next_gate = 0.0f;
+    if (chunks > 0) {
+        const int c = REV ? chunks - 1 : 0;
+        const float g = gate_load(c);
+        next_gate = gate_load(REV ? c - 1 : min(c + 1, chunks - 1));
+        fill_x(c);
+        fill_yz(c, 0);
+        if (wave == kWaves - 1) gate_factors<REV>(gate_of(c, g), p.m_o, p.m_s, gate_at[0]);
+    }
 
     for (int cc = 0; cc < chunks; ++cc) {
-        const int c = REV ? chunks - 1 - cc : cc, t0 = t_lo + c * kL;
-        if (!kAhead) fetch(c);
-        if (OUT) sx.store(xt);
-        sy.store(yt);
-        sz.store(zt);
-        if (wave == 0) gate_factors<REV>(gate, p.m_o, p.m_s, gates);
-        __syncthreads();
-        if (kAhead && cc + 1 < chunks) fetch(REV ? c - 1 : c + 1);
+        const int c = REV ? chunks - 1 - cc : cc, t0 = t_lo + c * kL, left = live - t0;
+        const Gates& gates = gate_at[cc & 1];
+        // The lane's place, unknown to the compiler to be the same in every chunk: the many LDS addresses made from it are cheap
+        // to make again, and kept over the loop they would not fit the 128 registers that two blocks per compute unit leave.
+        int here = lane;
+        __asm__ volatile("" : "+v"(here));
+        const int i16 = here & 15, qd = here >> 4;
+        const int n = n0 + 4 * qd;   // the lane's result columns n .. n + 3, of token 16 it + lane % 16
+        const int buf = kBufs == 2 ? cc & 1 : 0;
+        T* const yc = yt + buf * kL * KD;
+        T* const zc = zt + buf * kL * VD;
+        const bool more = cc + 1 < chunks;
+        const int next = REV ? c - 1 : c + 1;
+        tile_barrier();   // the chunk's tiles and gate factors are complete
+        if (kBufs == 2 && more) fill_yz(next, buf ^ 1);
+        // The next chunk's factors, by the last wave (it has one score tile, others two); its gates came a chunk ago.
+        if (more && wave == kWaves - 1) gate_factors<REV>(gate_of(next, next_gate), p.m_o, p.m_s, gate_at[(cc + 1) & 1]);
+        next_gate = gate_load(REV ? c - 2 : min(c + 2, chunks - 1));
 
         if constexpr (OUT) {
-            f32x4 O[4][NT];   // tile it: columns n0 + 16 nt + 4 quarter + r down, token 16 it + lane % 16
+            // The twelve score tiles, dealt to the waves.
+            for (int e = wave; e < 12; e += kWaves) {
+                const int pr = e >> 1, half = e & 1;
+                int it = 0, jb = 0;
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) O[it][nt] = f32x4{0, 0, 0, 0};
-            }
-            // S^T x
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                Parts<T, P2> sp[NT];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float s[8];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) { s[r] = S[2 * kb][nt][r]; s[4 + r] = S[2 * kb + 1][nt][r]; }
-                    cut(s, sp[nt]);
-                }
-#pragma unroll
-                for (int it = 0; it < 4; ++it) {
-                    const Frag<T> xf = row_frag<KD>(xt, 16 * it + i16, kb, qd);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int s = P2 - 1; s >= 0; --s) mma(sp[nt].p[s], xf, O[it][nt]);
+                for (int k = 0; k < 6; ++k) {
+                    if (k == pr) {
+                        it = Pairs<REV>::kIt[k];
+                        jb = Pairs<REV>::kJb[k];
                     }
                 }
-            }
-            // The chunk's own tokens.
-            Frag<T> zf[2][NT];
+                const int jt = 2 * jb + half;
+                float s[4];
+                if (REV ? jt < it : jt > it) {
 #pragma unroll
-            for (int jb = 0; jb < 2; ++jb) {
+                    for (int r = 0; r < 4; ++r) s[r] = 0.0f;
+                } else {
+                    f32x4 a = {0, 0, 0, 0};   // token 16 jt + 4 quarter + r down, token 16 it + lane % 16 across
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) zf[jb][nt] = col_frag<VD, 4>(zt, jb, n0 + 16 * nt, i16, qd);
-            }
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const float f = gates.f[16 * it + i16];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) O[it][nt] *= f;
-                Frag<T> xf[KB];
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) xf[kb] = row_frag<KD>(xt, 16 * it + i16, kb, qd);
-                const float own = (REV ? gates.down : gates.up)[16 * it + i16] * p.m_p;
-                const float lhi = gates.lhi[16 * it + i16], llo = gates.llo[16 * it + i16];
-#pragma unroll
-                for (int jb = 0; jb < 2; ++jb) {
-                    if (REV ? 2 * jb + 1 < it : 2 * jb > it) continue;
-                    float s[8];
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int jt = 2 * jb + half;
-                        if (REV ? jt < it : jt > it) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) s[4 * half + r] = 0.0f;
-                            continue;
-                        }
-                        f32x4 a = {0, 0, 0, 0};   // token 16 jt + 4 quarter + r down, token 16 it + lane % 16 across
-#pragma unroll
-                        for (int kb = 0; kb < KB; ++kb) mma(row_frag<KD>(yt, 16 * jt + i16, kb, qd), xf[kb], a);
-                        if (jt == it) {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                const int j = 4 * qd + r;
-                                const float dh = lhi - gates.lhi[16 * jt + j], dl = llo - gates.llo[16 * jt + j];
-                                const float e = expf(REV ? -(dh + dl) : dh + dl);
-                                s[4 * half + r] = (REV ? j >= i16 : j <= i16) ? a[r] * (e * p.m_p) : 0.0f;
-                            }
-                        } else {
-                            const float ot = own * gates.tau[4 * it + jt];
-                            const f32x4 d = *reinterpret_cast<const f32x4*>(&(REV ? gates.up : gates.down)[16 * jt + 4 * qd]);
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) s[4 * half + r] = a[r] * (ot * d[r]);
-                        }
-                    }
-                    Parts<T, P2> sp;
-                    cut(s, sp);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int k = P2 - 1; k >= 0; --k) mma(zf[jb][nt], sp.p[k], O[it][nt]);
-                    }
-                }
-                // Out.
-                const int t = t0 + 16 * it + i16;
-                float dot = 0.0f;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const int n = n0 + 16 * nt + 4 * qd;
-                    if (t >= live || n >= vd) continue;
-                    const f32x4 v = O[it][nt];
-                    if (p.dot != nullptr) {
-                        const T* w = static_cast<const T*>(p.w.p) + b * p.w.b + static_cast<int64_t>(t) * p.w.t + (h / p.w.per) * p.w.h + n;
+                    for (int kb = 0; kb < KB; ++kb)
+                        mma(row_frag<KD>(yc, 16 * jt + i16, kb, qd), row_frag<KD>(xt, 16 * it + i16, kb, qd), a);
+                    if (jt == it) {
+                        const float lhi = gates.lhi[16 * it + i16], llo = gates.llo[16 * it + i16];
+                        const f32x4 jh = *reinterpret_cast<const f32x4*>(&gates.lhi[16 * jt + 4 * qd]);
+                        const f32x4 jl = *reinterpret_cast<const f32x4*>(&gates.llo[16 * jt + 4 * qd]);
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            if (n + r < vd) dot = fmaf(widen(w[r]), v[r], dot);
-                        }
-                    }
-                    const int64_t at = b * p.o_b + t * p.o_t + h * p.o_h + n;
-                    if (p.out_f32 || sizeof(T) == 4) {
-                        float* o = static_cast<float*>(p.out) + at;
-                        if (p.out_wide) {
-                            *reinterpret_cast<f32x4*>(o) = v;
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                if (n + r < vd) o[r] = v[r];
-                            }
+                            const int j = 4 * qd + r;
+                            const float x = (lhi - jh[r]) + (llo - jl[r]);
+                            const float w = __builtin_amdgcn_exp2f(REV ? -x : x);
+                            s[r] = (REV ? j >= i16 : j <= i16) ? a[r] * (w * p.m_p) : 0.0f;
                         }
                     } else {
-                        bf16_t* o = static_cast<bf16_t*>(p.out) + at;
-                        if (p.out_wide) {
-                            *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                        const float ot = (REV ? gates.down : gates.up)[16 * it + i16] * (p.m_p * gates.tau[4 * it + jt]);
+                        const f32x4 d = *reinterpret_cast<const f32x4*>(&(REV ? gates.up : gates.down)[16 * jt + 4 * qd]);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[r] = a[r] * (ot * d[r]);
+                    }
+                }
+                if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                    for (int k = 0; k < P2; ++k) {
+                        *reinterpret_cast<u32x2*>(scores + ((pr * P2 + k) * kWave + here) * kScoreWords + 2 * half) =
+                            u32x2{__builtin_amdgcn_perm(__float_as_uint(s[1]), __float_as_uint(s[0]), 0x07060302u),
+                                  __builtin_amdgcn_perm(__float_as_uint(s[3]), __float_as_uint(s[2]), 0x07060302u)};
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) s[r] -= __uint_as_float(__float_as_uint(s[r]) & 0xFFFF0000u);
+                    }
+                } else {
+                    *reinterpret_cast<f32x4*>(scores + (pr * kWave + here) * kScoreWords + 4 * half) = f32x4{s[0], s[1], s[2], s[3]};
+                }
+            }
+            // S^T x
+            f32x4 O[4];   // tile it: columns n0 + 4 quarter + r down, token 16 it + lane % 16
+#pragma unroll
+            for (int it = 0; it < 4; ++it) O[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                Parts<T, P2> sp;
+                Frag<T> xf[4];
+#pragma unroll
+                for (int it = 0; it < 4; ++it) xf[it] = row_frag<KD>(xt, 16 * it + i16, kb, qd);
+                float s[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) { s[r] = S[2 * kb][r]; s[4 + r] = S[2 * kb + 1][r]; }
+                cut(s, sp);
+#pragma unroll
+                for (int k = P2 - 1; k >= 0; --k) {
+#pragma unroll
+                    for (int it = 0; it < 4; ++it) mma(sp.p[k], xf[it], O[it]);
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) O[it] *= gates.f[16 * it + i16];
+            lds_barrier();   // the scores are complete, and x's tile is free
+            if (more) fill_x(next);
+            // The chunk's own tokens.
+#pragma unroll
+            for (int jb = 0; jb < 2; ++jb) {
+                const Frag<T> zf = col_frag<VD, 4>(zc, jb, n0, i16, qd);
+#pragma unroll
+                for (int s = P2 - 1; s >= 0; --s) {
+#pragma unroll
+                    for (int pr = 0; pr < 6; ++pr) {
+                        if (Pairs<REV>::kJb[pr] != jb) continue;
+                        Frag<T> pf;
+                        __builtin_memcpy(&pf, scores + ((pr * P2 + s) * kWave + here) * kScoreWords, sizeof(pf));
+                        mma(zf, pf, O[Pairs<REV>::kIt[pr]]);
+                    }
+                }
+            }
+            // Results.
+            if constexpr (DOT) {
+                const T* w = static_cast<const T*>(p.w.p) + b * p.w.b + (h / p.w.per) * p.w.h + static_cast<int64_t>(t0) * p.w.t + n;
+#pragma unroll
+                for (int it = 0; it < 4; ++it) {
+                    const int i = 16 * it + i16;
+                    float dot = 0.0f, wx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (i < left && n < vd) {
+                        if (p.w.wide) {
+                            if constexpr (sizeof(T) == 2) {
+                                const u32x2 v = *reinterpret_cast<const u32x2*>(w + i * p.w.t);
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    wx[2 * r] = __uint_as_float(v[r] << 16);
+                                    wx[2 * r + 1] = __uint_as_float(v[r] & 0xFFFF0000u);
+                                }
+                            } else {
+                                const f32x4 v = *reinterpret_cast<const f32x4*>(w + i * p.w.t);
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) wx[r] = v[r];
+                            }
                         } else {
 #pragma unroll
                             for (int r = 0; r < 4; ++r) {
-                                if (n + r < vd) o[r] = narrow<bf16_t>(v[r]);
+                                if (n + r < vd) wx[r] = widen(w[i * p.w.t + r]);
                             }
                         }
                     }
-                }
-                if (p.dot != nullptr) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) dot = fmaf(wx[r], O[it][r], dot);
                     dot += lane_xor_f<16>(dot);
                     dot += lane_xor_f<32>(dot);
-                    if (qd == 0) dots[wave * kL + 16 * it + i16] = dot;
+                    if (qd == 0) dots[wave * kL + i] = dot;
+                }
+            }
+            const int64_t o0 = b * p.o_b + h * p.o_h + static_cast<int64_t>(t0) * p.o_t;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const int64_t at = o0 + (16 * it + i16) * p.o_t + n;
+                if (16 * it + i16 >= left || n >= vd) continue;
+                const f32x4 v = O[it];
+                if (F32) {
+                    float* o = static_cast<float*>(p.out) + at;
+                    if (p.out_wide) {
+                        *reinterpret_cast<f32x4*>(o) = v;
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (n + r < vd) o[r] = v[r];
+                        }
+                    }
+                } else {
+                    bf16_t* o = static_cast<bf16_t*>(p.out) + at;
+                    if (p.out_wide) {
+                        *reinterpret_cast<u32x2*>(o) = u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if (n + r < vd) o[r] = narrow<bf16_t>(v[r]);
+                        }
+                    }
                 }
             }
         } else {
             decay += gates.sum;
         }
 
-        // The state. (The last chunk's is only needed where someone reads it.)
+        // The state.
         const float all = gates.all;
 #pragma unroll
-        for (int d = 0; d < KT; ++d) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) S[d][nt] *= all;
-        }
+        for (int d = 0; d < KT; ++d) S[d] *= all;
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
-            Parts<T, P3> zp[NT];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float z[8];
-                widen8(col_frag<VD, 4>(zt, jb, n0 + 16 * nt, i16, qd), z);
+            Parts<T, P3> zp;
+            {
                 const f32x4 ua = *reinterpret_cast<const f32x4*>(&gates.u[32 * jb + 4 * qd]);
                 const f32x4 ub = *reinterpret_cast<const f32x4*>(&gates.u[32 * jb + 16 + 4 * qd]);
+                float z[8];
+                widen8(col_frag<VD, 4>(zc, jb, n0, i16, qd), z);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) { z[r] *= ua[r]; z[4 + r] *= ub[r]; }
-                cut(z, zp[nt]);
+                cut(z, zp);
             }
 #pragma unroll
-            for (int d = 0; d < KT; ++d) {
-                const Frag<T> yf = col_frag<KD, 8>(yt, jb, 32 * (d >> 1) + 4 * (d & 1), i16, qd);
+            for (int d = 0; d < KT; d += 4) {
+                Frag<T> yf[4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int e = 0; e < 4; ++e) yf[e] = col_frag<KD, 8>(yc, jb, 32 * ((d + e) >> 1) + 4 * (e & 1), i16, qd);
 #pragma unroll
-                    for (int s = P3 - 1; s >= 0; --s) mma(yf, zp[nt].p[s], S[d][nt]);
+                for (int s = P3 - 1; s >= 0; --s) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mma(yf[e], zp.p[s], S[d + e]);
                 }
             }
         }
-        __syncthreads();   // the tiles and factors may be overwritten; the dots are complete
-        if (OUT && p.dot != nullptr && threadIdx.x < kL && t0 + static_cast<int>(threadIdx.x) < live) {
+        if (kBufs == 1) {
+            lds_barrier();   // y's and z's tiles are free; the dots are complete
+            if (more) fill_yz(next, 0);
+        }
+        if (DOT && static_cast<int>(threadIdx.x) < min(kL, left)) {
             const int i = threadIdx.x;
-            p.dot[static_cast<int64_t>(bh) * p.T + t0 + i] = dots[i] + dots[kL + i] + dots[2 * kL + i] + dots[3 * kL + i];
+            float dot = dots[i];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) dot += dots[w * kL + i];
+            p.dot[static_cast<int64_t>(bh) * p.T + t0 + i] = dot;
         }
     }
 
     if constexpr (OUT) {
         // Tokens past the row's length.
-        for (int64_t e = threadIdx.x; e < static_cast<int64_t>(t_hi - max(live, t_lo)) * vd; e += kGlrThreads) {
-            const int t = max(live, t_lo) + static_cast<int>(e / vd), n = static_cast<int>(e % vd);
-            const int64_t at = b * p.o_b + t * p.o_t + h * p.o_h + n;
-            if (p.out_f32 || sizeof(T) == 4) static_cast<float*>(p.out)[at] = 0.0f;
+        const int t_dead = max(live, t_lo);
+        for (int64_t e = threadIdx.x; e < static_cast<int64_t>(t_hi - t_dead) * vd; e += kThreads) {
+            const int t = t_dead + static_cast<int>(e / vd), col = static_cast<int>(e % vd);
+            const int64_t at = b * p.o_b + t * p.o_t + h * p.o_h + col;
+            if (F32) static_cast<float*>(p.out)[at] = 0.0f;
             else static_cast<bf16_t*>(p.out)[at] = bf16_t{0};
         }
-        if (p.dot != nullptr) {
-            for (int t = max(live, t_lo) + static_cast<int>(threadIdx.x); t < t_hi; t += kGlrThreads)
-                p.dot[static_cast<int64_t>(bh) * p.T + t] = 0.0f;
-        }
-        if (p.cross != nullptr) {
-            // <S, R> at the segment's end.
-            const float* r_ = p.r_end != nullptr ? p.r_end + (static_cast<int64_t>(bh) * p.nseg + si) * one : nullptr;
-            float x = 0.0f;
-            if (r_ != nullptr) {
+    }
+    if constexpr (DOT) {
+        for (int t = max(live, t_lo) + static_cast<int>(threadIdx.x); t < t_hi; t += kThreads)
+            p.dot[static_cast<int64_t>(bh) * p.T + t] = 0.0f;
+        // <S, R> at the segment's end (forwards only). R is made up like S, from the row's end.
+        if (p.cross == nullptr) return;
+        float x = 0.0f;
+        if (p.r_segs != nullptr || p.r_start != nullptr) {
+            const bool whole = p.r_segs != nullptr && p.chained;
+            const float* r0 = whole ? p.r_segs + (static_cast<int64_t>(bh) * p.nseg + si) * one : p.r_start != nullptr ? p.r_start + bh * one : nullptr;
+            f32x4 R[KT];
+#pragma unroll
+            for (int d = 0; d < KT; ++d) R[d] = f32x4{0, 0, 0, 0};
+            if (r0 != nullptr) {
+                const auto s = state_of(r0);
 #pragma unroll
                 for (int d = 0; d < KT; ++d) {
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const int n = n0 + 16 * nt + i16, k0 = 32 * (d >> 1) + 8 * qd + 4 * (d & 1);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if (n < vd && k0 + r < kd) x = fmaf(S[d][nt][r], r_[(k0 + r) * p.r_k + n * p.r_v], x);
-                        }
-                    }
+                    for (int r = 0; r < 4; ++r) R[d][r] = state_read(s, d, r);
                 }
             }
-            x = group_sum<kWave>(x);
-            __syncthreads();   // the last chunk's dots have been read
-            if (lane == 0) dots[wave] = x;
-            __syncthreads();
-            if (threadIdx.x == 0) p.cross[static_cast<int64_t>(bh) * p.nseg + si] = dots[0] + dots[1] + dots[2] + dots[3];
+#pragma unroll 1
+            for (int n = p.nseg - 1; !whole && n > si; --n) {
+                const auto s = state_of(p.r_segs + (static_cast<int64_t>(bh) * p.nseg + n) * one);
+                const float dec = p.r_decays[static_cast<int64_t>(bh) * p.nseg + n];
+#pragma unroll
+                for (int d = 0; d < KT; ++d) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) R[d][r] = fmaf(dec, R[d][r], state_read(s, d, r));
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < KT; ++d) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x = fmaf(S[d][r], R[d][r], x);
+            }
         }
-    } else if (threadIdx.x == 0) {
-        p.seg_decay[static_cast<int64_t>(bh) * p.nseg + si] = expf(static_cast<float>(decay));
+        x = group_sum<kWave>(x);
+        __syncthreads();   // the last chunk's dots have been read
+        if (lane == 0) dots[wave] = x;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWaves; ++w) x += dots[w];
+            p.cross[static_cast<int64_t>(bh) * p.nseg + si] = x;
+        }
     }
-    float* so = OUT ? (p.s_out != nullptr && si == (REV ? 0 : p.nseg - 1) ? p.s_out + bh * one : nullptr)
-                    : p.seg_state + (static_cast<int64_t>(bh) * p.nseg + si) * one;
+    if (!OUT && threadIdx.x == 0) p.decays[static_cast<int64_t>(bh) * p.nseg + si] = exp2_of(decay);
+    float* so = OUT ? (p.last != nullptr && si == (REV ? 0 : p.nseg - 1) ? p.last + bh * one : nullptr)
+                    : p.segs + (static_cast<int64_t>(bh) * p.nseg + si) * one;
     if (so != nullptr) {
+        const auto s = state_of(so);
 #pragma unroll
         for (int d = 0; d < KT; ++d) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int n = n0 + 16 * nt + i16, k0 = 32 * (d >> 1) + 8 * qd + 4 * (d & 1);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    if (n < vd && k0 + r < kd) so[(k0 + r) * p.s_k + n * p.s_v] = S[d][nt][r];
-                }
-            }
+            for (int r = 0; r < 4; ++r) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(S[d][r]), s, state_at(d, r), 0, 0);
         }
     }
 }
@@ -757,7 +888,8 @@ int padded(int d) { return d <= 64 ? 64 : 128; }
 Rows rows_of(const void* p, int64_t b, int64_t t, int64_t h, int width, int per, int es) {
     const int unit = 16 / es;
     Rows r{p, b, t, h, width, per, 0};
-    r.wide = reinterpret_cast<uintptr_t>(p) % 16 == 0 && b % unit == 0 && t % unit == 0 && h % unit == 0 && width % unit == 0;
+    r.wide = reinterpret_cast<uintptr_t>(p) % 16 == 0 && b % unit == 0 && t % unit == 0 && h % unit == 0 && width % unit == 0 &&
+             t >= width && t < (int64_t(1) << 30) / (kL * es);
     return r;
 }
 
@@ -765,6 +897,9 @@ Rows rows_of(const void* p, int64_t b, int64_t t, int64_t h, int width, int per,
 // kGlrSegMin tokens long.
 constexpr int kGlrBlocks = 512;
 constexpr int kGlrSegMin = 256;
+// Up to so many segments, each block adds up the segments before it by itself (half of them on average, each read
+// once); past that a kernel chains the states (read and written once more, and read).
+constexpr int kGlrOwnChain = 6;
 struct SegPlan {
     int nseg, seg;
 };
@@ -821,49 +956,64 @@ GlrLayout glr_layout(const sdm_glr_io* io, bool backward) {
 }
 
 template <typename T, int KD, int VD>
-size_t glr_lds(bool out) {
-    return static_cast<size_t>(kL) * ((out ? 2 : 1) * KD + VD) * sizeof(T) + sizeof(Gates) + 4 * kL * sizeof(float);
+size_t glr_lds(bool out, int ns) {
+    const size_t parts = sizeof(T) == 4 ? 1 : ns;
+    const size_t tiles = out ? 2 * KD + VD : (sizeof(T) == 2 ? 2 : 1) * (KD + VD);
+    return kL * tiles * sizeof(T) + (out ? 6 * parts * kWave * 8 * sizeof(T) : 0) + 2 * sizeof(Gates) +
+           VD / 16 * kL * sizeof(float);
 }
 
-template <typename T, int KD, int VD, bool REV, bool OUT, int NS>
+template <typename T, int KD, int VD, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
 hipError_t glr_go3(const GlrPass& p, hipStream_t st) {
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * p.nseg);
-    glr_kernel<T, KD, VD, REV, OUT, NS><<<grid, kGlrThreads, glr_lds<T, KD, VD>(OUT), st>>>(p);
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (OUT ? p.nseg : p.nseg - 1));
+    glr_kernel<T, KD, VD, REV, OUT, NS, DOT, FOLD><<<grid, 4 * VD, glr_lds<T, KD, VD>(OUT, NS), st>>>(p);
     return hipGetLastError();
 }
-template <typename T, bool REV, bool OUT, int NS>
+template <typename T, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
 hipError_t glr_go2(const GlrPass& p, hipStream_t st) {
     const int kd = padded(p.y.width), vd = padded(p.z.width);
-    if (kd == 64) return vd == 64 ? glr_go3<T, 64, 64, REV, OUT, NS>(p, st) : glr_go3<T, 64, 128, REV, OUT, NS>(p, st);
-    return vd == 64 ? glr_go3<T, 128, 64, REV, OUT, NS>(p, st) : glr_go3<T, 128, 128, REV, OUT, NS>(p, st);
+    if (kd == 64) return vd == 64 ? glr_go3<T, 64, 64, REV, OUT, NS, DOT, FOLD>(p, st) : glr_go3<T, 64, 128, REV, OUT, NS, DOT, FOLD>(p, st);
+    return vd == 64 ? glr_go3<T, 128, 64, REV, OUT, NS, DOT, FOLD>(p, st) : glr_go3<T, 128, 128, REV, OUT, NS, DOT, FOLD>(p, st);
 }
-template <bool REV, bool OUT, int NS>
+template <bool REV, bool OUT, int NS, bool DOT>
 hipError_t glr_go(const GlrPass& p, int dtype, hipStream_t st) {
-    return dtype == SDM_BF16 ? glr_go2<bf16_t, REV, OUT, NS>(p, st) : glr_go2<float, REV, OUT, NS>(p, st);
+    // float32 factors are not cut and float32 results not narrowed: one instance whatever NS and out_f32.
+    if (dtype != SDM_BF16) return glr_go2<float, REV, OUT, 3, DOT, false>(p, st);
+    if constexpr (DOT) {
+        if (p.out_f32) return glr_go2<bf16_t, REV, OUT, NS, DOT, true>(p, st);
+    }
+    return glr_go2<bf16_t, REV, OUT, NS, DOT, false>(p, st);
 }
 
+// The segments' own states (y z^T), then chained when there are many.
 template <bool REV>
-hipError_t chain(float* states, const float* decay, const float* start, int nseg, int64_t one, int64_t bh, hipStream_t st) {
+hipError_t seg_states(GlrPass p, int dtype, int64_t one, int64_t bh, hipStream_t st) {
+    hipError_t e = glr_go<REV, false, 3, false>(p, dtype, st);
+    if (e != hipSuccess || !p.chained) return e;
     const int64_t total = bh * one;
-    glr_chain_kernel<REV><<<static_cast<unsigned>((total + 255) / 256), 256, 0, st>>>(states, decay, start, nseg, one, total);
+    glr_chain_kernel<REV><<<static_cast<unsigned>((total + 255) / 256), 256, 0, st>>>(p.segs, p.decays, p.start, p.nseg, one, total);
     return hipGetLastError();
 }
 
-template <typename T, bool REV, bool OUT, int NS>
+template <typename T, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
 void list(const void** all, int& n) {
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 64, REV, OUT, NS>);
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 128, REV, OUT, NS>);
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 64, REV, OUT, NS>);
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 128, REV, OUT, NS>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 64, REV, OUT, NS, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 128, REV, OUT, NS, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 64, REV, OUT, NS, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 128, REV, OUT, NS, DOT, FOLD>);
 }
-template <typename T>
+template <typename T, int NS>
 void list_type(const void** all, int& n) {
-    list<T, false, true, 2>(all, n);
-    list<T, false, true, 3>(all, n);
-    list<T, true, true, 2>(all, n);
-    list<T, true, true, 3>(all, n);
-    list<T, false, false, 3>(all, n);
-    list<T, true, false, 3>(all, n);
+    list<T, false, true, NS, false, false>(all, n);   // o
+    list<T, true, true, NS, false, false>(all, n);    // dv
+    list<T, false, true, 3, true, false>(all, n);     // dq
+    list<T, true, true, 3, true, false>(all, n);      // dk
+    if constexpr (sizeof(T) == 2) {
+        list<T, false, true, 3, true, true>(all, n);
+        list<T, true, true, 3, true, true>(all, n);
+    }
+    list<T, false, false, 3, false, false>(all, n);
+    list<T, true, false, 3, false, false>(all, n);
 }
 
 // A pass over io's shape.
@@ -879,6 +1029,7 @@ GlrPass base_pass(const sdm_glr_io* io, const SegPlan& sp) {
     p.H = io->H;
     p.nseg = sp.nseg;
     p.seg = sp.seg;
+    p.chained = sp.nseg > kGlrOwnChain;
     p.m_p = p.m_o = p.m_s = 1.0f;
     return p;
 }
@@ -886,10 +1037,10 @@ GlrPass base_pass(const sdm_glr_io* io, const SegPlan& sp) {
 }  // namespace
 
 int glr_lds_kernels(const void** fns, int cap) {
-    const void* all[64];
+    const void* all[96];
     int n = 0;
-    list_type<bf16_t>(all, n);
-    list_type<float>(all, n);
+    list_type<bf16_t, 2>(all, n);
+    list_type<float, 3>(all, n);
     int k = 0;
     for (; k < n && k < cap; ++k) fns[k] = all[k];
     return k;
@@ -909,27 +1060,23 @@ hipError_t glr_forward_launch(const sdm_glr_io* io, hipStream_t st) {
     p.x = rows_of(io->q, io->q_b, io->q_t, io->q_h, io->dk, per, es);
     p.y = rows_of(io->k, io->k_b, io->k_t, io->k_h, io->dk, per, es);
     p.z = rows_of(io->v, io->v_b, io->v_t, io->v_h, io->dv, 1, es);
+    p.start = io->state;
     p.s_k = io->dv;
     p.s_v = 1;
     hipError_t e = hipSuccess;
     if (sp.nseg > 1) {
-        p.seg_state = reinterpret_cast<float*>(ws + l.s);
-        p.seg_decay = reinterpret_cast<float*>(ws + l.sd);
-        if ((e = glr_go<false, false, 3>(p, io->dtype, st)) != hipSuccess) return e;
-        if ((e = chain<false>(p.seg_state, p.seg_decay, io->state, sp.nseg, one, bh, st)) != hipSuccess) return e;
-        p.s_in = p.seg_state;
-    } else {
-        p.s_in = io->state;
+        p.segs = reinterpret_cast<float*>(ws + l.s);
+        p.decays = reinterpret_cast<float*>(ws + l.sd);
+        if ((e = seg_states<false>(p, io->dtype, one, bh, st)) != hipSuccess) return e;
     }
-    p.s_out = io->last;
+    p.last = io->last;
     p.m_p = p.m_o = io->scale;
     p.out = io->o;
     p.o_b = io->o_b;
     p.o_t = io->o_t;
     p.o_h = io->o_h;
-    const int ou = 4;
-    p.out_wide = reinterpret_cast<uintptr_t>(io->o) % (ou * es) == 0 && io->o_b % ou == 0 && io->o_t % ou == 0 && io->o_h % ou == 0 && io->dv % ou == 0;
-    return glr_go<false, true, 2>(p, io->dtype, st);
+    p.out_wide = reinterpret_cast<uintptr_t>(io->o) % (4 * es) == 0 && io->o_b % 4 == 0 && io->o_t % 4 == 0 && io->o_h % 4 == 0 && io->dv % 4 == 0;
+    return glr_go<false, true, 2, false>(p, io->dtype, st);
 }
 
 hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipStream_t st) {
@@ -940,91 +1087,79 @@ hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipS
     char* ws = static_cast<char*>(io->workspace);
     const Rows q = rows_of(io->q, io->q_b, io->q_t, io->q_h, io->dk, per, es), k = rows_of(io->k, io->k_b, io->k_t, io->k_h, io->dk, per, es),
                v = rows_of(io->v, io->v_b, io->v_t, io->v_h, io->dv, 1, es), d = rows_of(g->d_o, g->do_b, g->do_t, g->do_h, io->dv, 1, es);
-    const GlrPass base = base_pass(io, sp);
-    float *S = nullptr, *R = nullptr;
     hipError_t e = hipSuccess;
+    // A pass forwards on the states, and one backwards on their gradients.
+    GlrPass fwd = base_pass(io, sp), bwd = fwd;
+    fwd.start = io->state;
+    bwd.start = g->d_last;
+    fwd.s_k = bwd.s_k = io->dv;
+    fwd.s_v = bwd.s_v = 1;
+    bwd.m_s = io->scale;
     if (sp.nseg > 1) {
-        GlrPass p = base;   // the states before the segments, and the gradients of those after them
-        S = reinterpret_cast<float*>(ws + l.s);
-        R = reinterpret_cast<float*>(ws + l.r);
-        p.s_k = io->dv;
-        p.s_v = 1;
-        p.y = k;
-        p.z = v;
-        p.seg_state = S;
-        p.seg_decay = reinterpret_cast<float*>(ws + l.sd);
-        if ((e = glr_go<false, false, 3>(p, io->dtype, st)) != hipSuccess) return e;
-        if ((e = chain<false>(S, p.seg_decay, io->state, sp.nseg, one, bh, st)) != hipSuccess) return e;
-        p.y = q;
-        p.z = d;
-        p.m_s = io->scale;
-        p.seg_state = R;
-        p.seg_decay = reinterpret_cast<float*>(ws + l.rd);
-        if ((e = glr_go<true, false, 3>(p, io->dtype, st)) != hipSuccess) return e;
-        if ((e = chain<true>(R, p.seg_decay, g->d_last, sp.nseg, one, bh, st)) != hipSuccess) return e;
+        fwd.segs = reinterpret_cast<float*>(ws + l.s);
+        fwd.decays = reinterpret_cast<float*>(ws + l.sd);
+        bwd.segs = reinterpret_cast<float*>(ws + l.r);
+        bwd.decays = reinterpret_cast<float*>(ws + l.rd);
+        fwd.y = k;
+        fwd.z = v;
+        bwd.y = q;
+        bwd.z = d;
+        if ((e = seg_states<false>(fwd, io->dtype, one, bh, st)) != hipSuccess) return e;
+        if ((e = seg_states<true>(bwd, io->dtype, one, bh, st)) != hipSuccess) return e;
     }
-    const float* s_in = sp.nseg > 1 ? S : io->state;
-    const float* r_in = sp.nseg > 1 ? R : g->d_last;
     const bool fold = per > 1;
     float* dqd = reinterpret_cast<float*>(ws + l.dqd);
     float* dkd = reinterpret_cast<float*>(ws + l.dkd);
     float* cross = reinterpret_cast<float*>(ws + l.cross);
-    auto key_out = [&](GlrPass& p, void* out, size_t at) {   // [B, T, H or Hk, dk]
+    auto key_out = [&](GlrPass& p, void* out, size_t at) {   // [B, T, H or Hk, dk], on the transposed states
         p.out = fold ? static_cast<void*>(ws + at) : out;
         p.out_f32 = fold;
         p.o_h = io->dk;
         p.o_t = static_cast<int64_t>(io->H) * io->dk;
         p.o_b = p.o_t * io->T;
         p.out_wide = io->dk % 4 == 0;
+        p.s_k = 1;
+        p.s_v = io->dv;
     };
-    {   // dq: keys and values exchanged, on the transposed state
-        GlrPass p = base;
+    {   // dq: keys and values exchanged
+        GlrPass p = fwd;
         p.x = d;
         p.y = v;
         p.z = k;
         p.w = q;
         p.m_p = p.m_o = io->scale;
-        p.s_in = s_in;
-        p.s_k = 1;
-        p.s_v = io->dv;
         key_out(p, g->dq, l.fq);
         p.dot = dqd;
-        p.r_end = r_in;
-        p.r_k = 1;
-        p.r_v = io->dv;
         p.cross = cross;
-        if ((e = glr_go<false, true, 3>(p, io->dtype, st)) != hipSuccess) return e;
+        p.r_start = bwd.start;
+        p.r_segs = bwd.segs;
+        p.r_decays = bwd.decays;
+        if ((e = glr_go<false, true, 3, true>(p, io->dtype, st)) != hipSuccess) return e;
     }
-    {   // dk: back in time on the transposed gradient of the state
-        GlrPass p = base;
+    {   // dk
+        GlrPass p = bwd;
         p.x = v;
         p.y = d;
         p.z = q;
         p.w = k;
-        p.m_p = p.m_s = io->scale;
-        p.s_in = r_in;
-        p.s_k = 1;
-        p.s_v = io->dv;
+        p.m_p = io->scale;
         key_out(p, g->dk, l.fk);
         p.dot = dkd;
-        if ((e = glr_go<true, true, 3>(p, io->dtype, st)) != hipSuccess) return e;
+        if ((e = glr_go<true, true, 3, true>(p, io->dtype, st)) != hipSuccess) return e;
     }
     {   // dv
-        GlrPass p = base;
+        GlrPass p = bwd;
         p.x = k;
         p.y = q;
         p.z = d;
-        p.m_p = p.m_s = io->scale;
-        p.s_in = r_in;
-        p.s_out = g->d_state;
-        p.s_k = io->dv;
-        p.s_v = 1;
+        p.m_p = io->scale;
+        p.last = g->d_state;
         p.out = g->dv;
         p.o_h = io->dv;
         p.o_t = static_cast<int64_t>(io->H) * io->dv;
         p.o_b = p.o_t * io->T;
         p.out_wide = io->dv % 4 == 0;
-        if ((e = glr_go<true, true, 2>(p, io->dtype, st)) != hipSuccess) return e;
+        if ((e = glr_go<true, true, 2, false>(p, io->dtype, st)) != hipSuccess) return e;
     }
     if (io->T == 0) return hipSuccess;
     const int64_t waves = bh * sp.nseg;
