@@ -241,7 +241,7 @@ struct Stage {
         off = c * kElems < s.width ? static_cast<uint32_t>(row * static_cast<int>(s.t) * static_cast<int>(sizeof(T)) + c * 16) : 0xC0000000u;
     }
     // base: the chunk's first row; left: its tokens. Complete after a wait for vector memory and a barrier.
-    __device__ __forceinline__ void fill(const Rows& s, const T* base, int left, T* tile, int wave) const {
+    __device__ __forceinline__ void fill(const Rows& s, const T* base, int left, T* tile, int wave, int tid) const {
         const int tok = left < kL ? left : kL;
         if (s.wide) {
             const int bytes = ((tok - 1) * static_cast<int>(s.t) + s.width) * static_cast<int>(sizeof(T));
@@ -252,7 +252,7 @@ struct Stage {
             for (int n = 0; n < kEach; ++n) to_lds16(rsrc, to + n * THREADS * 16, static_cast<int>(off + n * step));
             return;
         }
-        for (int at = static_cast<int>(threadIdx.x); at < kL * W; at += THREADS) {
+        for (int at = tid; at < kL * W; at += THREADS) {
             const int t = at / W, col = at % W;
             T v = narrow<T>(0.0f);
             if (t < tok && col < s.width) v = base[static_cast<int64_t>(t) * s.t + col];
@@ -275,9 +275,9 @@ struct Gates {
     double sum;               // G_L
 };
 
-__device__ __forceinline__ double shfl_up_d(double x, int n) {
+__device__ __forceinline__ double shfl_up_d(double x, int n, int lane) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const int src = (static_cast<int>(lane_id()) - n) << 2;
+    const int src = (lane - n) << 2;
     const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(u)));
     const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(u >> 32)));
     return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
@@ -301,12 +301,11 @@ __device__ __forceinline__ float exp2_of(double x) {
 constexpr double kLog2E = 1.4426950408889634074;
 
 template <bool REV>
-__device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gates& o) {
-    const int l = static_cast<int>(lane_id());
+__device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gates& o, int l) {
     double G = (g < kGateMin ? kGateMin : g) * kLog2E;   // NaN stays
 #pragma unroll
     for (int n = 1; n < kL; n *= 2) {
-        const double below = shfl_up_d(G, n);
+        const double below = shfl_up_d(G, n, l);
         if (l >= n) G += below;
     }
     const int tile = l & ~15;
@@ -425,26 +424,26 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
     if (OUT) sx.init(p.x);
     sy.init(p.y);
     sz.init(p.z);
-    auto fill_x = [&](int c) {
+    auto fill_x = [&](int c, int tid) {
         const int t0 = t_lo + c * kL;
-        if (OUT) sx.fill(p.x, xb + t0 * p.x.t, live - t0, xt, wave);
+        if (OUT) sx.fill(p.x, xb + t0 * p.x.t, live - t0, xt, wave, tid);
     };
-    auto fill_yz = [&](int c, int buf) {
+    auto fill_yz = [&](int c, int buf, int tid) {
         const int t0 = t_lo + c * kL;
-        sy.fill(p.y, yb + t0 * p.y.t, live - t0, yt + buf * kL * KD, wave);
-        sz.fill(p.z, zb + t0 * p.z.t, live - t0, zt + buf * kL * VD, wave);
+        sy.fill(p.y, yb + t0 * p.y.t, live - t0, yt + buf * kL * KD, wave, tid);
+        sz.fill(p.z, zb + t0 * p.z.t, live - t0, zt + buf * kL * VD, wave, tid);
     };
     // Chunk c's gates, one token per lane (c >= 0 has tokens; a lane past them loads the last one's, and drops it).
-    auto gate_load = [&](int c) { return gb[static_cast<int64_t>(min(t_lo + max(c, 0) * kL + lane, live - 1)) * p.g_t]; };
-    auto gate_of = [&](int c, float g) { return t_lo + c * kL + lane < live ? g : 0.0f; };
+    auto gate_load = [&](int c, int lane) { return gb[static_cast<int64_t>(min(t_lo + max(c, 0) * kL + lane, live - 1)) * p.g_t]; };
+    auto gate_of = [&](int c, float g, int lane) { return t_lo + c * kL + lane < live ? g : 0.0f; };
     float next_gate = 0.0f;
     if (chunks > 0) {
         const int c = REV ? chunks - 1 : 0;
-        const float g = gate_load(c);
-        next_gate = gate_load(REV ? c - 1 : min(c + 1, chunks - 1));
-        fill_x(c);
-        fill_yz(c, 0);
-        if (wave == kWaves - 1) gate_factors<REV>(gate_of(c, g), p.m_o, p.m_s, gate_at[0]);
+        const float g = gate_load(c, lane);
+        next_gate = gate_load(REV ? c - 1 : min(c + 1, chunks - 1), lane);
+        fill_x(c, threadIdx.x);
+        fill_yz(c, 0, threadIdx.x);
+        if (wave == kWaves - 1) gate_factors<REV>(gate_of(c, g, lane), p.m_o, p.m_s, gate_at[0], lane);
     }
 
     for (int cc = 0; cc < chunks; ++cc) {
@@ -452,8 +451,9 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
         const Gates& gates = gate_at[cc & 1];
         // The lane's place, unknown to the compiler to be the same in every chunk: the many LDS addresses made from it are cheap
         // to make again, and kept over the loop they would not fit the 128 registers that two blocks per compute unit leave.
-        int here = lane;
-        __asm__ volatile("" : "+v"(here));
+        int tid = static_cast<int>(threadIdx.x);
+        __asm__ volatile("" : "+v"(tid));
+        const int here = tid & (kWave - 1);
         const int i16 = here & 15, qd = here >> 4;
         const int n = n0 + 4 * qd;   // the lane's result columns n .. n + 3, of token 16 it + lane % 16
         const int buf = kBufs == 2 ? cc & 1 : 0;
@@ -462,10 +462,10 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
         const bool more = cc + 1 < chunks;
         const int next = REV ? c - 1 : c + 1;
         tile_barrier();   // the chunk's tiles and gate factors are complete
-        if (kBufs == 2 && more) fill_yz(next, buf ^ 1);
+        if (kBufs == 2 && more) fill_yz(next, buf ^ 1, tid);
         // The next chunk's factors, by the last wave (it has one score tile, others two); its gates came a chunk ago.
-        if (more && wave == kWaves - 1) gate_factors<REV>(gate_of(next, next_gate), p.m_o, p.m_s, gate_at[(cc + 1) & 1]);
-        next_gate = gate_load(REV ? c - 2 : min(c + 2, chunks - 1));
+        if (more && wave == kWaves - 1) gate_factors<REV>(gate_of(next, next_gate, here), p.m_o, p.m_s, gate_at[(cc + 1) & 1], here);
+        next_gate = gate_load(REV ? c - 2 : min(c + 2, chunks - 1), here);
 
         if constexpr (OUT) {
             // The twelve score tiles, dealt to the waves.
@@ -543,7 +543,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
             for (int it = 0; it < 4; ++it) O[it] *= gates.f[16 * it + i16];
             lds_barrier();   // the scores are complete, and x's tile is free
-            if (more) fill_x(next);
+            if (more) fill_x(next, tid);
             // The chunk's own tokens.
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb) {
@@ -656,10 +656,10 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
         }
         if (kBufs == 1) {
             lds_barrier();   // y's and z's tiles are free; the dots are complete
-            if (more) fill_yz(next, 0);
+            if (more) fill_yz(next, 0, tid);
         }
-        if (DOT && static_cast<int>(threadIdx.x) < min(kL, left)) {
-            const int i = threadIdx.x;
+        if (DOT && tid < min(kL, left)) {
+            const int i = tid;
             float dot = dots[i];
 #pragma unroll
             for (int w = 1; w < kWaves; ++w) dot += dots[w * kL + i];
@@ -781,7 +781,7 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(const float* dq_dot,
         double x = t >= t_lo ? static_cast<double>(dq_dot[bh * T + t]) - static_cast<double>(dk_dot[bh * T + t]) : 0.0;
 #pragma unroll
         for (int n = 1; n < kWave; n *= 2) {
-            const double below = shfl_up_d(x, n);
+            const double below = shfl_up_d(x, n, lane);
             if (lane >= n) x += below;
         }
         if (t >= t_lo) dg[(b * T + t) * H + h] = t < len ? static_cast<float>(carry + x) : 0.0f;
