@@ -179,6 +179,44 @@ struct Rows {
     int wide;      // 16-byte loads: aligned rows of whole 16-byte pieces that do not overlap, 64 of them within 2^30 bytes
 };
 
+// Four consecutive elements of a row; those from `left` on are 0.
+template <typename T>
+struct Four;
+template <>
+struct Four<bf16_t> {
+    u32x2 w;
+    __device__ __forceinline__ void load(const bf16_t* p, int left, int wide) {
+        w = u32x2{0, 0};
+        if (left <= 0) return;
+        if (wide) {   // rows of whole 16-byte pieces: left is a multiple of 4
+            w = *reinterpret_cast<const u32x2*>(p);
+            return;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (r < left) w[r >> 1] |= static_cast<uint32_t>(p[r].bits) << (16 * (r & 1));
+        }
+    }
+    __device__ __forceinline__ float at(int r) const { return __uint_as_float(r & 1 ? w[r >> 1] & 0xFFFF0000u : w[r >> 1] << 16); }
+};
+template <>
+struct Four<float> {
+    f32x4 w;
+    __device__ __forceinline__ void load(const float* p, int left, int wide) {
+        w = f32x4{0, 0, 0, 0};
+        if (left <= 0) return;
+        if (wide) {
+            w = *reinterpret_cast<const f32x4*>(p);
+            return;
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (r < left) w[r] = p[r];
+        }
+    }
+    __device__ __forceinline__ float at(int r) const { return w[r]; }
+};
+
 struct GlrPass {
     Rows x, y, z, w;          // w: the rows the results are dotted with (DOT)
     const float* g;
@@ -219,11 +257,18 @@ __device__ __forceinline__ int row_len(const GlrPass& p, int b) {
 // piece that belongs there by the twist); others element by element. Zero past the row's length and the
 // head's width: the loads' buffer descriptor ends with the chunk's last token, and what lies outside its
 // range reads as zero. The range check covers the register offset, which holds all of it.
-// 16 bytes per lane from the buffer's byte offset `off` to LDS at `to` (the wave's) + 16 lane.
-__device__ __forceinline__ void to_lds16(__amdgpu_buffer_rsrc_t rsrc, char* to, int off) {
-#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no such instruction
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)to, 16, off, 0, 0, 0);
+// 16 bytes per lane from the buffer's byte offset `off` to LDS at `to` (the wave's, uniform) + 16 lane. The wait for it is
+// tile_barrier's: the compiler, which knows the builtin of this instruction but not whether a later LDS read meets its bytes,
+// would wait for it before every such read. It has no result register, so nothing is in flight towards one.
+__device__ __forceinline__ void to_lds16(u32x4 rsrc, char* to, uint32_t off) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass has no such registers
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)to));
+    __asm__ volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(at), "v"(off), "s"(rsrc) : "memory", "m0");
 #endif
+}
+__device__ __forceinline__ u32x4 buffer_of(const void* base, int bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return u32x4{static_cast<uint32_t>(p), static_cast<uint32_t>(p >> 32) & 0xFFFFu, static_cast<uint32_t>(bytes), 0x00027000u};
 }
 
 template <typename T, int W, int THREADS>
@@ -245,11 +290,11 @@ struct Stage {
         const int tok = left < kL ? left : kL;
         if (s.wide) {
             const int bytes = ((tok - 1) * static_cast<int>(s.t) + s.width) * static_cast<int>(sizeof(T));
-            const auto rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), 0, bytes, 0x00027000);
+            const u32x4 rsrc = buffer_of(base, bytes);
             const uint32_t step = static_cast<uint32_t>(kStep * static_cast<int>(s.t) * static_cast<int>(sizeof(T)));
             char* to = reinterpret_cast<char*>(tile) + wave * (kWave * 16);
 #pragma unroll
-            for (int n = 0; n < kEach; ++n) to_lds16(rsrc, to + n * THREADS * 16, static_cast<int>(off + n * step));
+            for (int n = 0; n < kEach; ++n) to_lds16(rsrc, to + n * THREADS * 16, off + n * step);
             return;
         }
         for (int at = tid; at < kL * W; at += THREADS) {
@@ -543,6 +588,13 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
             for (int it = 0; it < 4; ++it) O[it] *= gates.f[16 * it + i16];
             lds_barrier();   // the scores are complete, and x's tile is free
+            // The rows to dot the results with, then the next x: a wait for the first does not wait for the second.
+            Four<T> wx[DOT ? 4 : 1];
+            if constexpr (DOT) {
+                const T* w = static_cast<const T*>(p.w.p) + b * p.w.b + (h / p.w.per) * p.w.h + static_cast<int64_t>(t0) * p.w.t + n;
+#pragma unroll
+                for (int it = 0; it < 4; ++it) wx[it].load(w + (16 * it + i16) * p.w.t, 16 * it + i16 < left ? vd - n : 0, p.w.wide);
+            }
             if (more) fill_x(next, tid);
             // The chunk's own tokens.
 #pragma unroll
@@ -561,37 +613,14 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
             }
             // Results.
             if constexpr (DOT) {
-                const T* w = static_cast<const T*>(p.w.p) + b * p.w.b + (h / p.w.per) * p.w.h + static_cast<int64_t>(t0) * p.w.t + n;
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
-                    const int i = 16 * it + i16;
-                    float dot = 0.0f, wx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (i < left && n < vd) {
-                        if (p.w.wide) {
-                            if constexpr (sizeof(T) == 2) {
-                                const u32x2 v = *reinterpret_cast<const u32x2*>(w + i * p.w.t);
+                    float dot = 0.0f;
 #pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    wx[2 * r] = __uint_as_float(v[r] << 16);
-                                    wx[2 * r + 1] = __uint_as_float(v[r] & 0xFFFF0000u);
-                                }
-                            } else {
-                                const f32x4 v = *reinterpret_cast<const f32x4*>(w + i * p.w.t);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) wx[r] = v[r];
-                            }
-                        } else {
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) {
-                                if (n + r < vd) wx[r] = widen(w[i * p.w.t + r]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) dot = fmaf(wx[r], O[it][r], dot);
+                    for (int r = 0; r < 4; ++r) dot = fmaf(wx[it].at(r), O[it][r], dot);
                     dot += lane_xor_f<16>(dot);
                     dot += lane_xor_f<32>(dot);
-                    if (qd == 0) dots[wave * kL + i] = dot;
+                    if (qd == 0) dots[wave * kL + 16 * it + i16] = dot;
                 }
             }
             const int64_t o0 = b * p.o_b + h * p.o_h + static_cast<int64_t>(t0) * p.o_t;
