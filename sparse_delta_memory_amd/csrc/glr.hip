@@ -320,17 +320,29 @@ struct Gates {
     double sum;               // G_L
 };
 
-__device__ __forceinline__ double shfl_up_d(double x, int n, int lane) {
+// x of the lane DPP names, 0 where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_d(double x) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const int src = (lane - n) << 2;
-    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(u)));
-    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(src, static_cast<int>(u >> 32)));
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u), CTRL, ROWS, 0xF, false));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(u >> 32), CTRL, ROWS, 0xF, false));
     return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
-__device__ __forceinline__ double lane_d(double x, int lane) {
+// Inclusive sums over the wave's lanes: row shifts by 1, 2, 4, 8, then the row ends (row_bcast 15, 31).
+__device__ __forceinline__ double scan_d(double x) {
+    x += dpp_d<0x111, 0xF>(x);
+    x += dpp_d<0x112, 0xF>(x);
+    x += dpp_d<0x114, 0xF>(x);
+    x += dpp_d<0x118, 0xF>(x);
+    x += dpp_d<0x142, 0xA>(x);
+    x += dpp_d<0x143, 0xC>(x);
+    return x;
+}
+// x of one lane, the same for all.
+__device__ __forceinline__ double uniform_d(double x, int lane) {
     const uint64_t u = __builtin_bit_cast(uint64_t, x);
-    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(lane << 2, static_cast<int>(u)));
-    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(lane << 2, static_cast<int>(u >> 32)));
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u), lane));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(u >> 32), lane));
     return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | lo);
 }
 
@@ -347,14 +359,10 @@ constexpr double kLog2E = 1.4426950408889634074;
 
 template <bool REV>
 __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gates& o, int l) {
-    double G = (g < kGateMin ? kGateMin : g) * kLog2E;   // NaN stays
-#pragma unroll
-    for (int n = 1; n < kL; n *= 2) {
-        const double below = shfl_up_d(G, n, l);
-        if (l >= n) G += below;
-    }
-    const int tile = l & ~15;
-    const double before = lane_d(G, (tile + 63) & 63), end = lane_d(G, tile + 15), last = lane_d(G, kL - 1);
+    const double G = scan_d((g < kGateMin ? kGateMin : g) * kLog2E);   // NaN stays
+    const double e0 = uniform_d(G, 15), e1 = uniform_d(G, 31), e2 = uniform_d(G, 47), last = uniform_d(G, 63);   // ends of the tiles of 16
+    const int tile = l >> 4;
+    const double before = tile == 1 ? e0 : tile == 2 ? e1 : e2, end = tile == 0 ? e0 : tile == 1 ? e1 : tile == 2 ? e2 : last;
     const double local = tile > 0 ? G - before : G;
     const float hi = static_cast<float>(local);
     o.lhi[l] = hi;
@@ -364,10 +372,10 @@ __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gate
     const float fwd = exp2_of(G), bwd = exp2_of(last - G);
     o.f[l] = (REV ? bwd : fwd) * m_o;
     o.u[l] = (REV ? fwd : bwd) * m_s;
-    {
-        const int it = (l >> 2) & 3, jt = l & 3, hi_t = it > jt ? it : jt, lo_t = it > jt ? jt : it;
-        const double a = lane_d(G, (16 * hi_t + 63) & 63), b = lane_d(G, 16 * lo_t + 15);   // start of tile hi_t, end of lo_t
-        if (l < 16) o.tau[l] = it == jt ? 1.0f : exp2_of(a - b);
+    if (l < 16) {   // tile it and jt: from the end of the lower to the start of the higher
+        const int it = l >> 2, jt = l & 3, hi_t = it > jt ? it : jt, lo_t = it > jt ? jt : it;
+        const double a = hi_t == 1 ? e0 : hi_t == 2 ? e1 : e2, b = lo_t == 0 ? e0 : lo_t == 1 ? e1 : e2;
+        o.tau[l] = it == jt ? 1.0f : exp2_of(a - b);
     }
     if (l == 0) {
         o.all = exp2_of(last);
@@ -792,29 +800,35 @@ __global__ __launch_bounds__(256) void glr_chain_kernel(float* states, const flo
     }
 }
 
-// dg: one wave per (stream, head, segment), 64 tokens at a time from the segment's end, in float64.
+// dg: one wave per (stream, head, segment), 256 tokens at a time from the segment's end, in float64.
 __global__ __launch_bounds__(256) void glr_gate_grad_kernel(const float* dq_dot, const float* dk_dot, const float* cross,
                                                             const int32_t* lens, float* dg, int T, int H, int nseg, int seg,
                                                             int64_t waves) {
     const int64_t id = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kWave;
     if (id >= waves) return;
+    constexpr int kU = 4;
     const int lane = static_cast<int>(lane_id());
     const int si = static_cast<int>(id % nseg);
     const int64_t bh = id / nseg, b = bh / H, h = bh - b * H;
     int len = lens != nullptr ? lens[b] : T;
     len = len < 0 ? 0 : len > T ? T : len;
     const int t_lo = si * seg, t_hi = min(T, t_lo + seg);
-    double carry = cross != nullptr ? cross[bh * nseg + si] : 0.0f;
-    for (int t1 = t_hi; t1 > t_lo; t1 -= kWave) {   // lane l takes token t1 - 1 - l
-        const int t = t1 - 1 - lane;
-        double x = t >= t_lo ? static_cast<double>(dq_dot[bh * T + t]) - static_cast<double>(dk_dot[bh * T + t]) : 0.0;
+    double carry = cross[bh * nseg + si];
+    for (int t1 = t_hi; t1 > t_lo; t1 -= kU * kWave) {   // lane l takes tokens t1 - 1 - l - 64 u
+        float q[kU], k[kU];
 #pragma unroll
-        for (int n = 1; n < kWave; n *= 2) {
-            const double below = shfl_up_d(x, n, lane);
-            if (lane >= n) x += below;
+        for (int u = 0; u < kU; ++u) {
+            const int64_t at = bh * T + max(t1 - 1 - lane - u * kWave, t_lo);
+            q[u] = dq_dot[at];
+            k[u] = dk_dot[at];
         }
-        if (t >= t_lo) dg[(b * T + t) * H + h] = t < len ? static_cast<float>(carry + x) : 0.0f;
-        carry += lane_d(x, kWave - 1);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int t = t1 - 1 - lane - u * kWave;
+            const double x = scan_d(t >= t_lo ? static_cast<double>(q[u]) - static_cast<double>(k[u]) : 0.0);
+            if (t >= t_lo) dg[(b * T + t) * H + h] = t < len ? static_cast<float>(carry + x) : 0.0f;
+            carry += uniform_d(x, kWave - 1);
+        }
     }
 }
 

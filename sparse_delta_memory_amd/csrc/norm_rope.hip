@@ -475,22 +475,31 @@ __global__ __launch_bounds__(kNrThreads) void norm_rope_back_any_kernel(NrBack b
     }
 }
 
-// The blocks' rows added: 16 columns per block, 16 rows at a time, then the 16 partial sums in order.
-__global__ __launch_bounds__(256) void norm_rope_sum_kernel(const float* part, int rows, int D, float* dwq, float* dwk) {
-    __shared__ float s[16][17];
-    const int col = blockIdx.x * 16 + threadIdx.x % 16, r0 = threadIdx.x / 16;
-    float v = 0.0f;
+// The blocks' rows added: 16 columns per block, 64 runs of rows side by side with 4 loads in flight each, then the 64
+// partial sums in a fixed tree.
+constexpr int kNrSumRuns = 64;
+__global__ __launch_bounds__(16 * kNrSumRuns) void norm_rope_sum_kernel(const float* part, int rows, int D, float* dwq, float* dwk) {
+    __shared__ float s[kNrSumRuns][17];
+    const int c = threadIdx.x % 16, r0 = threadIdx.x / 16, col = blockIdx.x * 16 + c;
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (col < 2 * D) {
-        for (int r = r0; r < rows; r += 16) v += part[static_cast<int64_t>(r) * 2 * D + col];
-    }
-    s[r0][threadIdx.x % 16] = v;
-    __syncthreads();
-    if (r0 == 0 && col < 2 * D) {
-        float t = 0.0f;
+        for (int r = r0; r < rows; r += 4 * kNrSumRuns) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) t += s[k][threadIdx.x];
+            for (int u = 0; u < 4; ++u) {
+                const int row = r + u * kNrSumRuns;
+                const float x = part[static_cast<int64_t>(min(row, rows - 1)) * 2 * D + col];
+                v[u] += row < rows ? x : 0.0f;
+            }
+        }
+    }
+    s[r0][c] = (v[0] + v[1]) + (v[2] + v[3]);
+    for (int n = kNrSumRuns / 2; n > 0; n /= 2) {
+        __syncthreads();
+        if (r0 < n) s[r0][c] += s[r0 + n][c];
+    }
+    if (r0 == 0 && col < 2 * D) {
         float* o = col < D ? dwq : dwk;
-        if (o != nullptr) o[col < D ? col : col - D] = t;
+        if (o != nullptr) o[col < D ? col : col - D] = s[0][c];
     }
 }
 
@@ -619,7 +628,7 @@ hipError_t norm_rope_back_launch(const sdm_norm_rope_io* io, const sdm_norm_rope
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || (g->dwq == nullptr && g->dwk == nullptr)) return e;
-    norm_rope_sum_kernel<<<(2 * io->D + 15) / 16, 256, 0, st>>>(b.part, static_cast<int>(blocks), io->D, g->dwq, g->dwk);
+    norm_rope_sum_kernel<<<(2 * io->D + 15) / 16, 16 * kNrSumRuns, 0, st>>>(b.part, static_cast<int>(blocks), io->D, g->dwq, g->dwk);
     return hipGetLastError();
 }
 
