@@ -515,6 +515,15 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
         const bool more = cc + 1 < chunks;
         const int next = REV ? c - 1 : c + 1;
         tile_barrier();   // the chunk's tiles and gate factors are complete
+        // The compiler does not count the tile loads: its own wait for an ordinary load would take in those issued behind it.
+        // So ordinary loads are waited for where no tile load is behind them: the next chunk's gates here, w's rows below.
+        __asm__ volatile("" : "+v"(next_gate));
+        Four<T> wx[DOT ? 4 : 1];   // the rows to dot the results with
+        if constexpr (DOT) {
+            const T* w = static_cast<const T*>(p.w.p) + b * p.w.b + (h / p.w.per) * p.w.h + static_cast<int64_t>(t0) * p.w.t + n;
+#pragma unroll
+            for (int it = 0; it < 4; ++it) wx[it].load(w + (16 * it + i16) * p.w.t, 16 * it + i16 < left ? vd - n : 0, p.w.wide);
+        }
         if (kBufs == 2 && more) fill_yz(next, buf ^ 1, tid);
         // The next chunk's factors, by the last wave (it has one score tile, others two); its gates came a chunk ago.
         if (more && wave == kWaves - 1) gate_factors<REV>(gate_of(next, next_gate, here), p.m_o, p.m_s, gate_at[(cc + 1) & 1], here);
@@ -596,12 +605,9 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
             for (int it = 0; it < 4; ++it) O[it] *= gates.f[16 * it + i16];
             lds_barrier();   // the scores are complete, and x's tile is free
-            // The rows to dot the results with, then the next x: a wait for the first does not wait for the second.
-            Four<T> wx[DOT ? 4 : 1];
             if constexpr (DOT) {
-                const T* w = static_cast<const T*>(p.w.p) + b * p.w.b + (h / p.w.per) * p.w.h + static_cast<int64_t>(t0) * p.w.t + n;
 #pragma unroll
-                for (int it = 0; it < 4; ++it) wx[it].load(w + (16 * it + i16) * p.w.t, 16 * it + i16 < left ? vd - n : 0, p.w.wide);
+                for (int it = 0; it < 4; ++it) __asm__ volatile("" : "+v"(wx[it].w));
             }
             if (more) fill_x(next, tid);
             // The chunk's own tokens.
