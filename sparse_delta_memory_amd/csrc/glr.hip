@@ -945,7 +945,7 @@ Rows rows_of(const void* p, int64_t b, int64_t t, int64_t h, int width, int per,
 // Segments of the time axis: enough that streams x heads x segments are kGlrBlocks blocks, each at least
 // kGlrSegMin tokens long.
 constexpr int kGlrBlocks = 512;
-constexpr int kGlrSegMin = 256;
+constexpr int kGlrSegMin = 128;
 // Up to so many segments, each block adds up the segments before it by itself (half of them on average, each read
 // once); past that a kernel chains the states (read and written once more, and read).
 constexpr int kGlrOwnChain = 6;
