@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -106,6 +107,17 @@ class PaIO(ctypes.Structure):
     ]
 
 
+_CODES = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_size_t: "N"}
+
+
+def packer(cls):
+    """A function of the structure's fields, in order, to its bytes: what a call of one small kernel passes (filling a
+    ctypes structure of 40 fields costs several times as much). A NULL pointer is 0."""
+    s = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0q")
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
 class NormRopeIO(ctypes.Structure):
     _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k")] + [
         (f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head")] + [
@@ -157,6 +169,10 @@ class GlrStepIO(ctypes.Structure):
         (f, ctypes.c_int32) for f in ("B", "H", "Hk", "dk", "dv", "dtype")] + [("scale", ctypes.c_float)]
 
 
+pack_norm_rope, pack_norm_rope_grad = packer(NormRopeIO), packer(NormRopeGrad)
+pack_slot_topk, pack_slot_topk_grad = packer(SlotTopkIO), packer(SlotTopkGrad)
+pack_glr, pack_glr_grad, pack_glr_step = packer(GlrIO), packer(GlrGrad), packer(GlrStepIO)
+
 EXPORTS = ["sdm_phase1_workspace", "sdm_phase1", "sdm_phase1_pairs", "sdm_dw_workspace", "sdm_dw_step", "sdm_dw_step_noalloc", "sdm_read_step",
            "sdm_gds_workspace", "sdm_gds_step", "sdm_gwr_step", "sdm_pa_workspace", "sdm_pa_step", "sdm_norm_rope",
            "sdm_norm_rope_workspace", "sdm_norm_rope_backward", "sdm_slot_topk", "sdm_slot_topk_backward", "sdm_glr_workspace",
@@ -169,6 +185,8 @@ _lib = None
 def load() -> ctypes.CDLL:
     """Load libsdm_amd.so; raises if it has not been built (no fallback path exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -209,11 +227,11 @@ def load() -> ctypes.CDLL:
                            ("sdm_slot_topk", [SlotTopkIO]), ("sdm_slot_topk_backward", [SlotTopkIO, SlotTopkGrad]),
                            ("sdm_glr_forward", [GlrIO]), ("sdm_glr_backward", [GlrIO, GlrGrad]), ("sdm_glr_step", [GlrStepIO])):
             fn = getattr(lib, name)
-            fn.argtypes = [ctypes.POINTER(a) for a in args] + [ctypes.c_void_p]
+            fn.argtypes = [ctypes.c_void_p] * (len(args) + 1)   # the structure's bytes or a reference to it, and the stream
             fn.restype = ctypes.c_int
-        lib.sdm_norm_rope_workspace.argtypes = [ctypes.POINTER(NormRopeIO)]
+        lib.sdm_norm_rope_workspace.argtypes = [ctypes.c_void_p]
         lib.sdm_norm_rope_workspace.restype = ctypes.c_size_t
-        lib.sdm_glr_workspace.argtypes = [ctypes.POINTER(GlrIO), ctypes.c_int32]
+        lib.sdm_glr_workspace.argtypes = [ctypes.c_void_p, ctypes.c_int32]
         lib.sdm_glr_workspace.restype = ctypes.c_size_t
         lib.sdm_status_string.argtypes = [ctypes.c_int]
         lib.sdm_status_string.restype = ctypes.c_char_p
