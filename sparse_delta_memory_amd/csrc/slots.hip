@@ -8,12 +8,14 @@
 // better a, then the better b). A NaN score counts as -infinity. The weights are the softmax of the K
 // sums times `scale`; a sum of -infinity weighs 0, and so does every one when all are.
 //
-// One wave per token. The row sits in registers as ordered keys (the unsigned order is the float
-// order); the K-th best of the 64 lanes' own maxima is a bound that at least K entries meet and few
+// One wave per token. The row sits in registers as integers of the same order (bfloat16 ones two to a word); the K-th best of the 64 lanes' own maxima is a bound that at least K entries meet and few
 // others do, so one sweep of ballots moves the few entries at or above it to LDS, and sorting networks
 // over the 64 lanes (compare-exchange across lanes, no LDS for most steps) order them. Reading the
 // scores bounds it from below; the networks' vector instructions are what it spends its time on.
 #include <hip/hip_runtime.h>
+
+#include <climits>
+#include <type_traits>
 
 #include "mixer_device.hpp"
 #include "sdm_launch.hpp"
@@ -53,15 +55,35 @@ constexpr PairTable kPairsHost = make_pairs();
 static_assert(kPairsHost.count[64] == kStMaxPairs, "pairs (i, j) with (i + 1)(j + 1) <= 64");
 __constant__ PairTable kPairs = make_pairs();
 
-// Float order as unsigned order; -0 as +0, NaN as -infinity. 0 is below every float's key.
+// Float order as integer order: the magnitude's bits, negated under a minus sign, so that both zeros are
+// 0. Of 16 bits for a bfloat16, of 32 for a float; beyond the infinities' lie the NaNs'.
+template <typename T>
+struct Order;
+template <>
+struct Order<bf16_t> {
+    static constexpr int kInf = 0x7F80, kPad = -0x8000;   // kPad: below every value, places past a row's end
+    static __device__ __forceinline__ int of(bf16_t x) {
+        const int b = x.bits;
+        return b & 0x8000 ? -(b & 0x7FFF) : b;
+    }
+    static __device__ __forceinline__ float value(int v) {
+        return __uint_as_float(v < 0 ? (static_cast<uint32_t>(-v) | 0x8000u) << 16 : static_cast<uint32_t>(v) << 16);
+    }
+};
+template <>
+struct Order<float> {
+    static constexpr int kInf = 0x7F800000, kPad = INT32_MIN;
+    static __device__ __forceinline__ int of(float x) {
+        const int b = __float_as_int(x);
+        return b < 0 ? -(b & 0x7FFFFFFF) : b;
+    }
+    static __device__ __forceinline__ float value(int v) { return v < 0 ? -__int_as_float(-v) : __int_as_float(v); }
+};
+// The same of a float32 sum as unsigned key, a NaN as -infinity; 0 is below every key.
 __device__ __forceinline__ uint32_t key_of(float f) {
-    f = f != f ? -INFINITY : f + 0.0f;
-    const uint32_t u = __float_as_uint(f);
-    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+    return static_cast<uint32_t>(Order<float>::of(f != f ? -INFINITY : f)) ^ 0x80000000u;
 }
-__device__ __forceinline__ float float_of(uint32_t k) {
-    return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-}
+__device__ __forceinline__ float float_of(uint32_t k) { return Order<float>::value(static_cast<int>(k ^ 0x80000000u)); }
 
 // An entry: its key, and the complement of its place, so that the larger pair is the better entry.
 struct Entry {
@@ -122,109 +144,205 @@ __device__ __forceinline__ void merge64(Entry& best, const Entry& other) {
     best = pick(above(best, o), best, o);
     merge_steps<32>(best, false, EntryStep{});
 }
+__device__ __forceinline__ void merge64(uint32_t& best, uint32_t other) {
+    best = max(best, static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute((63 - static_cast<int>(lane_id())) << 2, static_cast<int>(other))));
+    merge_steps<32>(best, false, KeyStep{});
+}
 
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
     return static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute(lane << 2, static_cast<int>(x)));
 }
 
-// Place of value v of a lane's registers: runs of E elements per lane (E = 16 bytes' worth on the
-// vector path, 1 on the element path).
+// The order values of a row's places: NV per lane, in runs of E (16 bytes' worth on the vector path, 1 on the
+// element path). Places past the row's end hold kPad. bfloat16 vectors stay packed, two values to a word.
 template <int E>
 __device__ __forceinline__ uint32_t place(int v) {
-    return static_cast<uint32_t>((v / E) * (kWave * E) + (v % E)) + lane_id() * E;
+    return static_cast<uint32_t>((v / E) * (kWave * E) + (v % E)) | (lane_id() * E);
 }
-
-// NV keys of the row per lane; entries past n have key 0.
 template <typename T, int E, int NV>
-__device__ __forceinline__ void load_keys(const T* row, int n, uint32_t (&k)[NV]) {
-    if constexpr (E == 1) {
+struct Values {
+    int v[NV];
+    __device__ __forceinline__ void load(const T* row, int n) {
+        if constexpr (E == 1) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const uint32_t i = place<1>(v);
-            k[v] = i < static_cast<uint32_t>(n) ? key_of(widen(row[i])) : 0u;
-        }
-    } else {
-        static_assert(NV % E == 0, "whole vectors");
-        u32x4 w[NV / E];
+            for (int i = 0; i < NV; ++i) {
+                const uint32_t at = place<1>(i);
+                v[i] = at < static_cast<uint32_t>(n) ? Order<T>::of(row[at]) : Order<T>::kPad;
+            }
+        } else {
+            static_assert(sizeof(T) == 4 && E == 4 && NV % 4 == 0, "float vectors");
+            u32x4 w[NV / 4];
 #pragma unroll
-        for (int c = 0; c < NV / E; ++c) {
-            const uint32_t i = place<E>(c * E);
-            w[c] = u32x4{0, 0, 0, 0};
-            if (i < static_cast<uint32_t>(n)) w[c] = *reinterpret_cast<const u32x4*>(row + i);   // n is a multiple of E
-        }
+            for (int c = 0; c < NV / 4; ++c) {
+                const uint32_t at = place<4>(c * 4);
+                w[c] = u32x4{0, 0, 0, 0};
+                if (at < static_cast<uint32_t>(n)) w[c] = *reinterpret_cast<const u32x4*>(row + at);   // n is a multiple of 4
+            }
 #pragma unroll
-        for (int c = 0; c < NV / E; ++c) {
-            const bool in = place<E>(c * E) < static_cast<uint32_t>(n);
+            for (int c = 0; c < NV / 4; ++c) {
+                const bool in = place<4>(c * 4) < static_cast<uint32_t>(n);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float f = sizeof(T) == 4 ? __uint_as_float(w[c][e % 4])
-                                               : __uint_as_float(e % 2 ? w[c][e / 2 % 4] & 0xFFFF0000u : w[c][e / 2 % 4] << 16);
-                k[c * E + e] = in ? key_of(f) : 0u;
+                for (int e = 0; e < 4; ++e) v[c * 4 + e] = in ? Order<T>::of(__uint_as_float(w[c][e])) : Order<T>::kPad;
             }
         }
     }
-}
+    // The largest of the first and of the second half of the lane's values.
+    __device__ __forceinline__ void largest(int& first, int& second) const {
+        constexpr int kHalf = NV / 2;
+        first = v[0];
+        second = v[kHalf];
+#pragma unroll
+        for (int i = 1; i < kHalf; ++i) {
+            first = max(first, v[i]);
+            second = max(second, v[kHalf + i]);
+        }
+    }
+    __device__ __forceinline__ int get(int i) const { return v[i]; }
+    // NaNs as -infinity.
+    __device__ __forceinline__ void clean() {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (v[i] > Order<T>::kInf || (v[i] < -Order<T>::kInf && v[i] != Order<T>::kPad)) v[i] = -Order<T>::kInf;
+        }
+    }
+};
+template <int NV>
+struct Values<bf16_t, 8, NV> {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    s16x2 w[NV / 2];
+    __device__ __forceinline__ void load(const bf16_t* row, int n) {
+        u32x4 x[NV / 8];
+#pragma unroll
+        for (int c = 0; c < NV / 8; ++c) {
+            const uint32_t at = place<8>(c * 8);
+            x[c] = u32x4{0, 0, 0, 0};
+            if (at < static_cast<uint32_t>(n)) x[c] = *reinterpret_cast<const u32x4*>(row + at);   // n is a multiple of 8
+        }
+#pragma unroll
+        for (int c = 0; c < NV / 8; ++c) {
+            const bool in = place<8>(c * 8) < static_cast<uint32_t>(n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t two = x[c][e];
+                const s16x2 b = __builtin_bit_cast(s16x2, two), s = b >> 15;   // -1 under a minus sign
+                const s16x2 y = ((b & static_cast<short>(0x7FFF)) ^ s) - s;
+                w[c * 4 + e] = in ? y : s16x2{-0x8000, -0x8000};
+            }
+        }
+    }
+    __device__ __forceinline__ void largest(int& first, int& second) const {
+        s16x2 a = w[0], b = w[NV / 4];
+#pragma unroll
+        for (int i = 1; i < NV / 4; ++i) {
+            a = __builtin_elementwise_max(a, w[i]);
+            b = __builtin_elementwise_max(b, w[NV / 4 + i]);
+        }
+        first = max(static_cast<int>(a[0]), static_cast<int>(a[1]));
+        second = max(static_cast<int>(b[0]), static_cast<int>(b[1]));
+    }
+    __device__ __forceinline__ int get(int i) const { return w[i / 2][i % 2]; }
+    __device__ __forceinline__ void clean() {
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int v = w[i][e];
+                if (v > Order<bf16_t>::kInf || (v < -Order<bf16_t>::kInf && v != Order<bf16_t>::kPad))
+                    w[i][e] = static_cast<short>(-Order<bf16_t>::kInf);
+            }
+        }
+    }
+};
 
-// The best `kept` entries of the row whose keys the lanes hold, best in lane 0. list: 128 entries of LDS.
-template <int E, int NV>
-__device__ __forceinline__ Entry best_of(const uint32_t (&k)[NV], int kept, u32x2* list) {
+// What the lists and networks hold of a row's entry: for bfloat16 one word (order value, place), compared as one
+// unsigned number after Item<bf16_t>::sortable; for float32 two.
+template <typename T>
+struct Item;
+template <>
+struct Item<bf16_t> {
+    typedef uint32_t type;
+    typedef uint32_t sorted;
+    static __device__ __forceinline__ type make(int v, uint32_t at) { return (static_cast<uint32_t>(v) << 16) | at; }
+    static __device__ __forceinline__ sorted sortable(type w) { return w ^ 0x8000FFFFu; }
+    static __device__ __forceinline__ sorted none() { return 0u; }
+    static __device__ __forceinline__ float value(sorted s) { return Order<bf16_t>::value(static_cast<int16_t>((s ^ 0x80000000u) >> 16)); }
+    static __device__ __forceinline__ uint32_t at(sorted s) { return ~s & 0xFFFFu; }
+};
+template <>
+struct Item<float> {
+    typedef u32x2 type;
+    typedef Entry sorted;
+    static __device__ __forceinline__ type make(int v, uint32_t at) { return u32x2{static_cast<uint32_t>(v), at}; }
+    static __device__ __forceinline__ sorted sortable(type w) { return Entry{w[0] ^ 0x80000000u, ~w[1]}; }
+    static __device__ __forceinline__ sorted none() { return Entry{0u, 0u}; }
+    static __device__ __forceinline__ float value(const sorted& s) { return float_of(s.key); }
+    static __device__ __forceinline__ uint32_t at(const sorted& s) { return ~s.inv; }
+};
+
+// The best `kept` entries of a row, best in lane 0. list: 64 items of LDS of this wave's own.
+template <typename T, int E, int NV>
+__device__ __forceinline__ typename Item<T>::sorted best_of_row(const void* base, int64_t from, int n, int kept, typename Item<T>::type* list) {
+    using I = Item<T>;
+    Values<T, E, NV> x;
+    x.load(static_cast<const T*>(base) + from, n);
     if constexpr (NV == 1) {
-        Entry e{k[0], ~place<E>(0)};
+        x.clean();
+        typename I::sorted e = I::sortable(I::make(x.get(0), place<E>(0)));
+        if (lane_id() >= static_cast<uint32_t>(n)) e = I::none();
         sort64(e);
         return e;
     } else {
-        uint32_t m = k[0];
-#pragma unroll
-        for (int v = 1; v < NV; ++v) m = max(m, k[v]);
-        sort64(m);
-        // At least `kept` entries are at or above the kept-th best lane maximum. Entries past the row's
-        // end (key 0) are not taken: a row has at least `kept` entries.
-        const uint32_t bound = max(1u, static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(m), kept - 1)));
-        Entry best{0u, 0u};
-        int n = 0;   // entries in the list, below 64 between sweeps
-        bool have = false;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const bool in = k[v] >= bound;
-            const uint64_t mask = __ballot(in);
-            if (mask == 0) continue;
-            const int at = n + static_cast<int>(__builtin_amdgcn_mbcnt_hi(
-                                   static_cast<uint32_t>(mask >> 32),
-                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), 0u)));
-            if (in) list[at] = u32x2{k[v], ~place<E>(v)};
-            n += __popcll(mask);
-            if (n >= 64) {   // 64 of them sorted and merged, the rest moved to the front
-                __builtin_amdgcn_wave_barrier();
-                const u32x2 x = list[lane_id()], r = list[64 + lane_id()];
-                Entry e{x[0], x[1]};
-                sort64(e);
-                if (have) merge64(best, e);
-                else best = e;
-                have = true;
-                n -= 64;
-                __builtin_amdgcn_wave_barrier();
-                list[lane_id()] = r;
-                __builtin_amdgcn_wave_barrier();
+        // At least `kept` entries are at or above the kept-th best of the lanes' largest, and not many more: of random
+        // rows' 64 largest the 32nd leaves about 44 entries. For more than 32, of the 128 largest of the lanes' halves.
+        auto bound_of = [&](int& top) {
+            int first, second;
+            x.largest(first, second);
+            uint32_t m = static_cast<uint32_t>(max(first, second)) ^ 0x80000000u;
+            if (kept > 32) {
+                m = static_cast<uint32_t>(first) ^ 0x80000000u;
+                uint32_t o = static_cast<uint32_t>(second) ^ 0x80000000u;
+                sort64(m);
+                sort64(o);
+                merge64(m, o);
+            } else {
+                sort64(m);
             }
+            top = static_cast<int>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(m), 0)) ^ 0x80000000u);
+            return static_cast<int>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(m), kept - 1)) ^ 0x80000000u);
+        };
+        int top, bound = bound_of(top);
+        // A NaN among the best, or too few entries above -infinity: with the NaNs as -infinity, once more. (Otherwise NaNs of either
+        // sign are not at or above the bound.) The row's end stays below: it has at least `kept` entries.
+        if (top > Order<T>::kInf || bound <= -Order<T>::kInf) {
+            x.clean();
+            bound = max(-Order<T>::kInf, bound_of(top));
         }
-        if (n > 0) {
+        // The entries at or above the bound in rounds of 64, in the order of the sweep: one round, but for rows of many
+        // equal scores.
+        typename I::sorted best = I::none();
+        int count = 64;
+        for (int round = 0; round < count; round += 64) {
+            count = 0;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const bool in = x.get(i) >= bound;
+                const uint64_t mask = __ballot(in);
+                if (mask == 0) continue;
+                const uint32_t at = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                                              __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), static_cast<uint32_t>(count - round)));
+                if (in && at < 64u) list[at] = I::make(x.get(i), place<E>(i));
+                count += __popcll(mask);
+            }
             __builtin_amdgcn_wave_barrier();
-            const u32x2 x = list[lane_id()];
-            Entry e{static_cast<int>(lane_id()) < n ? x[0] : 0u, static_cast<int>(lane_id()) < n ? x[1] : 0u};
+            typename I::sorted e = I::sortable(list[lane_id()]);
+            __builtin_amdgcn_wave_barrier();
+            if (round + static_cast<int>(lane_id()) >= count) e = I::none();
             sort64(e);
-            if (have) merge64(best, e);
-            else best = e;
-            __builtin_amdgcn_wave_barrier();
+            if (round == 0) best = e;
+            else merge64(best, e);
         }
         return best;
     }
-}
-
-template <typename T, int E, int NV>
-__device__ __forceinline__ Entry best_of_row(const void* base, int64_t at, int n, int kept, u32x2* list) {
-    uint32_t k[NV];
-    load_keys<T, E, NV>(static_cast<const T*>(base) + at, n, k);
-    return best_of<E, NV>(k, kept, list);
 }
 
 __device__ __forceinline__ float wave_max_first(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x))); }
@@ -239,14 +357,15 @@ __device__ __forceinline__ float slot_weight(float v, float top, float scale, bo
 template <typename T, int E, int NV>
 __global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
     const sdm_slot_topk_io& io = a.io;
-    __shared__ u32x2 lists[kStWaves][128];
-    u32x2* list = lists[threadIdx.x / kWave];
+    using I = Item<T>;
+    __shared__ typename I::type lists[kStWaves][64];
+    typename I::type* list = lists[threadIdx.x / kWave];
     const int lane = static_cast<int>(lane_id());
     const int64_t waves = static_cast<int64_t>(gridDim.x) * kStWaves;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kStWaves + threadIdx.x / kWave; t < io.N; t += waves) {
-        const Entry ea = best_of_row<T, E, NV>(io.a, t * io.a_row, io.n1, a.ka, list);
-        const Entry eb = best_of_row<T, E, NV>(io.b, t * io.b_row, io.n2, a.kb, list);
-        const float va = float_of(ea.key), vb = float_of(eb.key);
+        const auto ea = best_of_row<T, E, NV>(io.a, t * io.a_row, io.n1, a.ka, list);
+        const auto eb = best_of_row<T, E, NV>(io.b, t * io.b_row, io.n2, a.kb, list);
+        const float va = I::value(ea), vb = I::value(eb);
         Entry best{0u, 0u};
         for (int p0 = 0; p0 < a.pairs; p0 += kWave) {
             const int p = p0 + lane;
@@ -261,7 +380,7 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
         }
         const uint32_t ij = ~best.inv;
         const int i = static_cast<int>((ij >> 8) & 63u), j = static_cast<int>(ij & 63u);
-        const int64_t ia = static_cast<uint32_t>(lane_value(~ea.inv, i)), jb = static_cast<uint32_t>(lane_value(~eb.inv, j));
+        const int64_t ia = static_cast<uint32_t>(lane_value(I::at(ea), i)), jb = static_cast<uint32_t>(lane_value(I::at(eb), j));
         const float v = float_of(best.key);
         const float w = slot_weight(v, wave_max_first(v), io.scale, lane < io.K);
         if (lane < io.K) {

@@ -59,8 +59,12 @@ def _ptr(t):
     return 0 if t is None else t.data_ptr()
 
 
+# The current stream's handle without a Stream object around it, where torch has that (2 us of a small call's 10).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, dev, stream, *packed):
-    st = (torch.cuda.current_stream(dev) if stream is None else stream).cuda_stream
+    st = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
             _lib.check(fn(*packed, st))
