@@ -323,6 +323,7 @@ __device__ __forceinline__ typename Item<T>::sorted best_of_row(const void* base
         int count = 64;
         for (int round = 0; round < count; round += 64) {
             count = 0;
+            __asm__ volatile("" : "+s"(bound));   // the comparisons are made in the round, not all kept for the next
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const bool in = x.get(i) >= bound;
@@ -430,16 +431,19 @@ __device__ __forceinline__ void write_row(T* out, int n, float* acc) {
 template <typename T, bool VEC>
 __device__ __forceinline__ void scatter_row(T* out, int n, int col, float d, int K, float* acc) {
     const int lane = static_cast<int>(lane_id());
-    // The first lane with this column adds every lane's entry of it, in lane order.
-    bool first = lane < K;
+    // The first lane with this column adds every lane's entry of it, in lane order. (Lanes past K take no part: their
+    // column is no column.)
+    if (lane >= K) col = -1;
+    uint64_t firsts = 0;
     float sum = 0.0f;
+#pragma unroll 4
     for (int m = 0; m < K; ++m) {
-        const int cm = __builtin_amdgcn_readlane(col, m);
+        const bool same = __builtin_amdgcn_readlane(col, m) == col;
         const float dm = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(__float_as_int(d), m)));
-        const bool same = cm == col;
         sum += same ? dm : 0.0f;
-        first = first && !(same && m < lane);
+        firsts |= __ballot(same) & -__ballot(same);   // the lowest lane of m's column
     }
+    const bool first = (firsts >> lane) & 1;
     if (first) acc[col] = sum;
     __builtin_amdgcn_wave_barrier();
     write_row<T, VEC>(out, n, acc);
@@ -470,8 +474,9 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_back_kernel(StBack b) {
             // In bounds whatever the caller passed.
             const int64_t last = static_cast<int64_t>(io.n1) * io.n2 - 1;
             id = id < 0 ? 0 : id > last ? last : id;
-            i = static_cast<int>(id / io.n2);
-            j = static_cast<int>(id - static_cast<int64_t>(i) * io.n2);
+            const uint32_t local = static_cast<uint32_t>(id), n2 = static_cast<uint32_t>(io.n2);   // below 2^24
+            i = static_cast<int>(local / n2);
+            j = static_cast<int>(local - static_cast<uint32_t>(i) * n2);
             const float s = widen(static_cast<const T*>(io.a)[t * io.a_row + i]), u = widen(static_cast<const T*>(io.b)[t * io.b_row + j]);
             const float x = s + u;
             v = x != x ? -INFINITY : x;
