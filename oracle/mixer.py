@@ -146,7 +146,7 @@ def slot_topk(a, b, K, scale, n2=None):
         pairs = []
         for x, i in enumerate(ia):
             for y, j in enumerate(ib):
-                with np.errstate(invalid="ignore"):
+                with np.errstate(invalid="ignore", over="ignore"):
                     s = np.float32(a[t, i]) + np.float32(b[t, j])
                 s = np.float32(-np.inf) if np.isnan(s) else s
                 pairs.append((-s, x, y, i * n2 + j))

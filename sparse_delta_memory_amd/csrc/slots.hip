@@ -156,9 +156,11 @@ __device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
 // The order values of a row's places: NV per lane, in runs of E (16 bytes' worth on the vector path, 1 on the
 // element path). Places past the row's end hold kPad. bfloat16 vectors stay packed, two values to a word.
 template <int E>
-__device__ __forceinline__ uint32_t place(int v) {
-    return static_cast<uint32_t>((v / E) * (kWave * E) + (v % E)) | (lane_id() * E);
+__device__ __forceinline__ uint32_t place(int v, uint32_t lane) {
+    return static_cast<uint32_t>((v / E) * (kWave * E) + (v % E)) | (lane * E);
 }
+template <int E>
+__device__ __forceinline__ uint32_t place(int v) { return place<E>(v, lane_id()); }
 template <typename T, int E, int NV>
 struct Values {
     int v[NV];
@@ -198,6 +200,7 @@ struct Values {
         }
     }
     __device__ __forceinline__ int get(int i) const { return v[i]; }
+    __device__ __forceinline__ void touch() {}
     // NaNs as -infinity.
     __device__ __forceinline__ void clean() {
 #pragma unroll
@@ -241,6 +244,11 @@ struct Values<bf16_t, 8, NV> {
         second = max(static_cast<int>(b[0]), static_cast<int>(b[1]));
     }
     __device__ __forceinline__ int get(int i) const { return w[i / 2][i % 2]; }
+    // The words as if new: what is unpacked from them is not kept over a loop.
+    __device__ __forceinline__ void touch() {
+#pragma unroll
+        for (int i = 0; i < NV / 2; ++i) __asm__ volatile("" : "+v"(w[i]));
+    }
     __device__ __forceinline__ void clean() {
 #pragma unroll
         for (int i = 0; i < NV / 2; ++i) {
@@ -323,7 +331,11 @@ __device__ __forceinline__ typename Item<T>::sorted best_of_row(const void* base
         int count = 64;
         for (int round = 0; round < count; round += 64) {
             count = 0;
-            __asm__ volatile("" : "+s"(bound));   // the comparisons are made in the round, not all kept for the next
+            // Comparisons, values and places are made in the round, not all kept for the next.
+            __asm__ volatile("" : "+s"(bound));
+            uint32_t lane = lane_id();
+            __asm__ volatile("" : "+v"(lane));
+            x.touch();
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const bool in = x.get(i) >= bound;
@@ -331,7 +343,7 @@ __device__ __forceinline__ typename Item<T>::sorted best_of_row(const void* base
                 if (mask == 0) continue;
                 const uint32_t at = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
                                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), static_cast<uint32_t>(count - round)));
-                if (in && at < 64u) list[at] = I::make(x.get(i), place<E>(i));
+                if (in && at < 64u) list[at] = I::make(x.get(i), place<E>(i, lane));
                 count += __popcll(mask);
             }
             __builtin_amdgcn_wave_barrier();
@@ -348,10 +360,11 @@ __device__ __forceinline__ typename Item<T>::sorted best_of_row(const void* base
 
 __device__ __forceinline__ float wave_max_first(float x) { return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x))); }
 
-// Weights of the K sums in lanes 0 .. K-1 (best in lane 0).
+// Weights of the K sums, one per lane of each group of G lanes.
+template <int G>
 __device__ __forceinline__ float slot_weight(float v, float top, float scale, bool on) {
     const float e = on && v > -INFINITY ? expf((v - top) * scale) : 0.0f;
-    const float s = group_sum<kWave>(e);
+    const float s = group_sum<G>(e);
     return s > 0.0f ? e / s : (s != s ? s : 0.0f);
 }
 
@@ -383,7 +396,7 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
         const int i = static_cast<int>((ij >> 8) & 63u), j = static_cast<int>(ij & 63u);
         const int64_t ia = static_cast<uint32_t>(lane_value(I::at(ea), i)), jb = static_cast<uint32_t>(lane_value(I::at(eb), j));
         const float v = float_of(best.key);
-        const float w = slot_weight(v, wave_max_first(v), io.scale, lane < io.K);
+        const float w = slot_weight<kWave>(v, wave_max_first(v), io.scale, lane < io.K);
         if (lane < io.K) {
             const int64_t off = io.chunk_rows > 0 ? (t / io.chunk_rows) % io.P * io.stream_offset : 0;
             const int64_t id = ia * io.n2 + jb + off;
@@ -427,23 +440,35 @@ __device__ __forceinline__ void write_row(T* out, int n, float* acc) {
     }
 }
 
-// acc (zero on entry and on return) gains the entries (col, d) of lanes 0 .. K-1 and is written out.
-template <typename T, bool VEC>
-__device__ __forceinline__ void scatter_row(T* out, int n, int col, float d, int K, float* acc) {
-    const int lane = static_cast<int>(lane_id());
-    // The first lane with this column adds every lane's entry of it, in lane order. (Lanes past K take no part: their
-    // column is no column.)
-    if (lane >= K) col = -1;
+// acc (zero on entry and on return) gains the entries (col, d) of the wave's EN entry lanes (lane % EN; past K: col -1) and is
+// written out. Each lane compares its entry's column with EN / (64 / EN) of the others', read from LDS two at a time, and with
+// EN = 32 the two lanes of an entry add up their halves; the lowest entry of a column writes the sum. list: EN pairs.
+template <typename T, bool VEC, int EN>
+__device__ __forceinline__ void scatter_row(T* out, int n, int col, float d, float* acc, u32x2* list) {
+    constexpr int kOwn = EN * EN / kWave;   // others per lane
+    const int lane = static_cast<int>(lane_id()), part = lane / EN * kOwn;
+    if (lane < EN) list[lane] = u32x2{static_cast<uint32_t>(col), __float_as_uint(d)};
+    __builtin_amdgcn_wave_barrier();
     uint64_t firsts = 0;
     float sum = 0.0f;
-#pragma unroll 4
-    for (int m = 0; m < K; ++m) {
-        const bool same = __builtin_amdgcn_readlane(col, m) == col;
-        const float dm = __uint_as_float(static_cast<uint32_t>(__builtin_amdgcn_readlane(__float_as_int(d), m)));
-        sum += same ? dm : 0.0f;
-        firsts |= __ballot(same) & -__ballot(same);   // the lowest lane of m's column
+#pragma unroll 8
+    for (int m = 0; m < kOwn; m += 2) {
+        const u32x4 two = *reinterpret_cast<const u32x4*>(list + part + m);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const bool same = static_cast<int>(two[2 * e]) == col;
+            sum += same ? __uint_as_float(two[2 * e + 1]) : 0.0f;
+            const uint64_t mask = __ballot(same);
+            if constexpr (EN == kWave) {
+                firsts |= mask & -mask;
+            } else {   // the two parts' columns are two different ones
+                const uint32_t lo = static_cast<uint32_t>(mask), hi = static_cast<uint32_t>(mask >> 32);
+                firsts |= (lo & -lo) | (hi & -hi);
+            }
+        }
     }
-    const bool first = (firsts >> lane) & 1;
+    if constexpr (EN < kWave) sum += lane_xor_f<32>(sum);
+    const bool first = lane < EN && col >= 0 && ((firsts >> lane) & 1);
     if (first) acc[col] = sum;
     __builtin_amdgcn_wave_barrier();
     write_row<T, VEC>(out, n, acc);
@@ -452,35 +477,36 @@ __device__ __forceinline__ void scatter_row(T* out, int n, int col, float d, int
     __builtin_amdgcn_wave_barrier();
 }
 
-template <typename T, bool VEC>
+// EN: entry lanes, 32 (K up to 32: both halves of the wave hold the entries) or 64.
+template <typename T, bool VEC, int EN>
 __global__ __launch_bounds__(kStThreads) void slot_topk_back_kernel(StBack b) {
     const sdm_slot_topk_io& io = b.io;
-    extern __shared__ float accs[];   // [waves, width]
+    extern __shared__ __align__(16) float accs[];   // [waves, width]
+    __shared__ __align__(16) u32x2 lists[kStWaves][EN];
     const int width = (max(io.n1, io.n2) + 7) & ~7;
     float* acc = accs + static_cast<size_t>(threadIdx.x / kWave) * width;
-    const int lane = static_cast<int>(lane_id());
+    u32x2* list = lists[threadIdx.x / kWave];
+    const int lane = static_cast<int>(lane_id()), entry = lane & (EN - 1);
     for (int c = lane; c < width; c += kWave) acc[c] = 0.0f;
     __builtin_amdgcn_wave_barrier();
-    const int wpb = static_cast<int>(blockDim.x) / kWave;
-    const int64_t waves = static_cast<int64_t>(gridDim.x) * wpb;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * wpb + threadIdx.x / kWave; t < io.N; t += waves) {
-        const bool on = lane < io.K;
-        int i = 0, j = 0;
+    const int64_t waves = static_cast<int64_t>(gridDim.x) * kStWaves;
+    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kStWaves + threadIdx.x / kWave; t < io.N; t += waves) {
+        const bool on = entry < io.K;
+        int i = -1, j = -1;
         float v = -INFINITY, y = 0.0f;
         if (on) {
-            int64_t id = io.idx_bytes == 8 ? static_cast<const int64_t*>(io.idx)[t * io.K + lane]
-                                           : static_cast<const int32_t*>(io.idx)[t * io.K + lane];
+            int64_t id = io.idx_bytes == 8 ? static_cast<const int64_t*>(io.idx)[t * io.K + entry]
+                                           : static_cast<const int32_t*>(io.idx)[t * io.K + entry];
+            y = b.dval[t * io.K + entry];
             if (io.chunk_rows > 0) id -= (t / io.chunk_rows) % io.P * io.stream_offset;
             // In bounds whatever the caller passed.
             const int64_t last = static_cast<int64_t>(io.n1) * io.n2 - 1;
             id = id < 0 ? 0 : id > last ? last : id;
-            const uint32_t local = static_cast<uint32_t>(id), n2 = static_cast<uint32_t>(io.n2);   // below 2^24
+            const uint32_t local = static_cast<uint32_t>(id), n2 = static_cast<uint32_t>(io.n2);   // at most 2^24
             i = static_cast<int>(local / n2);
             j = static_cast<int>(local - static_cast<uint32_t>(i) * n2);
-            const float s = widen(static_cast<const T*>(io.a)[t * io.a_row + i]), u = widen(static_cast<const T*>(io.b)[t * io.b_row + j]);
-            const float x = s + u;
+            const float x = widen(static_cast<const T*>(io.a)[t * io.a_row + i]) + widen(static_cast<const T*>(io.b)[t * io.b_row + j]);
             v = x != x ? -INFINITY : x;
-            y = b.dval[t * io.K + lane];
         }
         float top = v;
         top = fmaxf(top, lane_xor_f<1>(top));
@@ -488,14 +514,14 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_back_kernel(StBack b) {
         top = fmaxf(top, lane_xor_f<4>(top));
         top = fmaxf(top, lane_xor_f<8>(top));
         top = fmaxf(top, lane_xor_f<16>(top));
-        top = fmaxf(top, lane_xor_f<32>(top));
-        const float p = slot_weight(v, top, io.scale, on);
+        if constexpr (EN == kWave) top = fmaxf(top, lane_xor_f<32>(top));
+        const float p = slot_weight<EN>(v, top, io.scale, on);
         // A slot of weight 0 takes part in neither sum: its gradient is 0 whatever came in.
         const float py = p > 0.0f ? p * y : 0.0f;
-        const float dot = group_sum<kWave>(py);
+        const float dot = group_sum<EN>(py);
         const float d = p > 0.0f ? p * (y - dot) * io.scale : p;
-        if (b.da != nullptr) scatter_row<T, VEC>(static_cast<T*>(b.da) + t * b.da_row, io.n1, i, d, io.K, acc);
-        if (b.db != nullptr) scatter_row<T, VEC>(static_cast<T*>(b.db) + t * b.db_row, io.n2, j, d, io.K, acc);
+        if (b.da != nullptr) scatter_row<T, VEC, EN>(static_cast<T*>(b.da) + t * b.da_row, io.n1, i, d, acc, list);
+        if (b.db != nullptr) scatter_row<T, VEC, EN>(static_cast<T*>(b.db) + t * b.db_row, io.n2, j, d, acc, list);
     }
 }
 
@@ -543,10 +569,14 @@ hipError_t slot_topk_launch(const sdm_slot_topk_io* io, hipStream_t st) {
 }
 
 int slot_lds_kernels(const void** fns, int cap) {
-    const void* all[] = {reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, true>),
-                         reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, false>),
-                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, true>),
-                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, false>)};
+    const void* all[] = {reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, true, 32>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, false, 32>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, true, 32>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, false, 32>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, true, 64>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<bf16_t, false, 64>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, true, 64>),
+                         reinterpret_cast<const void*>(&slot_topk_back_kernel<float, false, 64>)};
     int n = 0;
     for (const void* f : all) {
         if (n < cap) fns[n++] = f;
@@ -570,13 +600,18 @@ hipError_t slot_topk_back_launch(const sdm_slot_topk_io* io, const sdm_slot_topk
     const int64_t need = (io->N + kStWaves - 1) / kStWaves;
     const int64_t most = 4096;   // grid-stride past 16 blocks per compute unit: the LDS rows are zeroed once per wave
     const unsigned grid = static_cast<unsigned>(need < most ? need : most);
-    if (bf) {
-        if (b.vec) slot_topk_back_kernel<bf16_t, true><<<grid, kStThreads, lds, st>>>(b);
-        else slot_topk_back_kernel<bf16_t, false><<<grid, kStThreads, lds, st>>>(b);
-    } else {
-        if (b.vec) slot_topk_back_kernel<float, true><<<grid, kStThreads, lds, st>>>(b);
-        else slot_topk_back_kernel<float, false><<<grid, kStThreads, lds, st>>>(b);
-    }
+    auto go = [&](auto entries) {
+        constexpr int EN = decltype(entries)::value;
+        if (bf) {
+            if (b.vec) slot_topk_back_kernel<bf16_t, true, EN><<<grid, kStThreads, lds, st>>>(b);
+            else slot_topk_back_kernel<bf16_t, false, EN><<<grid, kStThreads, lds, st>>>(b);
+        } else {
+            if (b.vec) slot_topk_back_kernel<float, true, EN><<<grid, kStThreads, lds, st>>>(b);
+            else slot_topk_back_kernel<float, false, EN><<<grid, kStThreads, lds, st>>>(b);
+        }
+    };
+    if (io->K <= 32) go(std::integral_constant<int, 32>{});
+    else go(std::integral_constant<int, 64>{});
     return hipGetLastError();
 }
 
