@@ -787,7 +787,7 @@ __global__ __launch_bounds__(256) void glr_chain_kernel(float* states, const flo
     if (e >= total) return;
     const int64_t bh = e / one, at = e - bh * one;
     float s = start != nullptr ? start[e] : 0.0f;
-    constexpr int kU = 8;   // segments in flight
+    constexpr int kU = 32;   // segments in flight
     for (int n0 = 0; n0 < nseg; n0 += kU) {
         float own[kU];
 #pragma unroll

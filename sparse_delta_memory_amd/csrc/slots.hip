@@ -373,24 +373,51 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
     const sdm_slot_topk_io& io = a.io;
     using I = Item<T>;
     __shared__ typename I::type lists[kStWaves][64];
+    __shared__ u32x2 wons[kStWaves][2 * kWave];
     typename I::type* list = lists[threadIdx.x / kWave];
+    u32x2* won = wons[threadIdx.x / kWave];
     const int lane = static_cast<int>(lane_id());
     const int64_t waves = static_cast<int64_t>(gridDim.x) * kStWaves;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kStWaves + threadIdx.x / kWave; t < io.N; t += waves) {
         const auto ea = best_of_row<T, E, NV>(io.a, t * io.a_row, io.n1, a.ka, list);
         const auto eb = best_of_row<T, E, NV>(io.b, t * io.b_row, io.n2, a.kb, list);
         const float va = I::value(ea), vb = I::value(eb);
-        Entry best{0u, 0u};
-        for (int p0 = 0; p0 < a.pairs; p0 += kWave) {
-            const int p = p0 + lane;
+        // The pairs 64 at a time, those that (i + 1)(j + 1) lets come first first; of the later ones only what beats the K-th
+        // best so far is kept, and ordered when there are 64 of them (or no more).
+        auto pair_at = [&](int p) {
             const uint32_t ij = p < a.pairs ? kPairs.at[p] : 0xFFFFu;
             const int i = static_cast<int>(ij >> 8), j = static_cast<int>(ij & 255u);
             const float x = __uint_as_float(lane_value(__float_as_uint(va), i)) + __uint_as_float(lane_value(__float_as_uint(vb), j));
-            Entry e{key_of(x), ~ij};
-            if (i >= a.ka || j >= a.kb) e = Entry{0u, 0u};
-            sort64(e);
-            if (p0 == 0) best = e;
-            else merge64(best, e);
+            return i < a.ka && j < a.kb ? Entry{key_of(x), ~ij} : Entry{0u, 0u};
+        };
+        Entry best = pair_at(lane);
+        sort64(best);
+        int count = 0;
+        for (int p0 = kWave; p0 < a.pairs; p0 += kWave) {
+            const Entry e = pair_at(p0 + lane);
+            const Entry low{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best.key), io.K - 1)),
+                            static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best.inv), io.K - 1))};
+            const bool in = above(e, low);
+            const uint64_t mask = __ballot(in);
+            const uint32_t at = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
+                                                          __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), static_cast<uint32_t>(count)));
+            if (in) won[at] = u32x2{e.key, e.inv};
+            count += __popcll(mask);
+            __builtin_amdgcn_wave_barrier();
+            if (count == 0 || (count < kWave && p0 + kWave < a.pairs)) continue;
+            const u32x2 w = won[lane], rest = won[kWave + lane];
+            Entry o{lane < count ? w[0] : 0u, lane < count ? w[1] : 0u};
+            sort64(o);
+            merge64(best, o);
+            __builtin_amdgcn_wave_barrier();
+            won[lane] = rest;
+            __builtin_amdgcn_wave_barrier();
+            count -= kWave;
+            if (count > 0 && p0 + kWave >= a.pairs) {   // the last ones
+                Entry l{lane < count ? rest[0] : 0u, lane < count ? rest[1] : 0u};
+                sort64(l);
+                merge64(best, l);
+            }
         }
         const uint32_t ij = ~best.inv;
         const int i = static_cast<int>((ij >> 8) & 63u), j = static_cast<int>(ij & 63u);
