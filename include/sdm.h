@@ -593,7 +593,7 @@ typedef struct sdm_glr_io {
 /*
  * Per stream and head, from S = state:  S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t.
  * States and sums are float32; of bfloat16 inputs every product is exact, and a float32 factor (a decayed
- * score, a state) enters a matrix product as two or three bfloat16 parts. Requires B * H <= 2^20,
+ * score, a state) enters a matrix product as two or three bfloat16 parts. Requires B * H <= 2^20, T <= 2^30,
  * B * T * H <= 2^31 - 1.
  */
 sdm_status sdm_glr_forward(const sdm_glr_io* io, hipStream_t st);

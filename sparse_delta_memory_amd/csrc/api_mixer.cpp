@@ -92,7 +92,7 @@ sdm_status check_heads(int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dt
 
 sdm_status check_glr(const sdm_glr_io* io, bool backward, const char* fn) {
     if (io == nullptr) return fail(SDM_EINVAL, "%s: io is NULL", fn);
-    if (io->B < 0 || io->T < 0) return fail(SDM_ESHAPE, "%s: B = %d, T = %d", fn, io->B, io->T);
+    if (io->B < 0 || io->T < 0 || io->T > (1 << 30)) return fail(SDM_ESHAPE, "%s: B = %d, T = %d (at most 2^30)", fn, io->B, io->T);
     const sdm_status rc = check_heads(io->H, io->Hk, io->dk, io->dv, io->dtype, io->scale, fn);
     if (rc != SDM_OK) return rc;
     const int64_t bh = static_cast<int64_t>(io->B) * io->H;
@@ -178,7 +178,7 @@ sdm_status sdm_slot_topk_backward(const sdm_slot_topk_io* io, const sdm_slot_top
 }
 
 size_t sdm_glr_workspace(const sdm_glr_io* io, int32_t backward) {
-    if (io == nullptr || io->B < 1 || io->T < 0 || io->H < 1 || io->Hk < 1 || io->H % io->Hk != 0 || io->dk < 1 || io->dk > 128 ||
+    if (io == nullptr || io->B < 1 || io->T < 0 || io->T > (1 << 30) || io->H < 1 || io->Hk < 1 || io->H % io->Hk != 0 || io->dk < 1 || io->dk > 128 ||
         io->dv < 1 || io->dv > 128)
         return 0;
     const int64_t bh = static_cast<int64_t>(io->B) * io->H;

@@ -15,17 +15,21 @@
 // q . dq and k . dk come from the float32 results before they are rounded, and the sums start afresh at
 // every segment (below) from <S, R> there, so that what cancels is never longer than a segment.
 //
-// Layout. A block of four waves owns one (stream, head, segment); each wave owns VD/4 columns of z, out
-// and the state, and keeps its part of the state in registers over all chunks as the accumulators of
-// 16 x 16 matrix-product tiles (rows: the key dimension). The same registers, cut into bfloat16 parts, are
-// directly the other operand of x S, and a score tile y x^T is directly the other operand of the product
-// with z, because the accumulator layout (four rows at one column per lane) equals an operand's (some
-// inner indexes at one row): the inner index is only permuted, and the matching operand is read in the
-// same permutation. So neither scores nor state pass through LDS. The scores are computed by every wave
-// (40 of its 200 to 270 matrix instructions per chunk), which costs less than a barrier and the trip
-// through LDS. Tiles of x, y and z are staged in LDS with 16-byte pieces permuted per row such that row
-// reads and transposed reads (ds_read_tr) are both free of bank conflicts; the next chunk's global loads
-// are in flight during a chunk's products.
+// Layout. A block owns one (stream, head, segment); each of its waves owns 16 columns of z, out and the
+// state (8 waves for widths past 64, else 4) and keeps its part of the state in registers over all chunks
+// as the accumulators of 16 x 16 matrix-product tiles (rows: the key dimension). The same registers, cut
+// into bfloat16 parts, are directly the other operand of x S: the accumulator layout (four rows at one
+// column per lane) equals an operand's (some inner indexes at one row); the inner index is only permuted,
+// and the matching operand is read in the same permutation. So is a score tile y x^T the other operand of
+// the product with z; the twelve score tiles of a chunk are dealt to the waves and shared through LDS in
+// that form. (Every wave computing all of them saves a barrier but took 309 us where this takes 253: 8 x
+// 4096 tokens x 16 heads of 128, then at one block per compute unit.) The products are formed transposed,
+// so that a lane holds four consecutive columns of a result row: 8-byte stores, and row dots that need two
+// lane exchanges. Tiles of x, y and z go from global memory to LDS without registers between, 16-byte
+// pieces permuted per row such that row reads and transposed reads (ds_read_tr) are free of bank
+// conflicts; x's next tile is loaded once the scores are done, y's and z's at the chunk's end, and the
+// second block of the compute unit works meanwhile. That takes 128 registers (205 with a chunk's loads
+// held in registers and one block: 253 us; 151 so).
 //
 // Numbers. Products of bfloat16 inputs are exact; a float32 factor (decayed score, state, decayed z) is
 // cut into bfloat16 parts by truncation and multiplied part by part: three parts hold all 24 bits. The
@@ -36,8 +40,16 @@
 // neither long rows nor a reset (a gate of -infinity counts as -10000) cost digits.
 //
 // Segments. With few streams and heads the time axis is cut: a first kernel sums each segment's own
-// state, a second one walks the segments' states in order, and the main kernel starts every segment from
-// the state before it.
+// state, and the main kernel starts every segment from the state before it, made up of the start and the
+// segments before (by itself when they are few, else a kernel chains them).
+//
+// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): o in 213 us, 2.6 TB/s of its 547 MB: 146 us
+// of main kernel and 70 of the segments' states, which read k and v once more. Per chunk and compute unit
+// the main kernel's 776 matrix instructions take 3100 cycles, its vector instructions (cutting states and z
+// into parts, scaling, addresses) about 3600, its LDS reads and writes about 4000, and a chunk passes in
+// 6500: no one of them alone, but what is left of them beside each other with four waves per unit of the
+// vector hardware. The backward (718 us) is three such passes and two of states; dq and dk take three
+// parts everywhere and read a fourth row for the dots, 262 us each.
 #include <hip/hip_runtime.h>
 
 #include "mixer_device.hpp"
@@ -283,7 +295,7 @@ struct Stage {
     __device__ __forceinline__ void init(const Rows& s) {
         const int row = static_cast<int>(threadIdx.x) / kPieces;
         const int c = (static_cast<int>(threadIdx.x) % kPieces) ^ twist<T, W>(row);
-        off = c * kElems < s.width ? static_cast<uint32_t>(row * static_cast<int>(s.t) * static_cast<int>(sizeof(T)) + c * 16) : 0xC0000000u;
+        off = c * kElems < s.width ? (static_cast<uint32_t>(row) * static_cast<uint32_t>(s.t) * static_cast<uint32_t>(sizeof(T)) + c * 16) : 0xC0000000u;
     }
     // base: the chunk's first row; left: its tokens. Complete after a wait for vector memory and a barrier.
     __device__ __forceinline__ void fill(const Rows& s, const T* base, int left, T* tile, int wave, int tid) const {
@@ -853,7 +865,8 @@ __global__ __launch_bounds__(256) void glr_fold_kernel(const float* in, T* out, 
 //
 // A block owns a tile of columns of one request's head: rows of the state are dealt to its lanes in
 // 16-byte pieces, read, updated and written back at once, and each column's products with q are added
-// across the block in LDS in a fixed order. Bound by the state's bytes, read once and written once.
+// across the block in LDS in a fixed order. Bound by the state's bytes, read once and written once: 256 requests
+// of 16 heads of 128 x 128 take 111 us, 4.9 TB/s (a copy of as much: 103).
 struct GlrStep {
     sdm_glr_step_io io;
     int cols;        // columns of a tile
@@ -942,25 +955,32 @@ Rows rows_of(const void* p, int64_t b, int64_t t, int64_t h, int width, int per,
     return r;
 }
 
-// Segments of the time axis: enough that streams x heads x segments are kGlrBlocks blocks, each at least
-// kGlrSegMin tokens long.
-constexpr int kGlrBlocks = 512;
-constexpr int kGlrSegMin = 128;
-// Up to so many segments, each block adds up the segments before it by itself (half of them on average, each read
-// once); past that a kernel chains the states (read and written once more, and read).
-constexpr int kGlrOwnChain = 6;
+// Segments of the time axis: 256 blocks of (stream, head, segment), one per compute unit, if there are that many chunks. A
+// second block per unit fills the first one's waits but doubles the states that the first kernel writes and the others read:
+// it pays where segments stay long. Forward, microseconds at 512 and at 256 blocks, heads of 128: 8 x 4096 tokens x 16 heads
+// 236 and 253 (segments of 1024 and 2048 tokens); 1 x 16384 x 8 82 and 75 (256 and 512); 1 x 4096 x 16 61 and 57 (128 and
+// 256); 16 x 256 x 16, whole rows at 256 blocks, 36 and 26. Down to single chunks: 4 x 1000 x 4 (width 100) with segments
+// of 64, 128 and 256 tokens at least 53, 62 and 114.
+constexpr int kGlrUnits = 256;
+constexpr int kGlrLongSeg = 1024;
+// Up to so many segments, each block adds up the segments before it by itself (half of them on average); past that a kernel
+// chains the states in place. 8 x 4096 x 16, 4 segments: 236 by themselves, 264 chained; 2 x 2048 x 16 backward, 16
+// segments: 531 and 179.
+constexpr int kGlrOwnChain = 4;
 struct SegPlan {
     int nseg, seg;
 };
 SegPlan seg_plan(int64_t bh, int T) {
-    int64_t want = (kGlrBlocks + bh - 1) / bh;
-    const int64_t most = T / kGlrSegMin > 1 ? T / kGlrSegMin : 1;
-    if (want > most) want = most;
     const int64_t chunks = (static_cast<int64_t>(T) + kL - 1) / kL;
-    const int64_t per = want > 0 ? (chunks + want - 1) / want : 1;
+    auto at = [&](int64_t blocks) {   // chunks per segment
+        const int64_t want = (blocks + bh - 1) / bh, per = (chunks + want - 1) / want;
+        return per < 1 ? 1 : per;
+    };
+    int64_t per = at(2 * kGlrUnits);
+    if (per * kL < kGlrLongSeg) per = at(kGlrUnits);
     SegPlan s;
-    s.seg = static_cast<int>((per < 1 ? 1 : per) * kL);
-    s.nseg = static_cast<int>(chunks > 0 ? (chunks * kL + s.seg - 1) / s.seg : 1);
+    s.seg = static_cast<int>(per * kL);
+    s.nseg = static_cast<int>(chunks > 0 ? (chunks + per - 1) / per : 1);
     return s;
 }
 

@@ -11,7 +11,9 @@
 // of a pair are loaded once for both; only the sum of squares (and the backward's dot) crosses lanes.
 // A team walks the heads of one token, four in flight, with the token's angles in registers: the angles
 // are 8 bytes per pair in float32, twice a bfloat16 pair's bytes, and would otherwise be read for every
-// head. Sums, norms and the rotation are float32; each result is rounded once.
+// head. Sums, norms and the rotation are float32; each result is rounded once. 32768 tokens of 16 + 4 heads
+// of 128 (bfloat16): 71 us, 4.7 TB/s of the heads (a copy of as much: 67). Backward, 16381 tokens, half of each
+// head turned: 63 us, 47 of them the walk (5.4 TB/s) and 4 the sum of the blocks' weight gradients.
 #include <hip/hip_runtime.h>
 
 #include "mixer_device.hpp"
