@@ -26,8 +26,7 @@
 // 4096 tokens x 16 heads of 128, then at one block per compute unit.) The products are formed transposed,
 // so that a lane holds four consecutive columns of a result row: 8-byte stores, and row dots that need two
 // lane exchanges. Tiles of x, y and z go from global memory to LDS without registers between, 16-byte
-// pieces permuted per row such that row reads and transposed reads (ds_read_tr) are free of bank
-// conflicts; x's next tile is loaded once the scores are done, y's and z's at the chunk's end, and the
+// pieces permuted per row against bank conflicts; x's next tile is loaded once the scores are done, y's and z's at the chunk's end, and the
 // second block of the compute unit works meanwhile. That takes 128 registers (205 with a chunk's loads
 // held in registers and one block: 253 us; 151 so).
 //
@@ -114,7 +113,11 @@ __device__ __forceinline__ void cut(const float (&x)[8], Parts<float, NS>& o) {
 template <typename T, int NS>
 constexpr int kParts = sizeof(T) == 4 ? 1 : NS;
 
-// LDS tiles [64][W]: the 16-byte piece c of a row lies at piece c ^ twist(row).
+// LDS tiles [64][W]: the 16-byte piece c of a row lies at piece c ^ twist(row), which spreads 16 rows' reads of one piece
+// and 4 rows' transposed reads over the banks. Counted, a row read still takes 8 cycles (4 at best: the lanes LDS serves
+// together are not 16 in a row) and a transposed one 4. Twists from four row bits that bring them to 4 and 2 were measured
+// too: the addresses' instructions cost more than that saves (8 x 4096 tokens x 16 heads of 128, forward 219 against 216 us,
+// backward 749 against 730).
 template <typename T, int W>
 __device__ __forceinline__ int twist(int row) {
     constexpr int pieces = W * static_cast<int>(sizeof(T)) / 16;
