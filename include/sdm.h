@@ -607,7 +607,8 @@ typedef struct sdm_glr_grad {
     void* dk;               /* OUT [B, T, Hk, dk] */
     void* dv;               /* OUT [B, T, H, dv] */
     float* dg;              /* OUT [B, T, H] float32 */
-    float* d_state;         /* OUT [B, H, dk, dv] float32: the gradient of `state` (NULL: skipped) */
+    float* d_state;         /* OUT [B, H, dk, dv] float32: the gradient of `state` (NULL: skipped; must not be d_last or
+                               `state`) */
 } sdm_glr_grad;
 
 /* The backward of sdm_glr_forward (io's o and last are not used; its workspace is of the backward size). Heads that

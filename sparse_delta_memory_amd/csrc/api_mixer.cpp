@@ -214,6 +214,8 @@ sdm_status sdm_glr_backward(const sdm_glr_io* io, const sdm_glr_grad* g, hipStre
     if (!aligned(g->dq, 16) || !aligned(g->dk, 16) || !aligned(g->dv, 16) || !aligned(g->dg, 4) || !aligned(g->d_last, 16) ||
         !aligned(g->d_state, 16))
         return fail(SDM_EALIGN, "%s: dq, dk, dv, d_last and d_state must be 16-byte aligned", fn);
+    if (g->d_state != nullptr && (g->d_state == g->d_last || g->d_state == io->state))
+        return fail(SDM_EINVAL, "%s: d_state must not be d_last or state", fn);   // every segment starts from those
     rc = set_up(fn);
     if (rc != SDM_OK) return rc;
     return launched(sdm::glr_backward_launch(io, g, st), fn);

@@ -4,8 +4,8 @@ the current stream, the HIP kernels of libsdm_amd.so do every step, and there is
 
 Heads are [.., heads, columns] device tensors with contiguous columns and any strides before them (views
 of a packed projection, say), float32 or bfloat16. Outputs are allocated unless given. Every call takes
-the current stream of the inputs' device, or `stream`; tensors that come from another stream are the
-caller's to order, as everywhere in torch.
+the current stream of the inputs' device, or `stream` (a workspace that the call allocates is kept for
+it); inputs and outputs that another stream made or uses are the caller's to order, as everywhere in torch.
 """
 
 from __future__ import annotations
@@ -63,7 +63,10 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(fn, dev, stream, *packed):
+def _call(fn, dev, stream, *packed, workspace=None):
+    """Enqueues fn. workspace: a tensor of this call's own, whose memory its stream still needs when the call returns."""
+    if stream is not None and workspace is not None:
+        workspace.record_stream(stream)
     st = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -188,7 +191,7 @@ def norm_rope_backward(d_q, d_k, q, k, q_weight=None, k_weight=None, positions=N
     at = dw.data_ptr()
     (gq, gqr, gqh), (gk, gkr, gkh) = grads
     g = _lib.pack_norm_rope_grad(gq, gk, gqr, gqh, gkr, gkh, 0 if q is None else at, 0 if k is None else at + 4 * D, ws.data_ptr(), ws.numel())
-    _call(lib.sdm_norm_rope_backward, dev, stream, io, g)
+    _call(lib.sdm_norm_rope_backward, dev, stream, io, g, workspace=ws)
     return dict(dq=dq, dk=dk, dwq=None if q is None else dw[0], dwk=None if k is None else dw[1])
 
 
@@ -311,7 +314,7 @@ def glr_forward(q, k, v, g, scale=None, state=None, lens=None, out=None, last=No
         if last is None:
             last = torch.empty((q.shape[0], v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=v.device)
     dev, io, keep = _glr_io("glr_forward", q, k, v, g, scale, state, lens, out, last, 0, workspace)
-    _call(_lib.load().sdm_glr_forward, dev, stream, io)
+    _call(_lib.load().sdm_glr_forward, dev, stream, io, workspace=keep)
     return out, last
 
 
@@ -335,7 +338,7 @@ def glr_backward(d_out, q, k, v, g, scale=None, state=None, d_last=None, lens=No
     r = dict(dq=new(q.shape, q.dtype), dk=new(k.shape, q.dtype), dv=new(v.shape, q.dtype), dg=new((B, T, H), torch.float32),
              dstate=new((B, H, dk, dv), torch.float32))
     grad = _lib.pack_glr_grad(d_out.data_ptr(), *d_out.stride()[:3], _ptr(d_last), *[t.data_ptr() for t in r.values()])
-    _call(_lib.load().sdm_glr_backward, dev, stream, io, grad)
+    _call(_lib.load().sdm_glr_backward, dev, stream, io, grad, workspace=keep)
     return r
 
 

@@ -218,6 +218,26 @@ def test_bits_stream_and_graph():
         assert torch.equal(o, o3) and torch.equal(last, last3) and all(torch.equal(r[n], r3[n]) for n in r)
 
 
+def test_workspace_on_another_stream():
+    """A call on a stream of its own, whose workspace the call allocates: what the current stream allocates and fills
+    meanwhile does not reach it."""
+    x = cuda(make(1, 4096, 4, 4, 128, 128, torch.bfloat16))
+    args = [x[n] for n in ("q", "k", "v", "g")]
+    o, last = sdm.glr_forward(*args, state=x["state"])
+    r = sdm.glr_backward(x["d_o"], *args, state=x["state"], d_last=x["d_last"])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o2, last2 = sdm.glr_forward(*args, state=x["state"], stream=s)
+    size = max(sdm.glr_workspace_bytes(1, 4096, 4, 4, 128, 128, backward=b) for b in (False, True))
+    for _ in range(4):
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255)
+    r2 = sdm.glr_backward(x["d_o"], *args, state=x["state"], d_last=x["d_last"], stream=s)
+    for _ in range(4):
+        torch.empty(size, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    assert torch.equal(o, o2) and torch.equal(last, last2) and all(torch.equal(r[n], r2[n]) for n in r)
+
+
 # ---------------------------------------------------------------------------------------- one token
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

@@ -133,7 +133,7 @@ GG = dict(d_o=FAKE, dq=FAKE, dk=FAKE, dv=FAKE, dg=FAKE)
 @pytest.mark.parametrize("kw,status", [
     (dict(B=-1), _lib.SDM_ESHAPE), (dict(T=-1), _lib.SDM_ESHAPE), (dict(H=0), _lib.SDM_ESHAPE), (dict(H=3), _lib.SDM_ESHAPE), (dict(Hk=0), _lib.SDM_ESHAPE),
     (dict(dk=0), _lib.SDM_ESHAPE), (dict(dk=129), _lib.SDM_ESHAPE), (dict(dv=129), _lib.SDM_ESHAPE), (dict(B=1 << 19, H=4), _lib.SDM_ESHAPE),
-    (dict(B=1 << 16, T=1 << 16), _lib.SDM_ESHAPE), (dict(dtype=5), _lib.SDM_EINVAL), (dict(scale=float("nan")), _lib.SDM_EINVAL),
+    (dict(B=1 << 16, T=1 << 16), _lib.SDM_ESHAPE), (dict(B=1, H=1, Hk=1, T=(1 << 30) + 1), _lib.SDM_ESHAPE), (dict(dtype=5), _lib.SDM_EINVAL), (dict(scale=float("nan")), _lib.SDM_EINVAL),
     (dict(q=None), _lib.SDM_EINVAL), (dict(g=None), _lib.SDM_EINVAL), (dict(v=FAKE + 2), _lib.SDM_EALIGN), (dict(state=FAKE + 4), _lib.SDM_EALIGN),
     (dict(lens=FAKE + 2), _lib.SDM_EALIGN), (dict(workspace=FAKE + 16), _lib.SDM_EALIGN),
     (dict(B=1, T=4096, workspace=None), _lib.SDM_EWORKSPACE), (dict(B=1, T=4096, workspace_bytes=256), _lib.SDM_EWORKSPACE),
@@ -153,7 +153,7 @@ def test_glr_more_refusals():
         assert lib.sdm_glr_forward(ctypes.byref(fill(_lib.GlrIO, GL, kw)), None) == status
     io = fill(_lib.GlrIO, GL, {})
     for kw, status in ((dict(d_o=None), _lib.SDM_EINVAL), (dict(dq=None), _lib.SDM_EINVAL), (dict(dg=None), _lib.SDM_EINVAL),
-                       (dict(dv=FAKE + 4), _lib.SDM_EALIGN), (dict(d_last=FAKE + 4), _lib.SDM_EALIGN), (dict(d_o=FAKE + 1), _lib.SDM_EALIGN)):
+                       (dict(d_last=FAKE, d_state=FAKE), _lib.SDM_EINVAL), (dict(dv=FAKE + 4), _lib.SDM_EALIGN), (dict(d_last=FAKE + 4), _lib.SDM_EALIGN), (dict(d_o=FAKE + 1), _lib.SDM_EALIGN)):
         assert lib.sdm_glr_backward(ctypes.byref(io), ctypes.byref(fill(_lib.GlrGrad, GG, kw)), None) == status
     assert lib.sdm_glr_backward(ctypes.byref(io), None, None) == _lib.SDM_EINVAL
     assert lib.sdm_glr_forward(None, None) == _lib.SDM_EINVAL
