@@ -29,6 +29,9 @@ namespace {
 constexpr int kStThreads = 256;
 constexpr int kStWaves = kStThreads / kWave;
 
+// Entries up to which inserting them one by one is less than ordering and merging 64.
+constexpr int kStInsert = 20;
+
 struct StArgs {
     sdm_slot_topk_io io;
     int ka, kb;      // kept entries of each row: min(K, n)
@@ -150,6 +153,19 @@ __device__ __forceinline__ void merge64(Entry& best, const Entry& other) {
 __device__ __forceinline__ void merge64(uint32_t& best, uint32_t other) {
     best = max(best, static_cast<uint32_t>(__builtin_amdgcn_ds_bpermute((63 - static_cast<int>(lane_id())) << 2, static_cast<int>(other))));
     merge_steps<32>(best, false, KeyStep{});
+}
+
+// Lane `from`'s entry of e into the sorted list: the entries below it move down by a lane, the last one out.
+__device__ __forceinline__ void insert(Entry& best, const Entry& e, int from) {
+    const Entry x{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(e.key), from)),
+                  static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(e.inv), from))};
+    const int pos = __popcll(__ballot(above(best, x)));   // lanes with a better one, the first ones
+    if (pos >= kWave) return;
+    const int lane = static_cast<int>(lane_id());
+    const Entry up{static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(best.key), 0x138, 0xF, 0xF, false)),   // wave_shr:1
+                   static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(best.inv), 0x138, 0xF, 0xF, false))};
+    best = pick(lane > pos, up, best);
+    best = pick(lane == pos, x, best);
 }
 
 __device__ __forceinline__ uint32_t lane_value(uint32_t x, int lane) {
@@ -376,17 +392,15 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
     const sdm_slot_topk_io& io = a.io;
     using I = Item<T>;
     __shared__ typename I::type lists[kStWaves][64];
-    __shared__ u32x2 wons[kStWaves][2 * kWave];
     typename I::type* list = lists[threadIdx.x / kWave];
-    u32x2* won = wons[threadIdx.x / kWave];
     const int lane = static_cast<int>(lane_id());
     const int64_t waves = static_cast<int64_t>(gridDim.x) * kStWaves;
     for (int64_t t = static_cast<int64_t>(blockIdx.x) * kStWaves + threadIdx.x / kWave; t < io.N; t += waves) {
         const auto ea = best_of_row<T, E, NV>(io.a, t * io.a_row, io.n1, a.ka, list);
         const auto eb = best_of_row<T, E, NV>(io.b, t * io.b_row, io.n2, a.kb, list);
         const float va = I::value(ea), vb = I::value(eb);
-        // The pairs 64 at a time, those that (i + 1)(j + 1) lets come first first; of the later ones only what beats the K-th
-        // best so far is kept, and ordered when there are 64 of them (or no more).
+        // The pairs 64 at a time, those that (i + 1)(j + 1) lets come first first. Of the later ones only what beats the K-th
+        // best so far matters: a few are inserted one by one (9 vector instructions each), many ordered and merged (220).
         auto pair_at = [&](int p) {
             const uint32_t ij = p < a.pairs ? kPairs.at[p] : 0xFFFFu;
             const int i = static_cast<int>(ij >> 8), j = static_cast<int>(ij & 255u);
@@ -395,32 +409,17 @@ __global__ __launch_bounds__(kStThreads) void slot_topk_kernel(StArgs a) {
         };
         Entry best = pair_at(lane);
         sort64(best);
-        int count = 0;
         for (int p0 = kWave; p0 < a.pairs; p0 += kWave) {
-            const Entry e = pair_at(p0 + lane);
+            Entry e = pair_at(p0 + lane);
             const Entry low{static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best.key), io.K - 1)),
                             static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(best.inv), io.K - 1))};
-            const bool in = above(e, low);
-            const uint64_t mask = __ballot(in);
-            const uint32_t at = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(mask >> 32),
-                                                          __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(mask), static_cast<uint32_t>(count)));
-            if (in) won[at] = u32x2{e.key, e.inv};
-            count += __popcll(mask);
-            __builtin_amdgcn_wave_barrier();
-            if (count == 0 || (count < kWave && p0 + kWave < a.pairs)) continue;
-            const u32x2 w = won[lane], rest = won[kWave + lane];
-            Entry o{lane < count ? w[0] : 0u, lane < count ? w[1] : 0u};
-            sort64(o);
-            merge64(best, o);
-            __builtin_amdgcn_wave_barrier();
-            won[lane] = rest;
-            __builtin_amdgcn_wave_barrier();
-            count -= kWave;
-            if (count > 0 && p0 + kWave >= a.pairs) {   // the last ones
-                Entry l{lane < count ? rest[0] : 0u, lane < count ? rest[1] : 0u};
-                sort64(l);
-                merge64(best, l);
+            uint64_t in = __ballot(above(e, low));
+            if (__popcll(in) > kStInsert) {
+                sort64(e);
+                merge64(best, e);
+                continue;
             }
+            for (; in != 0; in &= in - 1) insert(best, e, __builtin_ctzll(in));
         }
         const uint32_t ij = ~best.inv;
         const int i = static_cast<int>((ij >> 8) & 63u), j = static_cast<int>(ij & 63u);
