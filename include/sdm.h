@@ -593,8 +593,9 @@ typedef struct sdm_glr_io {
 /*
  * Per stream and head, from S = state:  S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t.
  * States and sums are float32; of bfloat16 inputs every product is exact, and a float32 factor (a decayed
- * score, a state) enters a matrix product as two or three bfloat16 parts. Requires B * H <= 2^20, T <= 2^30,
- * B * T * H <= 2^31 - 1.
+ * score, a state) enters a matrix product as two or three bfloat16 parts. A gate that resets, and gates whose
+ * product is 0 in float32, leave nothing of the state before them, finite or not (a state need not be
+ * initialised where the first token resets it). Requires B * H <= 2^20, T <= 2^30, B * T * H <= 2^31 - 1.
  */
 sdm_status sdm_glr_forward(const sdm_glr_io* io, hipStream_t st);
 size_t sdm_glr_workspace(const sdm_glr_io* io, int32_t backward);
@@ -634,7 +635,8 @@ typedef struct sdm_glr_step_io {
     float scale;
 } sdm_glr_step_io;
 
-/* The recurrence by one token: the state is read once and written once. One kernel on st. */
+/* The recurrence by one token: the state is read once and written once (a gate that resets leaves nothing of it,
+ * finite or not). One kernel on st. */
 sdm_status sdm_glr_step(const sdm_glr_step_io* io, hipStream_t st);
 
 /* Static text for a status code. */

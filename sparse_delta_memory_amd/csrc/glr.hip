@@ -84,6 +84,15 @@ __device__ __forceinline__ void mma(const Frag<float>& a, const Frag<float>& b, 
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[e], b.v[e], c, 0, 0, 0);
 }
 
+// f x, but 0 where the factor f is 0, whatever x: a reset, or a decay past the smallest float32, leaves nothing of values
+// that are not finite either. One instruction, the multiplication in which 0 times anything is 0.
+extern "C" __device__ float sdm_decayed(float f, float x) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ f32x4 decayed(float f, f32x4 x) {
+    return f32x4{sdm_decayed(f, x[0]), sdm_decayed(f, x[1]), sdm_decayed(f, x[2]), sdm_decayed(f, x[3])};
+}
+// f x + y in the same sense.
+__device__ __forceinline__ float decay_add(float f, float x, float y) { return f == 0.0f ? y : fmaf(f, x, y); }
+
 // The parts of 8 float32 values: NS bfloat16 words by truncation, or the floats themselves.
 template <typename T, int NS>
 struct Parts {
@@ -481,7 +490,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
             for (int d = 0; d < KT; ++d) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) S[d][r] = fmaf(dec, S[d][r], state_read(s, d, r));
+                for (int r = 0; r < 4; ++r) S[d][r] = decay_add(dec, S[d][r], state_read(s, d, r));
             }
         }
     }
@@ -618,7 +627,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                 }
             }
 #pragma unroll
-            for (int it = 0; it < 4; ++it) O[it] *= gates.f[16 * it + i16];
+            for (int it = 0; it < 4; ++it) O[it] = decayed(gates.f[16 * it + i16], O[it]);
             lds_barrier();   // the scores are complete, and x's tile is free
             if constexpr (DOT) {
 #pragma unroll
@@ -687,7 +696,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
         // The state.
         const float all = gates.all;
 #pragma unroll
-        for (int d = 0; d < KT; ++d) S[d] *= all;
+        for (int d = 0; d < KT; ++d) S[d] = decayed(all, S[d]);
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
             Parts<T, P3> zp;
@@ -762,7 +771,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
                 for (int d = 0; d < KT; ++d) {
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) R[d][r] = fmaf(dec, R[d][r], state_read(s, d, r));
+                    for (int r = 0; r < 4; ++r) R[d][r] = decay_add(dec, R[d][r], state_read(s, d, r));
                 }
             }
 #pragma unroll
@@ -815,7 +824,7 @@ __global__ __launch_bounds__(256) void glr_chain_kernel(float* states, const flo
             if (n0 + u < nseg) {
                 const int n = REV ? nseg - 1 - (n0 + u) : n0 + u;
                 states[(bh * nseg + n) * one + at] = s;
-                s = fmaf(decay[bh * nseg + n], s, own[u]);
+                s = decay_add(decay[bh * nseg + n], s, own[u]);
             }
         }
     }
@@ -927,7 +936,7 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrStep a) {
                 fv x = s[u];
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    x[e] = fmaf(kd, v[e], ga * x[e]);
+                    x[e] = fmaf(kd, v[e], sdm_decayed(ga, x[e]));
                     acc[e] = fmaf(qd, x[e], acc[e]);
                 }
                 *reinterpret_cast<fv*>(io.new_state + base + static_cast<int64_t>(d) * io.dv) = x;

@@ -304,7 +304,7 @@ def glr_forward(q, k, v, g, scale=None, state=None, lens=None, out=None, last=No
         S_t = exp(g_t) S_{t-1} + k_t v_t^T,    out_t = scale S_t^T q_t.
 
     q, k [B, T, Hk, dk], v [B, T, H, dv] float32 or bfloat16, g [B, T, H] float32 log gates (<= 0; -infinity resets the
-    state). H is a multiple of Hk: value head h uses query and key head h // (H // Hk). dk, dv: 1..128. scale: dk^-0.5
+    state, whatever it held). H is a multiple of Hk: value head h uses query and key head h // (H // Hk). dk, dv: 1..128. scale: dk^-0.5
     by default. state [B, H, dk, dv] float32 (None: zero). lens [B] int32 on the device: tokens of each stream, whose later tokens
     are not read and get zero outputs (None: T). last: the state after the last token. workspace: a uint8 tensor of
     glr_workspace_bytes (allocated per call by default)."""
@@ -347,7 +347,7 @@ def glr_step(q, k, v, g, state, scale=None, new_state=None, slots=None, out=None
 
     q, k [B, Hk, dk], v [B, H, dv], g [B, H] float32, state [rows, H, dk, dv] float32 contiguous. slots [B] int32 on the device:
     the row of each request (None: row b); rows must be distinct, and a request whose row is outside the
-    tensor is left out (output 0). Returns out [B, H, dv]."""
+    tensor is left out (output 0). A gate of -infinity starts from nothing, whatever the row held. Returns out [B, H, dv]."""
     fn = "glr_step"
     if q.dim() != 3 or v.dim() != 3:
         raise ValueError("%s: q, k are [B, Hk, dk] and v is [B, H, dv]" % fn)

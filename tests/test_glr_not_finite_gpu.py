@@ -1,0 +1,95 @@
+"""GPU: what the gated linear recurrence makes of values that are not finite. Where the float64 oracle's result is
+finite the kernels' is within the bounds of finite inputs (a reset, or a later token, lets nothing through), and
+where it is not, neither is the kernels' (infinity or NaN)."""
+
+import os
+import sys
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import sparse_delta_memory_amd as sdm  # noqa: E402
+from oracle import mixer as M  # noqa: E402
+from test_glr_gpu import DT, cuda, host, make, near, say  # noqa: E402
+
+INF, NAN = float("inf"), float("nan")
+
+
+def same(name, got, want, mag, n, bf):
+    fin = np.isfinite(want)
+    assert np.isfinite(mag[fin]).all()
+    g = got.float().cpu()
+    assert not np.isfinite(g.numpy()[~fin]).any(), "%s: finite where the definition is not" % name
+    near(name, g[torch.from_numpy(fin)], want[fin], mag[fin], n, bf)
+
+
+def check(x, dtype, scale, grads=("dq", "dk", "dv", "dstate")):
+    bf = dtype == torch.bfloat16
+    d, h = cuda(x), {k: host(t) for k, t in x.items()}
+    B, T, Hk, dk = x["q"].shape
+    H, dv = x["v"].shape[2:]
+    n = dk + dv + 96 + T // 64
+    args = [d[k] for k in ("q", "k", "v", "g")]
+    o, last = sdm.glr_forward(*args, scale=scale, state=d["state"], lens=d["lens"])
+    r = sdm.glr_backward(d["d_o"], *args, scale=scale, state=d["state"], d_last=d["d_last"], lens=d["lens"])
+    with np.errstate(invalid="ignore", over="ignore"):
+        wo, wl, mo, ml = M.glr_forward(h["q"], h["k"], h["v"], h["g"], scale, h["state"], h["lens"])
+        w, m = M.glr_backward(h["d_o"], h["q"], h["k"], h["v"], h["g"], scale, h["state"], h["d_last"], h["lens"])
+    same("o", o, wo, mo, n, bf)
+    same("last", last, wl, ml, n, False)
+    for name in grads:
+        rounded = bf and name in ("dq", "dk", "dv")
+        same(name, r[name], w[name], m[name], n + (2 * (H // Hk) if name != "dg" else 0), rounded)
+    return wo, w
+
+
+# (streams, tokens, heads): one chunk per segment, joined by each block or chained; rows of four chunks and no segments.
+SHAPES = [(1, 60, 2), (1, 200, 1), (1, 700, 1), (64, 200, 4)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H", SHAPES)
+def test_a_reset_clears_what_is_not_finite(dtype, B, T, H):
+    """States that hold NaN or infinity (rows of an uninitialised pool), cleared at the row's first token or later; and
+    gradients of the last state that do, backwards."""
+    say("glr reset of a state that is not finite", dtype, B, T, H)
+    x = make(B, T, H, max(1, H // 2), 16, 24, DT[dtype])
+    x["state"][:, 0] = NAN
+    x["state"][:, -1, 3:5, ::2] = INF
+    x["d_last"][0] = -INF
+    x["d_last"][-1, -1, 2, 2] = NAN
+    x["g"][0, 0] = -INF                      # a new sequence in every head
+    x["g"][-1, min(T - 1, 70), 0] = -INF
+    x["g"][-1, T // 2, -1] = -1e30
+    wo, w = check(x, DT[dtype], 0.3)
+    assert np.isfinite(wo[0]).all() and np.isfinite(w["dstate"][0]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dv", [24, 33])
+def test_a_reset_in_a_step(dtype, dv):
+    """Single tokens in rows of a pool that nobody has written: a gate of -infinity starts from nothing."""
+    say("glr step reset", dtype, dv)
+    B, H, dk, rows = 6, 2, 40, 9
+    x = cuda(make(B, 1, H, 1, dk, dv, DT[dtype]))
+    one = [x[n][:, 0] for n in ("q", "k", "v", "g")]
+    one[3][:] = -INF
+    one[3][5] = -0.5
+    want_state = torch.zeros_like(x["state"])
+    want_state[5] = x["state"][5]
+    want = sdm.glr_step(*one, want_state)
+    pool = torch.full((rows, H, dk, dv), NAN, device="cuda")
+    pool[1::2] = INF
+    slots = torch.tensor([8, 3, 0, 1, 4, 6], dtype=torch.int32, device="cuda")
+    pool[6] = x["state"][5]
+    out = sdm.glr_step(*one, pool, slots=slots)
+    assert torch.isfinite(want).all() and torch.equal(out, want) and torch.equal(pool[slots.long()], want_state)
+    assert not torch.isfinite(pool[2]).any()
