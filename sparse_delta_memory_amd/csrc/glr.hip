@@ -195,6 +195,42 @@ __device__ __forceinline__ void widen8(const Frag<float>& f, float (&x)[8]) {
     for (int e = 0; e < 8; ++e) x[e] = f.v[e];
 }
 
+// Whether any value of the wave's two operands is infinity or NaN: 0 times a finite value is 0. For bfloat16 a matrix product
+// does the 16 multiplications (four vector instructions beside it; 20 by comparisons of the exponents).
+__device__ __forceinline__ bool not_finite(const Frag<bf16_t>& f, const Frag<bf16_t>& g) {
+    f32x4 c = {0, 0, 0, 0};
+    const Frag<bf16_t> zero{u32x4{0, 0, 0, 0}};
+    mma(f, zero, c);
+    mma(g, zero, c);
+    const float x = (c[0] + c[1]) + (c[2] + c[3]);
+    return x != x;
+}
+__device__ __forceinline__ bool not_finite(const Frag<float>& f, const Frag<float>& g) {
+    float x = 0.0f;   // 0 times a finite value is 0
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x = fmaf(f.v[e], 0.0f, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x = fmaf(g.v[e], 0.0f, x);
+    return x != x;
+}
+// The values with 0 in place of those that are not finite, and 1 in their places with 0 elsewhere.
+__device__ __forceinline__ void split_finite(const Frag<bf16_t>& f, Frag<bf16_t>& finite, Frag<bf16_t>& mark) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool lo = (f.w[e] & 0x7F80u) == 0x7F80u, hi = (f.w[e] & 0x7F800000u) == 0x7F800000u;
+        finite.w[e] = (lo ? 0u : f.w[e] & 0xFFFFu) | (hi ? 0u : f.w[e] & 0xFFFF0000u);
+        mark.w[e] = (lo ? 0x3F80u : 0u) | (hi ? 0x3F800000u : 0u);
+    }
+}
+__device__ __forceinline__ void split_finite(const Frag<float>& f, Frag<float>& finite, Frag<float>& mark) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const bool bad = (__float_as_uint(f.v[e]) & 0x7F800000u) == 0x7F800000u;
+        finite.v[e] = bad ? 0.0f : f.v[e];
+        mark.v[e] = bad ? 1.0f : 0.0f;
+    }
+}
+
 // Rows of one operand: element (b, t, h / per) at p + ..., `width` of them contiguous.
 struct Rows {
     const void* p;
@@ -341,6 +377,8 @@ struct Gates {
     float f[kL], u[kL];       // factors of S^T x_i and of y_j z_j^T
     float tau[16];            // [it][jt]: exp(G at the start of tile max - G at the end of tile min)
     float all;                // exp(G_L)
+    int gone;                 // whether a token's u is 0
+    int odd;                  // set with the scores: whether one of a token with itself is not finite
     double sum;               // G_L
 };
 
@@ -395,7 +433,9 @@ __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gate
     o.down[l] = exp2_of(end - G);
     const float fwd = exp2_of(G), bwd = exp2_of(last - G);
     o.f[l] = (REV ? bwd : fwd) * m_o;
-    o.u[l] = (REV ? fwd : bwd) * m_s;
+    const float u = (REV ? fwd : bwd) * m_s;
+    o.u[l] = u;
+    const bool gone = __ballot(u == 0.0f) != 0;
     if (l < 16) {   // tile it and jt: from the end of the lower to the start of the higher
         const int it = l >> 2, jt = l & 3, hi_t = it > jt ? it : jt, lo_t = it > jt ? jt : it;
         const double a = hi_t == 1 ? e0 : hi_t == 2 ? e1 : e2, b = lo_t == 0 ? e0 : lo_t == 1 ? e1 : e2;
@@ -403,6 +443,8 @@ __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gate
     }
     if (l == 0) {
         o.all = exp2_of(last);
+        o.gone = gone;
+        o.odd = 0;
         o.sum = last;
     }
 }
@@ -415,6 +457,46 @@ struct Pairs {
     static constexpr int kIt[6] = {REV ? 0 : 0, REV ? 0 : 1, REV ? 1 : 2, REV ? 1 : 2, REV ? 2 : 3, REV ? 3 : 3};
     static constexpr int kJb[6] = {REV ? 0 : 0, REV ? 1 : 0, REV ? 0 : 0, REV ? 1 : 1, REV ? 1 : 0, REV ? 1 : 1};
 };
+
+// out_i of a chunk is not finite in the columns where z_j is not, for every token i that j reaches (D_ij > 0): NaN there.
+// Which ones is the product of the marks of such z_j with the marks of D_ij > 0.
+template <typename T, int VD, bool REV>
+__device__ __forceinline__ void stray_values(T* zc, const Gates& gates, int n0, int i16, int qd, f32x4 (&O)[4]) {
+    f32x4 E[4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) E[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) {
+        Frag<T> mark, finite;
+        split_finite(col_frag<VD, 4>(zc, jb, n0, i16, qd), finite, mark);
+#pragma unroll
+        for (int pr = 0; pr < 6; ++pr) {
+            if (Pairs<REV>::kJb[pr] != jb) continue;
+            const int it = Pairs<REV>::kIt[pr], i = 16 * it + i16;
+            float reach[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int jt = 2 * jb + (e >> 2), jj = 4 * qd + (e & 3), j = 16 * jt + jj;
+                float d = 0.0f;
+                if (jt == it) {
+                    const float x = (gates.lhi[i] - gates.lhi[j]) + (gates.llo[i] - gates.llo[j]);
+                    if (REV ? jj >= i16 : jj <= i16) d = __builtin_amdgcn_exp2f(REV ? -x : x);
+                } else if (REV ? jt > it : jt < it) {
+                    d = (REV ? gates.down : gates.up)[i] * gates.tau[4 * it + jt] * (REV ? gates.up : gates.down)[j];
+                }
+                reach[e] = d > 0.0f ? 1.0f : 0.0f;
+            }
+            Parts<T, 1> to;
+            cut(reach, to);
+            mma(mark, to.p[0], E[it]);
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) O[it][r] = E[it][r] > 0.0f ? __builtin_nanf("") : O[it][r];
+    }
+}
 
 // KD, VD: padded widths of x / y and of z (64 or 128). NS: parts of scores and of the state where it meets x.
 // OUT: results (else the segments' own states alone). DOT: row dots of the results, and <S, R>. FOLD: float32 results
@@ -525,7 +607,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 
     for (int cc = 0; cc < chunks; ++cc) {
         const int c = REV ? chunks - 1 - cc : cc, t0 = t_lo + c * kL, left = live - t0;
-        const Gates& gates = gate_at[cc & 1];
+        Gates& gates = gate_at[cc & 1];
         // The lane's place, unknown to the compiler to be the same in every chunk: the many LDS addresses made from it are cheap
         // to make again, and kept over the loop they would not fit the 128 registers that two blocks per compute unit leave.
         int tid = static_cast<int>(threadIdx.x);
@@ -576,6 +658,9 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                     for (int kb = 0; kb < KB; ++kb)
                         mma(row_frag<KD>(yc, 16 * jt + i16, kb, qd), row_frag<KD>(xt, 16 * it + i16, kb, qd), a);
                     if (jt == it) {
+                        // Every row of y is part of a score here, and with it what is not finite in y.
+                        const float odd = fmaf(a[0], 0.0f, fmaf(a[1], 0.0f, fmaf(a[2], 0.0f, a[3] * 0.0f)));
+                        if (odd != odd) gates.odd = 1;
                         const float lhi = gates.lhi[16 * it + i16], llo = gates.llo[16 * it + i16];
                         const f32x4 jh = *reinterpret_cast<const f32x4*>(&gates.lhi[16 * jt + 4 * qd]);
                         const f32x4 jl = *reinterpret_cast<const f32x4*>(&gates.llo[16 * jt + 4 * qd]);
@@ -584,13 +669,13 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                             const int j = 4 * qd + r;
                             const float x = (lhi - jh[r]) + (llo - jl[r]);
                             const float w = __builtin_amdgcn_exp2f(REV ? -x : x);
-                            s[r] = (REV ? j >= i16 : j <= i16) ? a[r] * (w * p.m_p) : 0.0f;
+                            s[r] = (REV ? j >= i16 : j <= i16) ? sdm_decayed(w * p.m_p, a[r]) : 0.0f;
                         }
                     } else {
                         const float ot = (REV ? gates.down : gates.up)[16 * it + i16] * (p.m_p * gates.tau[4 * it + jt]);
                         const f32x4 d = *reinterpret_cast<const f32x4*>(&(REV ? gates.up : gates.down)[16 * jt + 4 * qd]);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) s[r] = a[r] * (ot * d[r]);
+                        for (int r = 0; r < 4; ++r) s[r] = sdm_decayed(ot * d[r], a[r]);
                     }
                 }
                 if constexpr (sizeof(T) == 2) {
@@ -634,10 +719,22 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                 for (int it = 0; it < 4; ++it) __asm__ volatile("" : "+v"(wx[it].w));
             }
             if (more) fill_x(next, tid);
-            // The chunk's own tokens.
+            // The chunk's own tokens. A tile product multiplies z_j by the scores that are 0 as well (tokens before j, and those
+            // that a reset cuts off), so what is not finite in the wave's columns of z is taken out of it, and put
+            // where it belongs afterwards.
+            Frag<T> zf[2];
+#pragma unroll
+            for (int jb = 0; jb < 2; ++jb) zf[jb] = col_frag<VD, 4>(zc, jb, n0, i16, qd);
+            const bool stray = __ballot(not_finite(zf[0], zf[1])) != 0;
+            if (__builtin_expect(stray, 0)) {
+#pragma unroll
+                for (int jb = 0; jb < 2; ++jb) {
+                    Frag<T> mark;
+                    split_finite(zf[jb], zf[jb], mark);
+                }
+            }
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb) {
-                const Frag<T> zf = col_frag<VD, 4>(zc, jb, n0, i16, qd);
 #pragma unroll
                 for (int s = P2 - 1; s >= 0; --s) {
 #pragma unroll
@@ -645,10 +742,11 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                         if (Pairs<REV>::kJb[pr] != jb) continue;
                         Frag<T> pf;
                         __builtin_memcpy(&pf, scores + ((pr * P2 + s) * kWave + here) * kScoreWords, sizeof(pf));
-                        mma(zf, pf, O[Pairs<REV>::kIt[pr]]);
+                        mma(zf[jb], pf, O[Pairs<REV>::kIt[pr]]);
                     }
                 }
             }
+            if (__builtin_expect(stray, 0)) stray_values<T, VD, REV>(zc, gates, n0, i16, qd, O);
             // Results.
             if constexpr (DOT) {
 #pragma unroll
@@ -693,7 +791,16 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
             decay += gates.sum;
         }
 
-        // The state.
+        // The state. Tokens that a later one's reset cuts off from it have a factor of 0; their rows of y are cleared, since 0
+        // times what is not finite there would not be 0.
+        if (__builtin_expect(__builtin_amdgcn_readfirstlane(OUT ? gates.gone & gates.odd : gates.gone), 0)) {
+            constexpr int kPieces = KD * static_cast<int>(sizeof(T)) / 16;
+            for (int at = tid; at < kL * kPieces; at += kThreads) {
+                const int row = at / kPieces;
+                if (gates.u[row] == 0.0f) *reinterpret_cast<u32x4*>(piece<T, KD>(yc, row, at % kPieces)) = u32x4{0, 0, 0, 0};
+            }
+            lds_barrier();
+        }
         const float all = gates.all;
 #pragma unroll
         for (int d = 0; d < KT; ++d) S[d] = decayed(all, S[d]);
@@ -706,7 +813,10 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                 float z[8];
                 widen8(col_frag<VD, 4>(zc, jb, n0, i16, qd), z);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) { z[r] *= ua[r]; z[4 + r] *= ub[r]; }
+                for (int r = 0; r < 4; ++r) {
+                    z[r] = sdm_decayed(ua[r], z[r]);
+                    z[4 + r] = sdm_decayed(ub[r], z[4 + r]);
+                }
                 cut(z, zp);
             }
 #pragma unroll

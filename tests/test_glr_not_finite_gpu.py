@@ -93,3 +93,43 @@ def test_a_reset_in_a_step(dtype, dv):
     out = sdm.glr_step(*one, pool, slots=slots)
     assert torch.isfinite(want).all() and torch.equal(out, want) and torch.equal(pool[slots.long()], want_state)
     assert not torch.isfinite(pool[2]).any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H", SHAPES)
+@pytest.mark.parametrize("what", ["q", "k", "v", "d_o"])
+@pytest.mark.parametrize("resets", [False, True])
+def test_values_reach_only_what_they_are_part_of(dtype, B, T, H, what, resets):
+    """NaN and infinities at single tokens and columns: no earlier token (no later one in the gradients that run backwards),
+    no token on the other side of a reset, and no column or head of its own sees them."""
+    say("glr values that are not finite", dtype, B, T, H, what, resets)
+    # Gates near 0: no decay of a row's whole length falls below float32's smallest value.
+    x = make(B, T, H, max(1, H // 2), 16, 24, DT[dtype], gate=6.0)
+    heads = x[what].shape[2]
+    for b, t, h, c, val in ((0, T // 2, 0, 3, NAN), (0, min(T - 1, 58), 0, 15, INF), (B - 1, min(T - 1, 20), heads - 1, 0, -INF),
+                            (B // 2, min(T - 1, 177), heads // 2, 7, NAN), (B // 2, min(T - 1, 178), heads // 2, 8, INF)):
+        x[what][b, t, h, c] = val
+    if resets:
+        for t in (T // 2 - 1, T // 2 + 1, 19, 22, 50, 178):
+            if t < T:
+                x["g"][:, t] = -INF
+    wo, w = check(x, DT[dtype], 0.3)
+    reached = wo if what in ("q", "k", "v") else w["dq"]
+    assert 0 < np.isfinite(reached).sum() < reached.size
+
+
+def test_every_token_of_a_chunk():
+    """One infinity in v, at every place of two chunks in turn: outputs before it as without it, bit for bit."""
+    T, dk, dv = 128, 32, 40
+    x = cuda(make(1, T, 1, 1, dk, dv, torch.bfloat16, state=False))
+    q, k, g = (x[n].expand(T, *x[n].shape[1:]) for n in ("q", "k", "g"))
+    v = x["v"].repeat(T, 1, 1, 1)
+    want, _ = sdm.glr_forward(q, k, v, g)
+    at = torch.arange(T, device="cuda")
+    v[at, at, 0, at % dv] = INF
+    o, last = sdm.glr_forward(q, k, v, g)
+    for t in range(T):
+        c = t % dv
+        assert torch.equal(o[t, :t], want[t, :t]) and not torch.isfinite(o[t, t:, 0, c]).any(), t
+        rest = [n for n in range(dv) if n != c]
+        assert torch.equal(o[t][..., rest], want[t][..., rest]) and not torch.isfinite(last[t, 0, :, c]).any(), t
