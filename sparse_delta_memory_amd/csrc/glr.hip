@@ -38,6 +38,12 @@
 // chunk (one wave, one token per lane) and only differences of a chunk's sums are rounded to float32, so
 // neither long rows nor a reset (a gate of -infinity counts as -10000) cost digits.
 //
+// What is not finite reaches what it is part of by the recurrence and nothing else: no token before it, nothing past a
+// reset, although a tile product multiplies it by zeros there. Factors of 0 are applied by a multiplication
+// whose 0 times anything is 0; z is looked over before its product with the scores, and a chunk with such a value
+// goes another way; rows of y that a reset cuts off from the state are cleared. Looking costs 3 to 5 % (8 x 4096
+// tokens x 16 heads of 128, forward 213 -> 220 us, backward 706 -> 720).
+//
 // Segments. With few streams and heads the time axis is cut: a first kernel sums each segment's own
 // state, and the main kernel starts every segment from the state before it, made up of the start and the
 // segments before (by itself when they are few, else a kernel chains them).
@@ -195,8 +201,8 @@ __device__ __forceinline__ void widen8(const Frag<float>& f, float (&x)[8]) {
     for (int e = 0; e < 8; ++e) x[e] = f.v[e];
 }
 
-// Whether any value of the wave's two operands is infinity or NaN: 0 times a finite value is 0. For bfloat16 a matrix product
-// does the 16 multiplications (four vector instructions beside it; 20 by comparisons of the exponents).
+// Whether the wave's two operands hold an infinity or NaN (seen by some lane): 0 times a finite value is 0. For bfloat16 a
+// matrix product does the multiplications (4 vector instructions beside it; comparing the exponents takes 20).
 __device__ __forceinline__ bool not_finite(const Frag<bf16_t>& f, const Frag<bf16_t>& g) {
     f32x4 c = {0, 0, 0, 0};
     const Frag<bf16_t> zero{u32x4{0, 0, 0, 0}};
