@@ -78,7 +78,7 @@ def glr_backward(d_o, q, k, v, g, scale, state=None, d_last=None, lens=None):
                 part[t] += np.abs(kk) @ (N @ np.abs(vv))
                 r["dv"][b, t, h] = kk @ R
                 m["dv"][b, t, h] = np.abs(kk) @ N
-                r["dg"][b, t, h] = a * (before[t] * R).sum()
+                r["dg"][b, t, h] = a * (before[t] * R).sum() if a > 0 else 0.0
                 rest += part[t]
                 m["dg"][b, t, h] = rest
                 R, N = (a * R, a * N) if a > 0 else (np.zeros_like(R), np.zeros_like(N))

@@ -13,7 +13,7 @@
 // R the gradient of the state. A gate scales all that reaches t or a later token from before t, so
 //     dg_t = sum_{s >= t} (q_s . dq_s - k_s . dk_s) + <S_T, R_T>;
 // q . dq and k . dk come from the float32 results before they are rounded, and the sums start afresh at
-// every segment (below) from <S, R> there, so that what cancels is never longer than a segment.
+// every segment (below) from <S, R> there and at every reset from 0, so that what cancels is never longer than a segment.
 //
 // Layout. A block owns one (stream, head, segment); each of its waves owns 16 columns of z, out and the
 // state (8 waves for widths past 64, else 4) and keeps its part of the state in registers over all chunks
@@ -946,35 +946,113 @@ __global__ __launch_bounds__(256) void glr_chain_kernel(float* states, const flo
     }
 }
 
-// dg: one wave per (stream, head, segment), 256 tokens at a time from the segment's end, in float64.
-__global__ __launch_bounds__(256) void glr_gate_grad_kernel(const float* dq_dot, const float* dk_dot, const float* cross,
-                                                            const int32_t* lens, float* dg, int T, int H, int nseg, int seg,
-                                                            int64_t waves) {
+// The lanes [from, to) of a wave's 64 tokens, in pieces that no reset cuts: per piece its inclusive sums of x, which start
+// afresh in each. cuts: the lanes that start a piece of their own. f(piece's first lane, its end, the lane's sum).
+template <typename F>
+__device__ __forceinline__ void pieces(uint64_t cuts, double x, int lane, F f) {
+    for (int from = 0; from < kWave;) {
+        const uint64_t rest = from + 1 < kWave ? cuts >> (from + 1) << (from + 1) : 0;
+        const int to = rest != 0 ? __builtin_ctzll(rest) : kWave;
+        f(from, to, scan_d(lane >= from && lane < to ? x : 0.0));
+        from = to;
+    }
+}
+
+struct GateGrad {
+    const float *dq, *dk;     // [B H, T] the row dots q . dq and k . dk
+    const float* cross;       // [B H, nseg]
+    const float* g;
+    int64_t g_b, g_t, g_h;
+    const int32_t* lens;
+    const float *state, *d_state;   // [B H, one] or NULL
+    int64_t one;
+    float* dg;
+    int T, H, nseg, seg;
+    int64_t waves;
+};
+
+// dg: one wave per (stream, head, segment), 256 tokens at a time from the segment's end, in float64. A token that
+// resets has a gradient of 0, and with it the sums start afresh: nothing of a later sequence, be it large
+// or not finite, is in an earlier one's. Where the sum from the end is not finite, that from the front,
+//     dg_t = dg_{t0} - sum_{t0 <= s < t} (q_s . dq_s - k_s . dk_s),
+// may be, since what makes q . dq infinite or NaN is a key or value behind t; dg_{t0} is <S, R> of the segment before,
+// or <state, its gradient>.
+__global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
     const int64_t id = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kWave;
-    if (id >= waves) return;
+    if (id >= p.waves) return;
     constexpr int kU = 4;
-    const int lane = static_cast<int>(lane_id());
-    const int si = static_cast<int>(id % nseg);
-    const int64_t bh = id / nseg, b = bh / H, h = bh - b * H;
-    int len = lens != nullptr ? lens[b] : T;
+    const int lane = static_cast<int>(lane_id()), T = p.T;
+    const int si = static_cast<int>(id % p.nseg);
+    const int64_t bh = id / p.nseg, b = bh / p.H, h = bh - b * p.H;
+    int len = p.lens != nullptr ? p.lens[b] : T;
     len = len < 0 ? 0 : len > T ? T : len;
-    const int t_lo = si * seg, t_hi = min(T, t_lo + seg);
-    double carry = cross[bh * nseg + si];
+    const int t_lo = si * p.seg, t_hi = min(T, t_lo + p.seg);
+    const float* gates = p.g + b * p.g_b + h * p.g_h;
+    float* out = p.dg + b * T * p.H + h;
+    double carry = p.cross[bh * p.nseg + si];
+    bool lost = false;
     for (int t1 = t_hi; t1 > t_lo; t1 -= kU * kWave) {   // lane l takes tokens t1 - 1 - l - 64 u
-        float q[kU], k[kU];
+        float q[kU], k[kU], g[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int64_t at = bh * T + max(t1 - 1 - lane - u * kWave, t_lo);
-            q[u] = dq_dot[at];
-            k[u] = dk_dot[at];
+            const int t = max(t1 - 1 - lane - u * kWave, t_lo);
+            q[u] = p.dq[bh * T + t];
+            k[u] = p.dk[bh * T + t];
+            g[u] = t < len ? gates[t * p.g_t] : 0.0f;
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
             const int t = t1 - 1 - lane - u * kWave;
-            const double x = scan_d(t >= t_lo ? static_cast<double>(q[u]) - static_cast<double>(k[u]) : 0.0);
-            if (t >= t_lo) dg[(b * T + t) * H + h] = t < len ? static_cast<float>(carry + x) : 0.0f;
-            carry += uniform_d(x, kWave - 1);
+            const double x = t >= t_lo ? static_cast<double>(q[u]) - static_cast<double>(k[u]) : 0.0;
+            const uint64_t resets = __ballot(t >= t_lo && g[u] <= kGateMin);
+            double y;
+            if (resets == 0) {
+                const double sum = scan_d(x);
+                y = carry + sum;
+                carry += uniform_d(sum, kWave - 1);
+            } else {
+                // A piece ends with the token that resets, the first one in time: the next starts behind it, from 0.
+                y = 0.0;
+                pieces(resets << 1, x, lane, [&](int from, int to, double sum) {
+                    if (lane >= from && lane < to) y = carry + sum;
+                    carry = to < kWave || (resets >> (kWave - 1)) != 0 ? 0.0 : carry + uniform_d(sum, kWave - 1);
+                });
+                if ((resets >> lane) & 1) y = 0.0;
+            }
+            const float d = t < len ? static_cast<float>(y) : 0.0f;
+            lost |= t >= t_lo && !(fabsf(d) < INFINITY);
+            if (t >= t_lo) out[static_cast<int64_t>(t) * p.H] = d;
         }
+    }
+    if (__builtin_expect(__ballot(lost) == 0, 1)) return;
+    double start;
+    if (si > 0) {
+        start = p.cross[bh * p.nseg + si - 1];
+    } else if (p.d_state != nullptr) {
+        float x = 0.0f;
+        for (int64_t e = lane; e < p.one; e += kWave)
+            x = fmaf(p.state != nullptr ? p.state[bh * p.one + e] : 0.0f, p.d_state[bh * p.one + e], x);
+        start = group_sum<kWave>(x);
+    } else {
+        return;
+    }
+    __threadfence_block();   // what the lanes above stored is there for the others
+    const int end = min(t_hi, len);
+    for (int t0 = t_lo; t0 < end; t0 += kWave) {
+        const int t = t0 + lane, at = min(t, end - 1);
+        const double x = t < end ? static_cast<double>(p.dk[bh * T + at]) - static_cast<double>(p.dq[bh * T + at]) : 0.0;
+        const uint64_t resets = __ballot(t < end && gates[at * p.g_t] <= kGateMin);
+        double y = 0.0;
+        if (resets & 1) start = 0.0;
+        pieces(resets, x, lane, [&](int from, int to, double sum) {   // a piece starts with the token that resets, from 0
+            if (from > 0) start = 0.0;
+            const double before = dpp_d<0x138, 0xF>(sum);   // wave_shr:1: the sum of the tokens before the lane's
+            if (lane >= from && lane < to) y = start + (lane == from ? 0.0 : before);
+            start += uniform_d(sum, kWave - 1);
+        });
+        const float d = static_cast<float>(y);
+        float* o = out + static_cast<int64_t>(at) * p.H;
+        if (t < end && fabsf(d) < INFINITY && !(fabsf(*o) < INFINITY)) *o = d;
     }
 }
 
@@ -1360,8 +1438,9 @@ hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipS
     }
     if (io->T == 0) return hipSuccess;
     const int64_t waves = bh * sp.nseg;
-    glr_gate_grad_kernel<<<static_cast<unsigned>((waves * kWave + 255) / 256), 256, 0, st>>>(dqd, dkd, cross, io->lens, g->dg, io->T, io->H,
-                                                                                             sp.nseg, sp.seg, waves);
+    const GateGrad gg{dqd, dkd, cross, io->g, io->g_b, io->g_t, io->g_h, io->lens, io->state, g->d_state, one, g->dg, io->T, io->H,
+                      sp.nseg, sp.seg, waves};
+    glr_gate_grad_kernel<<<static_cast<unsigned>((waves * kWave + 255) / 256), 256, 0, st>>>(gg);
     if ((e = hipGetLastError()) != hipSuccess || !fold) return e;
     const int64_t total = static_cast<int64_t>(io->B) * io->T * io->Hk * io->dk;
     const int64_t need = (total + 255) / 256;

@@ -51,8 +51,8 @@ def check(x, dtype, scale, grads=("dq", "dk", "dv", "dstate")):
     return wo, w
 
 
-# (streams, tokens, heads): one chunk per segment, joined by each block or chained; rows of four chunks and no segments.
-SHAPES = [(1, 60, 2), (1, 200, 1), (1, 700, 1), (64, 200, 4)]
+# (streams, tokens, heads): one chunk per segment, joined by each block or chained; rows of three chunks and no segments.
+SHAPES = [(1, 60, 2), (1, 200, 1), (1, 700, 1), (128, 140, 2)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -133,3 +133,58 @@ def test_every_token_of_a_chunk():
         assert torch.equal(o[t, :t], want[t, :t]) and not torch.isfinite(o[t, t:, 0, c]).any(), t
         rest = [n for n in range(dv) if n != c]
         assert torch.equal(o[t][..., rest], want[t][..., rest]) and not torch.isfinite(last[t, 0, :, c]).any(), t
+
+
+def gate_gradients(x, dtype, scale=0.3):
+    """dg of the kernels and the oracle's, and the magnitude of a row's whole sum, from finite values in place of the others."""
+    d, h = cuda(x), {k: host(t) for k, t in x.items()}
+    r = sdm.glr_backward(*(d[k] for k in ("d_o", "q", "k", "v", "g")), scale=scale, state=d["state"], d_last=d["d_last"], lens=d["lens"])
+    args = lambda z: (*(z[k] for k in ("d_o", "q", "k", "v", "g")), scale, z["state"], z["d_last"], z["lens"])  # noqa: E731
+    with np.errstate(invalid="ignore", over="ignore"):
+        w, _ = M.glr_backward(*args(h))
+        clean = {n: t if t is None or n in ("g", "lens") else np.where(np.isfinite(t), t, 1.0) for n, t in h.items()}
+        _, m = M.glr_backward(*args(clean))
+    return r["dg"], w["dg"], np.broadcast_to(m["dg"][:, :1], w["dg"].shape)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,H", SHAPES)
+@pytest.mark.parametrize("what", ["q", "k", "v", "d_o", "state", "d_last"])
+@pytest.mark.parametrize("resets", [False, True])
+def test_gate_gradients(dtype, B, T, H, what, resets):
+    """A gate's gradient is made of the states before it and what comes from behind it: a key or value that is not finite
+    leaves the gates up to it alone, a query or gradient those behind it, a reset both sides."""
+    say("glr gate gradients, not finite", dtype, B, T, H, what, resets)
+    x = make(B, T, H, max(1, H // 2), 16, 24, DT[dtype], gate=6.0, lens=[T - 3 * (b % 4) for b in range(B)])
+    if what in ("state", "d_last"):
+        x[what][0, 0, 2, 3] = NAN
+        x[what][B - 1, H - 1, 0, 5] = INF
+    else:
+        x[what][0, T // 2, 0, 3] = NAN
+        x[what][B - 1, min(T - 20, 70), -1, 1] = -INF
+    if resets:
+        for t in (T // 2 - 9, T // 2 - 8, T // 2 + 1, 3, 64, 150):
+            if t < T:
+                x["g"][:, t] = -INF
+    got, want, mag = gate_gradients(x, DT[dtype])
+    if resets:
+        assert (got[torch.isneginf(x["g"]).cuda()] == 0).all()
+    same("dg", got, want, mag, 16 + 24 + 96 + T // 64, False)
+    if what not in ("state", "d_last"):
+        assert np.isfinite(want).any(1).all()
+
+
+@pytest.mark.parametrize("T", [60, 200, 1000])
+def test_gate_gradients_of_packed_sequences(T):
+    """Gates before a reset have the gradients that they have without the sequence behind it, however large that is."""
+    x = make(2, T, 2, 1, 16, 24, torch.float32, gate=6.0)
+    x["g"][:, T // 2] = -INF
+    x["d_last"] = x["d_last"] * 0
+    d = cuda(x)
+    run = lambda n: sdm.glr_backward(*(d[k][:, :n] for k in ("d_o", "q", "k", "v", "g")), state=d["state"], d_last=d["d_last"])["dg"]  # noqa: E731
+    alone = run(T // 2)
+    for k in ("q", "v", "d_o"):
+        d[k][:, T // 2:] *= 1e4
+    both = run(T)
+    assert (both[:, T // 2] == 0).all()
+    assert torch.allclose(both[:, :T // 2], alone, rtol=0, atol=1e-5 * float(alone.abs().max()))
