@@ -982,8 +982,9 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
     if (id >= p.waves) return;
     constexpr int kU = 4;
     const int lane = static_cast<int>(lane_id()), T = p.T;
-    const int si = static_cast<int>(id % p.nseg);
-    const int64_t bh = id / p.nseg, b = bh / p.H, h = bh - b * p.H;
+    // Neighbouring waves take neighbouring heads, whose gates and results share cache lines.
+    const int64_t h = id % p.H, bs = id / p.H, b = bs / p.nseg, bh = b * p.H + h;
+    const int si = static_cast<int>(bs - b * p.nseg);
     int len = p.lens != nullptr ? p.lens[b] : T;
     len = len < 0 ? 0 : len > T ? T : len;
     const int t_lo = si * p.seg, t_hi = min(T, t_lo + p.seg);
