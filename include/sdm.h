@@ -593,11 +593,11 @@ typedef struct sdm_glr_io {
 /*
  * Per stream and head, from S = state:  S_t = exp(g_t) S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t.
  * States and sums are float32; of bfloat16 inputs every product is exact, and a float32 factor (a decayed
- * score, a state) enters a matrix product as two or three bfloat16 parts. A gate that resets, and gates whose
- * product is 0 in float32, leave nothing of the state before them, finite or not (a state need not be
- * initialised where the first token resets it). A value of q, k or v that is not finite makes what the
- * recurrence takes it into infinity or NaN, and nothing else: no earlier token, no other column, stream or
- * head, nothing past a reset. Requires B * H <= 2^20, T <= 2^30, B * T * H <= 2^31 - 1.
+ * score, a state) enters a matrix product as three bfloat16 parts, all its 24 bits. A gate that resets, and
+ * gates whose product is 0 in float32, leave nothing of the state before them, finite or not (a state need
+ * not be initialised where the first token resets it). A value of q, k or v that is not finite makes what the
+ * recurrence takes it into infinity or NaN and nothing else: no earlier token, stream or head, nothing past a
+ * reset. Requires B * H <= 2^20, T <= 2^30, B * T * H <= 2^31 - 1.
  */
 sdm_status sdm_glr_forward(const sdm_glr_io* io, hipStream_t st);
 size_t sdm_glr_workspace(const sdm_glr_io* io, int32_t backward);

@@ -31,10 +31,9 @@
 // held in registers and one block: 253 us; 151 so).
 //
 // Numbers. Products of bfloat16 inputs are exact; a float32 factor (decayed score, state, decayed z) is
-// cut into bfloat16 parts by truncation and multiplied part by part: three parts hold all 24 bits. The
-// state's update and everything a dg sums takes three; o and dv are rounded to bfloat16 in the end, so
-// their scores and the state's use take two (16 bits, a 2^-16 relative error beside the 2^-9 of the
-// result). float32 inputs go through the float32 matrix instructions. Gates are summed in float64 per
+// cut into three bfloat16 parts by truncation, which hold all 24 bits, and multiplied part by part. (For o and dv,
+// which are rounded to bfloat16 in the end, two parts of the scores and of the state that meets x take 6 % less,
+// 8 x 4096 x 16 forward 218 against 233 us, but sums that cancel show their error of up to 2^-15.) float32 inputs go through the float32 matrix instructions. Gates are summed in float64 per
 // chunk (one wave, one token per lane) and only differences of a chunk's sums are rounded to float32, so
 // neither long rows nor a reset (a gate of -infinity counts as -10000) cost digits.
 //
@@ -125,8 +124,8 @@ __device__ __forceinline__ void cut(const float (&x)[8], Parts<float, NS>& o) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) o.p[0].v[e] = x[e];
 }
-template <typename T, int NS>
-constexpr int kParts = sizeof(T) == 4 ? 1 : NS;
+template <typename T>
+constexpr int kParts = sizeof(T) == 4 ? 1 : 3;
 
 // LDS tiles [64][W]: the 16-byte piece c of a row lies at piece c ^ twist(row), which spreads 16 rows' reads of one piece
 // and 4 rows' transposed reads over the banks. Counted, a row read still takes 8 cycles (4 at best: the lanes LDS serves
@@ -504,13 +503,13 @@ __device__ __forceinline__ void stray_values(T* zc, const Gates& gates, int n0, 
     }
 }
 
-// KD, VD: padded widths of x / y and of z (64 or 128). NS: parts of scores and of the state where it meets x.
+// KD, VD: padded widths of x / y and of z (64 or 128).
 // OUT: results (else the segments' own states alone). DOT: row dots of the results, and <S, R>. FOLD: float32 results
 // of bfloat16 inputs.
-template <typename T, int KD, int VD, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
+template <typename T, int KD, int VD, bool REV, bool OUT, bool DOT, bool FOLD>
 __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(GlrPass p) {
     constexpr int KB = KD / 32, KT = KD / 16, kThreads = 4 * VD, kWaves = VD / 16;
-    constexpr int P2 = kParts<T, NS>, P3 = kParts<T, 3>;
+    constexpr int NP = kParts<T>;
     constexpr bool F32 = sizeof(T) == 4 || FOLD;
     // Without results two chunks' tiles fit beside each other (in bfloat16) and the next chunk's loads run under a chunk's
     // products; with them x's tile is free half way through a chunk, y's and z's at its end.
@@ -520,8 +519,8 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
     T* xt = reinterpret_cast<T*>(lds);
     T* yt = xt + (OUT ? kL * KD : 0);
     T* zt = yt + kBufs * kL * KD;
-    uint32_t* scores = reinterpret_cast<uint32_t*>(zt + kBufs * kL * VD);   // [6][P2][64 lanes][kScoreWords]
-    Gates* gate_at = reinterpret_cast<Gates*>(scores + (OUT ? 6 * P2 * kWave * kScoreWords : 0));   // two chunks
+    uint32_t* scores = reinterpret_cast<uint32_t*>(zt + kBufs * kL * VD);   // [6][NP][64 lanes][kScoreWords]
+    Gates* gate_at = reinterpret_cast<Gates*>(scores + (OUT ? 6 * NP * kWave * kScoreWords : 0));   // two chunks
     float* dots = reinterpret_cast<float*>(gate_at + 2);   // [waves][64]
 
     const int nblk = OUT ? p.nseg : p.nseg - 1;   // the last segment's own state (in the pass's direction) is not needed
@@ -686,8 +685,8 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                 }
                 if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                    for (int k = 0; k < P2; ++k) {
-                        *reinterpret_cast<u32x2*>(scores + ((pr * P2 + k) * kWave + here) * kScoreWords + 2 * half) =
+                    for (int k = 0; k < NP; ++k) {
+                        *reinterpret_cast<u32x2*>(scores + ((pr * NP + k) * kWave + here) * kScoreWords + 2 * half) =
                             u32x2{__builtin_amdgcn_perm(__float_as_uint(s[1]), __float_as_uint(s[0]), 0x07060302u),
                                   __builtin_amdgcn_perm(__float_as_uint(s[3]), __float_as_uint(s[2]), 0x07060302u)};
 #pragma unroll
@@ -703,7 +702,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
             for (int it = 0; it < 4; ++it) O[it] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                Parts<T, P2> sp;
+                Parts<T, NP> sp;
                 Frag<T> xf[4];
 #pragma unroll
                 for (int it = 0; it < 4; ++it) xf[it] = row_frag<KD>(xt, 16 * it + i16, kb, qd);
@@ -712,7 +711,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
                 for (int r = 0; r < 4; ++r) { s[r] = S[2 * kb][r]; s[4 + r] = S[2 * kb + 1][r]; }
                 cut(s, sp);
 #pragma unroll
-                for (int k = P2 - 1; k >= 0; --k) {
+                for (int k = NP - 1; k >= 0; --k) {
 #pragma unroll
                     for (int it = 0; it < 4; ++it) mma(sp.p[k], xf[it], O[it]);
                 }
@@ -742,12 +741,12 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
             for (int jb = 0; jb < 2; ++jb) {
 #pragma unroll
-                for (int s = P2 - 1; s >= 0; --s) {
+                for (int s = NP - 1; s >= 0; --s) {
 #pragma unroll
                     for (int pr = 0; pr < 6; ++pr) {
                         if (Pairs<REV>::kJb[pr] != jb) continue;
                         Frag<T> pf;
-                        __builtin_memcpy(&pf, scores + ((pr * P2 + s) * kWave + here) * kScoreWords, sizeof(pf));
+                        __builtin_memcpy(&pf, scores + ((pr * NP + s) * kWave + here) * kScoreWords, sizeof(pf));
                         mma(zf[jb], pf, O[Pairs<REV>::kIt[pr]]);
                     }
                 }
@@ -812,7 +811,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
         for (int d = 0; d < KT; ++d) S[d] = decayed(all, S[d]);
 #pragma unroll
         for (int jb = 0; jb < 2; ++jb) {
-            Parts<T, P3> zp;
+            Parts<T, NP> zp;
             {
                 const f32x4 ua = *reinterpret_cast<const f32x4*>(&gates.u[32 * jb + 4 * qd]);
                 const f32x4 ub = *reinterpret_cast<const f32x4*>(&gates.u[32 * jb + 16 + 4 * qd]);
@@ -831,7 +830,7 @@ __global__ __launch_bounds__(4 * VD, sizeof(T) == 2 ? 4 : 1) void glr_kernel(Glr
 #pragma unroll
                 for (int e = 0; e < 4; ++e) yf[e] = col_frag<KD, 8>(yc, jb, 32 * ((d + e) >> 1) + 4 * (e & 1), i16, qd);
 #pragma unroll
-                for (int s = P3 - 1; s >= 0; --s) {
+                for (int s = NP - 1; s >= 0; --s) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) mma(yf[e], zp.p[s], S[d + e]);
                 }
@@ -1232,64 +1231,63 @@ GlrLayout glr_layout(const sdm_glr_io* io, bool backward) {
 }
 
 template <typename T, int KD, int VD>
-size_t glr_lds(bool out, int ns) {
-    const size_t parts = sizeof(T) == 4 ? 1 : ns;
+size_t glr_lds(bool out) {
     const size_t tiles = out ? 2 * KD + VD : (sizeof(T) == 2 ? 2 : 1) * (KD + VD);
-    return kL * tiles * sizeof(T) + (out ? 6 * parts * kWave * 8 * sizeof(T) : 0) + 2 * sizeof(Gates) +
+    return kL * tiles * sizeof(T) + (out ? 6 * kParts<T> * kWave * 8 * sizeof(T) : 0) + 2 * sizeof(Gates) +
            VD / 16 * kL * sizeof(float);
 }
 
-template <typename T, int KD, int VD, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
+template <typename T, int KD, int VD, bool REV, bool OUT, bool DOT, bool FOLD>
 hipError_t glr_go3(const GlrPass& p, hipStream_t st) {
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.B) * p.H * (OUT ? p.nseg : p.nseg - 1));
-    glr_kernel<T, KD, VD, REV, OUT, NS, DOT, FOLD><<<grid, 4 * VD, glr_lds<T, KD, VD>(OUT, NS), st>>>(p);
+    glr_kernel<T, KD, VD, REV, OUT, DOT, FOLD><<<grid, 4 * VD, glr_lds<T, KD, VD>(OUT), st>>>(p);
     return hipGetLastError();
 }
-template <typename T, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
+template <typename T, bool REV, bool OUT, bool DOT, bool FOLD>
 hipError_t glr_go2(const GlrPass& p, hipStream_t st) {
     const int kd = padded(p.y.width), vd = padded(p.z.width);
-    if (kd == 64) return vd == 64 ? glr_go3<T, 64, 64, REV, OUT, NS, DOT, FOLD>(p, st) : glr_go3<T, 64, 128, REV, OUT, NS, DOT, FOLD>(p, st);
-    return vd == 64 ? glr_go3<T, 128, 64, REV, OUT, NS, DOT, FOLD>(p, st) : glr_go3<T, 128, 128, REV, OUT, NS, DOT, FOLD>(p, st);
+    if (kd == 64) return vd == 64 ? glr_go3<T, 64, 64, REV, OUT, DOT, FOLD>(p, st) : glr_go3<T, 64, 128, REV, OUT, DOT, FOLD>(p, st);
+    return vd == 64 ? glr_go3<T, 128, 64, REV, OUT, DOT, FOLD>(p, st) : glr_go3<T, 128, 128, REV, OUT, DOT, FOLD>(p, st);
 }
-template <bool REV, bool OUT, int NS, bool DOT>
+template <bool REV, bool OUT, bool DOT>
 hipError_t glr_go(const GlrPass& p, int dtype, hipStream_t st) {
-    // float32 factors are not cut and float32 results not narrowed: one instance whatever NS and out_f32.
-    if (dtype != SDM_BF16) return glr_go2<float, REV, OUT, 3, DOT, false>(p, st);
+    // float32 results are not narrowed: one instance whatever out_f32.
+    if (dtype != SDM_BF16) return glr_go2<float, REV, OUT, DOT, false>(p, st);
     if constexpr (DOT) {
-        if (p.out_f32) return glr_go2<bf16_t, REV, OUT, NS, DOT, true>(p, st);
+        if (p.out_f32) return glr_go2<bf16_t, REV, OUT, DOT, true>(p, st);
     }
-    return glr_go2<bf16_t, REV, OUT, NS, DOT, false>(p, st);
+    return glr_go2<bf16_t, REV, OUT, DOT, false>(p, st);
 }
 
 // The segments' own states (y z^T), then chained when there are many.
 template <bool REV>
 hipError_t seg_states(GlrPass p, int dtype, int64_t one, int64_t bh, hipStream_t st) {
-    hipError_t e = glr_go<REV, false, 3, false>(p, dtype, st);
+    hipError_t e = glr_go<REV, false, false>(p, dtype, st);
     if (e != hipSuccess || !p.chained) return e;
     const int64_t total = bh * one;
     glr_chain_kernel<REV><<<static_cast<unsigned>((total + 255) / 256), 256, 0, st>>>(p.segs, p.decays, p.start, p.nseg, one, total);
     return hipGetLastError();
 }
 
-template <typename T, bool REV, bool OUT, int NS, bool DOT, bool FOLD>
+template <typename T, bool REV, bool OUT, bool DOT, bool FOLD>
 void list(const void** all, int& n) {
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 64, REV, OUT, NS, DOT, FOLD>);
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 128, REV, OUT, NS, DOT, FOLD>);
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 64, REV, OUT, NS, DOT, FOLD>);
-    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 128, REV, OUT, NS, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 64, REV, OUT, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 64, 128, REV, OUT, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 64, REV, OUT, DOT, FOLD>);
+    all[n++] = reinterpret_cast<const void*>(&glr_kernel<T, 128, 128, REV, OUT, DOT, FOLD>);
 }
-template <typename T, int NS>
+template <typename T>
 void list_type(const void** all, int& n) {
-    list<T, false, true, NS, false, false>(all, n);   // o
-    list<T, true, true, NS, false, false>(all, n);    // dv
-    list<T, false, true, 3, true, false>(all, n);     // dq
-    list<T, true, true, 3, true, false>(all, n);      // dk
+    list<T, false, true, false, false>(all, n);   // o
+    list<T, true, true, false, false>(all, n);    // dv
+    list<T, false, true, true, false>(all, n);     // dq
+    list<T, true, true, true, false>(all, n);      // dk
     if constexpr (sizeof(T) == 2) {
-        list<T, false, true, 3, true, true>(all, n);
-        list<T, true, true, 3, true, true>(all, n);
+        list<T, false, true, true, true>(all, n);
+        list<T, true, true, true, true>(all, n);
     }
-    list<T, false, false, 3, false, false>(all, n);
-    list<T, true, false, 3, false, false>(all, n);
+    list<T, false, false, false, false>(all, n);
+    list<T, true, false, false, false>(all, n);
 }
 
 // A pass over io's shape.
@@ -1315,8 +1313,8 @@ GlrPass base_pass(const sdm_glr_io* io, const SegPlan& sp) {
 int glr_lds_kernels(const void** fns, int cap) {
     const void* all[96];
     int n = 0;
-    list_type<bf16_t, 2>(all, n);
-    list_type<float, 3>(all, n);
+    list_type<bf16_t>(all, n);
+    list_type<float>(all, n);
     int k = 0;
     for (; k < n && k < cap; ++k) fns[k] = all[k];
     return k;
@@ -1352,7 +1350,7 @@ hipError_t glr_forward_launch(const sdm_glr_io* io, hipStream_t st) {
     p.o_t = io->o_t;
     p.o_h = io->o_h;
     p.out_wide = reinterpret_cast<uintptr_t>(io->o) % (4 * es) == 0 && io->o_b % 4 == 0 && io->o_t % 4 == 0 && io->o_h % 4 == 0 && io->dv % 4 == 0;
-    return glr_go<false, true, 2, false>(p, io->dtype, st);
+    return glr_go<false, true, false>(p, io->dtype, st);
 }
 
 hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipStream_t st) {
@@ -1410,7 +1408,7 @@ hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipS
         p.r_start = bwd.start;
         p.r_segs = bwd.segs;
         p.r_decays = bwd.decays;
-        if ((e = glr_go<false, true, 3, true>(p, io->dtype, st)) != hipSuccess) return e;
+        if ((e = glr_go<false, true, true>(p, io->dtype, st)) != hipSuccess) return e;
     }
     {   // dk
         GlrPass p = bwd;
@@ -1421,7 +1419,7 @@ hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipS
         p.m_p = io->scale;
         key_out(p, g->dk, l.fk);
         p.dot = dkd;
-        if ((e = glr_go<true, true, 3, true>(p, io->dtype, st)) != hipSuccess) return e;
+        if ((e = glr_go<true, true, true>(p, io->dtype, st)) != hipSuccess) return e;
     }
     {   // dv
         GlrPass p = bwd;
@@ -1435,7 +1433,7 @@ hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipS
         p.o_t = static_cast<int64_t>(io->H) * io->dv;
         p.o_b = p.o_t * io->T;
         p.out_wide = io->dv % 4 == 0;
-        if ((e = glr_go<true, true, 2, false>(p, io->dtype, st)) != hipSuccess) return e;
+        if ((e = glr_go<true, true, false>(p, io->dtype, st)) != hipSuccess) return e;
     }
     if (io->T == 0) return hipSuccess;
     const int64_t waves = bh * sp.nseg;
