@@ -4,8 +4,9 @@ the current stream, the HIP kernels of libsdm_amd.so do every step, and there is
 
 Heads are [.., heads, columns] device tensors with contiguous columns and any strides before them (views
 of a packed projection, say), float32 or bfloat16. Outputs are allocated unless given. Every call takes
-the current stream of the inputs' device, or `stream` (a workspace that the call allocates is kept for
-it); inputs and outputs that another stream made or uses are the caller's to order, as everywhere in torch.
+the current stream of the inputs' device, or `stream`: then the outputs and the workspace that the call allocates
+are that stream's (no work still queued elsewhere uses their memory), the outputs kept for the current one too. Inputs
+and outputs that another stream made or uses are the caller's to order, as everywhere in torch.
 """
 
 from __future__ import annotations
@@ -63,10 +64,32 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+def _own(stream, shape, dtype, dev):
+    """Memory of the stream that will use it: what a block freed on the current stream held may still be in use there, and
+    `stream` does not wait for that."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _output(stream, shape, dtype, dev):
+    """A tensor that the call returns: the caller goes on with it on the current stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    t = _own(stream, shape, dtype, dev)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
 def _call(fn, dev, stream, *packed, workspace=None):
-    """Enqueues fn. workspace: a tensor of this call's own, whose memory its stream still needs when the call returns."""
-    if stream is not None and workspace is not None:
-        workspace.record_stream(stream)
+    """Enqueues fn. workspace: the caller's, which the stream still needs when the call returns."""
+    if stream is not None:
+        if stream.device != dev:
+            raise TypeError("the stream is on %s, the tensors are on %s" % (stream.device, dev))
+        if workspace is not None:
+            workspace.record_stream(stream)
     st = _raw_stream(dev.index) if stream is None else stream.cuda_stream
     if dev.index != torch.cuda.current_device():
         with torch.cuda.device(dev):
@@ -155,9 +178,9 @@ def norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=None, in
     if q is None and k is None:
         raise TypeError("norm_rope: q or k is required")
     if q_out is None and q is not None:
-        q_out = q.new_empty(q.shape)
+        q_out = _output(stream, q.shape, q.dtype, q.device)
     if k_out is None and k is not None:
-        k_out = k.new_empty(k.shape)
+        k_out = _output(stream, k.shape, k.dtype, k.device)
     dev, io = _norm_rope_io("norm_rope", q, k, q_weight, k_weight, positions, table, interleaved, eps, q_out, k_out)
     _call(_lib.load().sdm_norm_rope, dev, stream, io)
     return q_out, k_out
@@ -170,8 +193,8 @@ def norm_rope_backward(d_q, d_k, q, k, q_weight=None, k_weight=None, positions=N
     fn = "norm_rope_backward"
     if q is None and k is None:
         raise TypeError("%s: q or k is required" % fn)
-    dq = None if q is None else q.new_empty(q.shape)
-    dk = None if k is None else k.new_empty(k.shape)
+    dq = None if q is None else _output(stream, q.shape, q.dtype, q.device)
+    dk = None if k is None else _output(stream, k.shape, k.dtype, k.device)
     dev, io = _norm_rope_io(fn, q, k, q_weight, k_weight, positions, table, interleaved, eps, dq, dk)
     one = q if q is not None else k
     grads = []
@@ -185,13 +208,13 @@ def norm_rope_backward(d_q, d_k, q, k, q_weight=None, k_weight=None, positions=N
         _columns(fn, d)
         grads.append((d.data_ptr(), d.stride(0), d.stride(1)))
     lib = _lib.load()
-    ws = torch.empty(max(int(lib.sdm_norm_rope_workspace(io)), 16), dtype=torch.uint8, device=dev)
+    ws = _own(stream, max(int(lib.sdm_norm_rope_workspace(io)), 16), torch.uint8, dev)
     D = one.shape[-1]
-    dw = torch.empty((2, D), dtype=torch.float32, device=dev)
+    dw = _output(stream, (2, D), torch.float32, dev)
     at = dw.data_ptr()
     (gq, gqr, gqh), (gk, gkr, gkh) = grads
     g = _lib.pack_norm_rope_grad(gq, gk, gqr, gqh, gkr, gkh, 0 if q is None else at, 0 if k is None else at + 4 * D, ws.data_ptr(), ws.numel())
-    _call(lib.sdm_norm_rope_backward, dev, stream, io, g, workspace=ws)
+    _call(lib.sdm_norm_rope_backward, dev, stream, io, g)
     return dict(dq=dq, dk=dk, dwq=None if q is None else dw[0], dwk=None if k is None else dw[1])
 
 
@@ -222,9 +245,9 @@ def slot_topk(a, b, K, scale=1.0, shape=None, idx=None, val=None, idx_dtype=torc
     K = int(K)
     out = a.shape[:-1] + (K,)
     if idx is None:
-        idx = torch.empty(out, dtype=idx_dtype, device=a.device)
+        idx = _output(stream, out, idx_dtype, a.device)
     if val is None:
-        val = torch.empty(out, dtype=val_dtype, device=a.device)
+        val = _output(stream, out, val_dtype, a.device)
     for name, t in (("idx", idx), ("val", val)):
         _shape("slot_topk", name, t, out)
         if not t.is_contiguous():
@@ -248,7 +271,7 @@ def slot_topk_backward(d_val, idx, a, b, scale=1.0, shape=None, stream=None):
     _shape(fn, "d_val", d_val, idx.shape)
     _same(fn, a, d_val)
     dev, io = _slot_io(fn, a, b, K, idx, None, scale, shape)
-    da, db = torch.empty(a.shape, dtype=a.dtype, device=dev), torch.empty(b.shape, dtype=b.dtype, device=dev)
+    da, db = _output(stream, a.shape, a.dtype, dev), _output(stream, b.shape, b.dtype, dev)
     g = _lib.pack_slot_topk_grad(d_val.data_ptr(), da.data_ptr(), db.data_ptr(), a.shape[-1], b.shape[-1])
     _call(_lib.load().sdm_slot_topk_backward, dev, stream, io, g)
     return da, db
@@ -256,7 +279,7 @@ def slot_topk_backward(d_val, idx, a, b, scale=1.0, shape=None, stream=None):
 
 # ------------------------------------------------------------------------- the gated linear recurrence
 
-def _glr_io(fn, q, k, v, g, scale, state, lens, o, last, backward, workspace):
+def _glr_io(fn, q, k, v, g, scale, state, lens, o, last, backward, workspace, stream):
     """The call's device and structure, and the workspace to keep until it is enqueued."""
     if q.dim() != 4 or v.dim() != 4:
         raise ValueError("%s: q, k are [B, T, Hk, dk] and v is [B, T, H, dv]" % fn)
@@ -287,7 +310,7 @@ def _glr_io(fn, q, k, v, g, scale, state, lens, o, last, backward, workspace):
               _code(fn, q), float(dk ** -0.5 if scale is None else scale))
     if workspace is None:
         need = int(_lib.load().sdm_glr_workspace(_lib.pack_glr(*fields, 0, 0), backward))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        workspace = _own(stream, need, torch.uint8, dev) if need else None
     size = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return dev, _lib.pack_glr(*fields, _ptr(workspace), size), workspace
 
@@ -310,11 +333,11 @@ def glr_forward(q, k, v, g, scale=None, state=None, lens=None, out=None, last=No
     glr_workspace_bytes (allocated per call by default)."""
     if q.dim() == 4 and v.dim() == 4:
         if out is None:
-            out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+            out = _output(stream, v.shape, v.dtype, v.device)
         if last is None:
-            last = torch.empty((q.shape[0], v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=v.device)
-    dev, io, keep = _glr_io("glr_forward", q, k, v, g, scale, state, lens, out, last, 0, workspace)
-    _call(_lib.load().sdm_glr_forward, dev, stream, io, workspace=keep)
+            last = _output(stream, (q.shape[0], v.shape[2], q.shape[3], v.shape[3]), torch.float32, v.device)
+    dev, io, keep = _glr_io("glr_forward", q, k, v, g, scale, state, lens, out, last, 0, workspace, stream)
+    _call(_lib.load().sdm_glr_forward, dev, stream, io, workspace=workspace)
     return out, last
 
 
@@ -323,7 +346,7 @@ def glr_backward(d_out, q, k, v, g, scale=None, state=None, d_last=None, lens=No
     last state (None: zero): a dict of dq, dk, dv (contiguous, like q, k, v), dg [B, T, H] float32 and dstate (the
     gradient of the first state, [B, H, dk, dv] float32). Nothing of the forward is needed but its inputs."""
     fn = "glr_backward"
-    dev, io, keep = _glr_io(fn, q, k, v, g, scale, state, lens, None, None, 1, workspace)
+    dev, io, keep = _glr_io(fn, q, k, v, g, scale, state, lens, None, None, 1, workspace, stream)
     _same(fn, q, d_out, d_last)
     _shape(fn, "d_out", d_out, v.shape)
     if d_out.dtype is not v.dtype:
@@ -334,11 +357,11 @@ def glr_backward(d_out, q, k, v, g, scale=None, state=None, d_last=None, lens=No
     H, dv = v.shape[2:]
     if d_last is not None:
         _shape(fn, "d_last", d_last, (B, H, dk, dv))
-    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    new = lambda shape, dtype: _output(stream, shape, dtype, dev)  # noqa: E731
     r = dict(dq=new(q.shape, q.dtype), dk=new(k.shape, q.dtype), dv=new(v.shape, q.dtype), dg=new((B, T, H), torch.float32),
              dstate=new((B, H, dk, dv), torch.float32))
     grad = _lib.pack_glr_grad(d_out.data_ptr(), *d_out.stride()[:3], _ptr(d_last), *[t.data_ptr() for t in r.values()])
-    _call(_lib.load().sdm_glr_backward, dev, stream, io, grad, workspace=keep)
+    _call(_lib.load().sdm_glr_backward, dev, stream, io, grad, workspace=workspace)
     return r
 
 
@@ -354,7 +377,7 @@ def glr_step(q, k, v, g, state, scale=None, new_state=None, slots=None, out=None
     B, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
     if out is None:
-        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        out = _output(stream, v.shape, v.dtype, v.device)
     if new_state is None:
         new_state = state
     dev = _same(fn, q, k, v, g, state, new_state, slots, out)
