@@ -488,8 +488,8 @@ typedef struct sdm_norm_rope_io {
                                gradients of q and k */
     void* k_out;
     int64_t qo_row, qo_head, ko_row, ko_head;
-    const void* wq;         /* [D] norm weights of the query heads (NULL: ones) */
-    const void* wk;         /* [D] norm weights of the key heads (NULL: ones) */
+    const void* wq;         /* [D] norm weights of the query heads (NULL: ones; not read when Hq is 0) */
+    const void* wk;         /* [D] norm weights of the key heads (NULL: ones; not read when Hk is 0) */
     const void* pos;        /* [N] positions, int32 or int64 (pos_bytes); only read when rot > 0. A position
                                outside 0 .. table_rows-1 takes the nearest row of the table */
     const float* table;     /* [table_rows, rot] float32: the cosines of a position's rot/2 angles, then the sines */

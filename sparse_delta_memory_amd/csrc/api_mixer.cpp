@@ -52,7 +52,7 @@ sdm_status check_norm_rope(const sdm_norm_rope_io* io, const char* fn) {
     for (const void* p : {io->q, io->k, static_cast<const void*>(io->q_out), static_cast<const void*>(io->k_out)}) {
         if (!aligned(p, es)) return fail(SDM_EALIGN, "%s: a head pointer is not element-aligned", fn);
     }
-    if (!aligned(io->wq, size_of(io->w_dtype)) || !aligned(io->wk, size_of(io->w_dtype)))
+    if ((io->Hq > 0 && !aligned(io->wq, size_of(io->w_dtype))) || (io->Hk > 0 && !aligned(io->wk, size_of(io->w_dtype))))
         return fail(SDM_EALIGN, "%s: wq or wk is not element-aligned", fn);
     if (io->rot > 0 && (!aligned(io->pos, io->pos_bytes) || !aligned(io->table, 4)))
         return fail(SDM_EALIGN, "%s: pos or table is misaligned", fn);

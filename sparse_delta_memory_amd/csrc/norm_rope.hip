@@ -505,6 +505,15 @@ __global__ __launch_bounds__(16 * kNrSumRuns) void norm_rope_sum_kernel(const fl
     }
 }
 
+// The call as the kernels take it: a tensor without heads has no weights either, whatever the pointer (every lane loads both
+// tensors' weights before it walks the heads).
+sdm_norm_rope_io nr_used(const sdm_norm_rope_io* io) {
+    sdm_norm_rope_io u = *io;
+    if (u.Hq == 0) u.wq = nullptr;
+    if (u.Hk == 0) u.wk = nullptr;
+    return u;
+}
+
 // Whether the vector path takes this call: pairs in whole runs of four on 16-byte addresses.
 bool nr_vector(const sdm_norm_rope_io* io, const sdm_norm_rope_grad* g) {
     const int es = io->dtype == SDM_BF16 ? 2 : 4, unit = 16 / es;
@@ -565,7 +574,8 @@ void nr_back_go(const NrBack& b, int tl, unsigned blocks, hipStream_t st) {
 
 }  // namespace
 
-hipError_t norm_rope_launch(const sdm_norm_rope_io* io, hipStream_t st) {
+hipError_t norm_rope_launch(const sdm_norm_rope_io* call, hipStream_t st) {
+    const sdm_norm_rope_io used = nr_used(call), *io = &used;
     NrArgs a{*io, io->Hq + io->Hk, 1, 1};
     if (nr_vector(io, nullptr)) {
         const int tl = team_lanes(io->D);
@@ -598,7 +608,8 @@ size_t norm_rope_back_workspace(int64_t N, int H, int D) {
     return static_cast<size_t>(most) * 2 * D * sizeof(float);
 }
 
-hipError_t norm_rope_back_launch(const sdm_norm_rope_io* io, const sdm_norm_rope_grad* g, hipStream_t st) {
+hipError_t norm_rope_back_launch(const sdm_norm_rope_io* call, const sdm_norm_rope_grad* g, hipStream_t st) {
+    const sdm_norm_rope_io used = nr_used(call), *io = &used;
     NrBack b;
     b.a = NrArgs{*io, io->Hq + io->Hk, 1, 1};
     b.dq = g->dq;

@@ -146,6 +146,10 @@ def _norm_rope_io(fn, q, k, q_weight, k_weight, positions, table, interleaved, e
         else:
             _head(fn, t, o, w, N, D, one.dtype, rows)
     wd = _lib.SDM_F32
+    if q is None:      # a weight without its heads is not used
+        q_weight = None
+    if k is None:
+        k_weight = None
     w = q_weight if q_weight is not None else k_weight
     if w is not None:
         wd = _code(fn, w)
