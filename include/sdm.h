@@ -508,7 +508,7 @@ typedef struct sdm_norm_rope_io {
 /*
  * Per head x: y = x w / sqrt(mean(x^2) + eps), its first rot columns turned by the token's angles:
  * (y1, y2) -> (y1 c - y2 s, y2 c + y1 s). One kernel on st; float32 inside, rounded once.
- * Requires N * (Hq + Hk) <= 2^25.
+ * Requires N * (Hq + Hk) <= 2^26 - 4 (work items of one grid).
  */
 sdm_status sdm_norm_rope(const sdm_norm_rope_io* io, hipStream_t st);
 

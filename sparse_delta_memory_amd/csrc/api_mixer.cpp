@@ -12,6 +12,9 @@ namespace {
 
 using sdm::fail;
 
+// Heads of a norm_rope call: the element path takes a wave per head, and a grid holds fewer than 2^32 work items.
+constexpr int64_t kMaxHeads = (int64_t(1) << 26) - 4;   // whole blocks of four waves
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool known(int32_t dtype) { return dtype == SDM_F32 || dtype == SDM_BF16; }
 uintptr_t size_of(int32_t dtype) { return dtype == SDM_BF16 ? 2 : 4; }
@@ -34,7 +37,7 @@ sdm_status check_norm_rope(const sdm_norm_rope_io* io, const char* fn) {
         return fail(SDM_ESHAPE, "%s: N = %lld, Hq = %d, Hk = %d", fn, static_cast<long long>(io->N), io->Hq, io->Hk);
     const int64_t heads = static_cast<int64_t>(io->Hq) + io->Hk;
     if (heads < 1 || heads > (1 << 20)) return fail(SDM_ESHAPE, "%s: Hq + Hk = %lld outside 1..2^20", fn, static_cast<long long>(heads));
-    if (io->N > (int64_t(1) << 25) / heads) return fail(SDM_ESHAPE, "%s: N (Hq + Hk) exceeds 2^25 heads", fn);
+    if (io->N > kMaxHeads / heads) return fail(SDM_ESHAPE, "%s: N (Hq + Hk) exceeds 2^26 - 4 heads", fn);
     if (io->D < 1 || io->D > 512) return fail(SDM_ESHAPE, "%s: D = %d outside 1..512", fn, io->D);
     if (io->rot < 0 || io->rot > io->D || io->rot % 2 != 0)
         return fail(SDM_ESHAPE, "%s: rot = %d (even, 0..D = %d)", fn, io->rot, io->D);
@@ -128,7 +131,7 @@ sdm_status sdm_norm_rope(const sdm_norm_rope_io* io, hipStream_t st) {
 size_t sdm_norm_rope_workspace(const sdm_norm_rope_io* io) {
     if (io == nullptr || io->N < 1 || io->Hq < 0 || io->Hk < 0 || io->D < 1 || io->D > 512) return 0;
     const int64_t heads = static_cast<int64_t>(io->Hq) + io->Hk;
-    if (heads < 1 || heads > (1 << 20) || io->N > (int64_t(1) << 25) / heads) return 0;
+    if (heads < 1 || heads > (1 << 20) || io->N > kMaxHeads / heads) return 0;
     return sdm::norm_rope_back_workspace(io->N, static_cast<int>(heads), io->D);
 }
 

@@ -177,3 +177,17 @@ GS = dict(q=FAKE, k=FAKE, v=FAKE, g=FAKE, o=FAKE, state=FAKE, new_state=FAKE, ro
 ])
 def test_glr_step_refusals(kw, status):
     assert _lib.load().sdm_glr_step(ctypes.byref(fill(_lib.GlrStepIO, GS, kw)), None) == status
+
+
+@built
+def test_norm_rope_heads_of_one_grid():
+    """524288 tokens of 72 heads are taken; what no grid of a wave per head holds is refused."""
+    lib = _lib.load()
+    ok = fill(_lib.NormRopeIO, NR, dict(N=1 << 19, Hq=64, Hk=8))
+    assert lib.sdm_norm_rope_workspace(ctypes.byref(ok)) == 1024 * 2 * 64 * 4
+    most = fill(_lib.NormRopeIO, NR, dict(N=(1 << 26) - 4, Hq=1, Hk=0))
+    assert lib.sdm_norm_rope_workspace(ctypes.byref(most)) == 1024 * 2 * 64 * 4
+    for kw in (dict(N=(1 << 26) - 3, Hq=1, Hk=0), dict(N=1 << 20, Hq=64)):
+        io = fill(_lib.NormRopeIO, NR, kw)
+        assert lib.sdm_norm_rope_workspace(ctypes.byref(io)) == 0
+        assert lib.sdm_norm_rope(ctypes.byref(io), None) == _lib.SDM_ESHAPE
