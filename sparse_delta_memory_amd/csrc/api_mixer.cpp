@@ -76,8 +76,11 @@ sdm_status check_slots(const sdm_slot_topk_io* io, const char* fn) {
     if (io->chunk_rows < 0 || (io->chunk_rows > 0 && (io->P < 1 || io->stream_offset < 0 || io->stream_offset > (int64_t(1) << 40))))
         return fail(SDM_EINVAL, "%s: chunk_rows = %lld, P = %d, stream_offset = %lld", fn, static_cast<long long>(io->chunk_rows), io->P,
                     static_cast<long long>(io->stream_offset));
-    const int64_t most = static_cast<int64_t>(io->n1) * io->n2 + (io->chunk_rows > 0 ? (io->P - 1) * io->stream_offset : 0);
-    if (io->idx_bytes == 4 && most > (int64_t(1) << 31)) return fail(SDM_EINVAL, "%s: ids up to %lld do not fit int32", fn, static_cast<long long>(most - 1));
+    // The last stream's largest id, by division: the product of the largest P and offset passes 64 bits.
+    const int64_t slots = static_cast<int64_t>(io->n1) * io->n2, top = io->idx_bytes == 4 ? INT32_MAX : INT64_MAX;
+    if (io->chunk_rows > 0 && io->stream_offset > 0 && io->P - 1 > (top - (slots - 1)) / io->stream_offset)
+        return fail(SDM_EINVAL, "%s: ids of %d streams of %lld do not fit int%d", fn, io->P, static_cast<long long>(io->stream_offset),
+                    8 * io->idx_bytes);
     if (io->N == 0) return SDM_OK;
     if (io->a == nullptr || io->b == nullptr || io->idx == nullptr) return fail(SDM_EINVAL, "%s: a, b and idx are required", fn);
     if (!aligned(io->a, size_of(io->dtype)) || !aligned(io->b, size_of(io->dtype)) || !aligned(io->idx, io->idx_bytes))

@@ -191,3 +191,24 @@ def test_norm_rope_heads_of_one_grid():
         io = fill(_lib.NormRopeIO, NR, kw)
         assert lib.sdm_norm_rope_workspace(ctypes.byref(io)) == 0
         assert lib.sdm_norm_rope(ctypes.byref(io), None) == _lib.SDM_ESHAPE
+
+
+@built
+@pytest.mark.parametrize("kw", [
+    dict(P=(1 << 24) + 1, stream_offset=1 << 40), dict(P=(1 << 24) + 1, stream_offset=1 << 40, idx_bytes=8),   # products of 2^64, 2^63
+    dict(P=(1 << 23) + 1, stream_offset=1 << 40, idx_bytes=8), dict(P=(1 << 31) - 1, stream_offset=1 << 40), dict(P=2, stream_offset=(1 << 31) - 4095),
+])
+def test_slot_ids_past_their_type(kw):
+    lib = _lib.load()
+    io = fill(_lib.SlotTopkIO, {**ST, "chunk_rows": 8}, kw)
+    g = fill(_lib.SlotTopkGrad, dict(dval=FAKE, da=FAKE, db=FAKE, da_row=64, db_row=64), {})
+    assert lib.sdm_slot_topk(ctypes.byref(io), None) == _lib.SDM_EINVAL
+    assert lib.sdm_slot_topk_backward(ctypes.byref(io), ctypes.byref(g), None) == _lib.SDM_EINVAL
+
+
+@built
+def test_slot_ids_that_fit():
+    lib = _lib.load()
+    for kw in (dict(P=2, stream_offset=(1 << 31) - 4096), dict(P=(1 << 23) - 1, stream_offset=1 << 40, idx_bytes=8), dict(P=1 << 30, stream_offset=0)):
+        io = fill(_lib.SlotTopkIO, {**ST, "chunk_rows": 8, "N": 0}, kw)
+        assert lib.sdm_slot_topk(ctypes.byref(io), None) == _lib.SDM_OK
