@@ -50,34 +50,40 @@ using sdm::fail;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// Once per device, before the first launch there: the device's LDS bytes per workgroup, and every
-// dynamic-LDS kernel's limit raised to it. Entry points call this after their argument checks and
-// before their first enqueue.
+// Once per device and family of kernels, before the family's first launch there: the device's LDS bytes
+// per workgroup, and the limits of the family's dynamic-LDS kernels raised to it. Entry points call this
+// after their argument checks and before their first enqueue. By family, since raising a limit loads its
+// kernel: the first call of a process that only uses the bank takes 2.8 ms, and took 7.0 with the mixer
+// operators' 64 kernels in it.
 constexpr int kMaxDevices = 64;
 struct DeviceSetup {
     std::once_flag once;
     hipError_t err = hipSuccess;
     int lds_max = 0;
 };
-DeviceSetup g_setup[kMaxDevices];
+DeviceSetup g_setup[3][kMaxDevices];
+
+int bank_kernels(const void** fns, int cap) {
+    const int n = sdm::p1_lds_kernels(fns, cap);
+    return n + sdm::read_lds_kernels(fns + n, cap - n);
+}
 
 }  // namespace
 
-hipError_t sdm::device_setup(int* lds_max) {
+hipError_t sdm::device_setup(int* lds_max, KernelFamily family) {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
-    DeviceSetup& d = g_setup[dev];
-    std::call_once(d.once, [&d, dev]() {
+    DeviceSetup& d = g_setup[static_cast<int>(family)][dev];
+    std::call_once(d.once, [&d, dev, family]() {
         int lds = 0;
         d.err = hipDeviceGetAttribute(&lds, hipDeviceAttributeMaxSharedMemoryPerBlock, dev);
         if (d.err != hipSuccess) return;
-        const void* fns[256];
-        int n = sdm::p1_lds_kernels(fns, 256);
-        n += sdm::read_lds_kernels(fns + n, 256 - n);
-        n += sdm::slot_lds_kernels(fns + n, 256 - n);
-        n += sdm::glr_lds_kernels(fns + n, 256 - n);
+        const void* fns[128];
+        const int n = family == KernelFamily::slots ? sdm::slot_lds_kernels(fns, 128)
+                      : family == KernelFamily::recurrence ? sdm::glr_lds_kernels(fns, 128)
+                                                           : bank_kernels(fns, 128);
         for (int i = 0; i < n && d.err == hipSuccess; ++i) {
             // The dynamic limit is what the device holds beside the kernel's static LDS.
             hipFuncAttributes fa;

@@ -25,8 +25,8 @@ sdm_status launched(hipError_t e, const char* fn) {
     return fail(SDM_EHIP, "%s: %s", fn, hipGetErrorString(e));
 }
 
-sdm_status set_up(const char* fn) {
-    const hipError_t e = sdm::device_setup(nullptr);
+sdm_status set_up(const char* fn, sdm::KernelFamily family) {
+    const hipError_t e = sdm::device_setup(nullptr, family);
     if (e != hipSuccess) return fail(SDM_EHIP, "%s: device set-up: %s", fn, hipGetErrorString(e));
     return SDM_OK;
 }
@@ -178,7 +178,7 @@ sdm_status sdm_slot_topk_backward(const sdm_slot_topk_io* io, const sdm_slot_top
     if (!aligned(g->dval, 4) || !aligned(g->da, size_of(io->dtype)) || !aligned(g->db, size_of(io->dtype)))
         return fail(SDM_EALIGN, "%s: dval, da or db is not element-aligned", fn);
     if (g->da == nullptr && g->db == nullptr) return SDM_OK;
-    rc = set_up(fn);
+    rc = set_up(fn, sdm::KernelFamily::slots);
     if (rc != SDM_OK) return rc;
     return launched(sdm::slot_topk_back_launch(io, g, st), fn);
 }
@@ -201,7 +201,7 @@ sdm_status sdm_glr_forward(const sdm_glr_io* io, hipStream_t st) {
     if (!aligned(io->o, size_of(io->dtype))) return fail(SDM_EALIGN, "%s: o is not element-aligned", fn);
     if (!aligned(io->last, 16)) return fail(SDM_EALIGN, "%s: last must be 16-byte aligned", fn);
     if (io->last != nullptr && io->last == io->state) return fail(SDM_EINVAL, "%s: last must not be state", fn);
-    rc = set_up(fn);
+    rc = set_up(fn, sdm::KernelFamily::recurrence);
     if (rc != SDM_OK) return rc;
     return launched(sdm::glr_forward_launch(io, st), fn);
 }
@@ -222,7 +222,7 @@ sdm_status sdm_glr_backward(const sdm_glr_io* io, const sdm_glr_grad* g, hipStre
         return fail(SDM_EALIGN, "%s: dq, dk, dv, d_last and d_state must be 16-byte aligned", fn);
     if (g->d_state != nullptr && (g->d_state == g->d_last || g->d_state == io->state))
         return fail(SDM_EINVAL, "%s: d_state must not be d_last or state", fn);   // every segment starts from those
-    rc = set_up(fn);
+    rc = set_up(fn, sdm::KernelFamily::recurrence);
     if (rc != SDM_OK) return rc;
     return launched(sdm::glr_backward_launch(io, g, st), fn);
 }

@@ -138,8 +138,9 @@ PaWorkspace pa_workspace_layout(const sdm_pa_io* io);
 // The message of a refused call (sdm_last_error) and its status; clear_error starts an entry point.
 sdm_status fail(sdm_status s, const char* fmt, ...);
 void clear_error();
-// Once per device, before the first launch there: the dynamic-LDS limits (see api.cpp).
-hipError_t device_setup(int* lds_max);
+// Once per device and family of kernels, before the family's first launch there: its dynamic-LDS limits (see api.cpp).
+enum class KernelFamily { bank, slots, recurrence };
+hipError_t device_setup(int* lds_max, KernelFamily family = KernelFamily::bank);
 
 // Head norms with rotation (validated by sdm_norm_rope and sdm_norm_rope_backward). workspace: bytes of the
 // backward's partial weight gradients.
