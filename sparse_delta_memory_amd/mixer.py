@@ -31,14 +31,19 @@ class Mixer:
         self.heads, self.key_heads, self.d, self.hd, self.n, self.W, self.R, self.C = heads, key_heads, d, hd, n, W, R, C
         # q, k, v heads; scores of the writes and of the reads (two rows each); bank values; gates of the heads, the bank, and beta
         self.split = [key_heads * d, key_heads * d, heads * d, n, n, n, n, hd, heads + 2]
-        self.w = (torch.randn((model, sum(self.split)), generator=gen, device=device) * model ** -0.5).to(dtype)
+        w = (torch.randn((model, sum(self.split)), generator=gen, device=device) * model ** -0.5).to(dtype)
+        # Each part starts on 16 bytes in every row, rows included (unused columns between): views of the projection's rows
+        # then take the operators' wide loads. Without it one odd part, the gates', puts all of them on the element paths.
+        unit = 16 // dtype.itemsize
+        self.padded = [-(-c // unit) * unit for c in self.split]
+        self.w = torch.cat([torch.nn.functional.pad(c, (0, wide - c.shape[1])) for c, wide in zip(w.split(self.split, 1), self.padded)], 1)
         self.q_norm, self.k_norm = torch.ones(d, device=device), torch.ones(d, device=device)
         self.table = rope_table(positions, rot, device=device)
 
     def project(self, x, pos):
         """x [P, T, model], pos [P * T] -> everything the two memories take, rows in x's order."""
         P, T = x.shape[:2]
-        q, k, v, wa, wb, ra, rb, u, g = (x.flatten(0, 1) @ self.w).split(self.split, 1)
+        q, k, v, wa, wb, ra, rb, u, g = (t[:, :c] for t, c in zip((x.flatten(0, 1) @ self.w).split(self.padded, 1), self.split))
         heads = lambda t, h: t.view(P * T, h, self.d)  # noqa: E731
         q, k = norm_rope(heads(q, self.key_heads), heads(k, self.key_heads), self.q_norm, self.k_norm, pos, self.table)
         k_idx, k_val = slot_topk(wa, wb, self.W)

@@ -1,0 +1,41 @@
+"""GPU: the example mixer layer gives its operators rows on which their wide loads work."""
+
+import os
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+from sparse_delta_memory_amd import mixer  # noqa: E402
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kw", [dict(), dict(heads=3, key_heads=1, n=20, hd=33)])
+def test_every_part_of_the_projection_is_aligned(monkeypatch, dtype, kw):
+    m = mixer.Mixer(dtype=dtype, C=8, **kw)
+    seen = []
+
+    def spy(f):
+        def g(*args, **kwargs):
+            # The gates are read one by one: the recurrence's fourth argument.
+            rows = args[:3] if f.__name__.startswith("glr") else args
+            seen.extend(t for t in rows if isinstance(t, torch.Tensor) and t.dtype == dtype and t.dim() > 1)
+            return f(*args, **kwargs)
+        return g
+
+    for name in ("norm_rope", "slot_topk", "glr_forward", "glr_step"):
+        monkeypatch.setattr(mixer, name, spy(getattr(mixer, name)))
+    x = torch.randn(2, 17, m.w.shape[0], device="cuda").to(dtype)
+    bank = m.bank(2)
+    y, state = m.prompt(x[:, :16], bank)
+    m.token(x[:, 16], bank, state, 16)
+    unit = 16 // dtype.itemsize
+    assert len(seen) >= 2 * (2 + 4 + 3)      # heads, scores of the writes and reads, q k v (and a float32 table)
+    for t in seen:
+        assert t.data_ptr() % 16 == 0 and all(s % unit == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1), (t.shape, t.stride())
