@@ -6,7 +6,7 @@ One projection of the token rows x [P, T, model] gives everything:
 
   query and key heads  -> norm_rope                      -> glr_forward / glr_step  (the dense state, value heads v)
   write scores a, b    -> slot_topk -> k_idx, k_val      -> phase1, read_step, dw_step (the bank, value rows u)
-  read scores a, b     -> slot_topk -> q_idx, q_val
+  read scores a, b     -> slot_topk -> q_idx, q_val         (absolute ids, in Phase 1's chunks)
   gates, beta                        (log-sigmoid per token and head, sigmoid per token)
 
 and the layer's output is the dense heads' outputs and the bank's reads, side by side. Streams are rows of
@@ -40,33 +40,45 @@ class Mixer:
         self.q_norm, self.k_norm = torch.ones(d, device=device), torch.ones(d, device=device)
         self.table = rope_table(positions, rot, device=device)
 
-    def project(self, x, pos):
-        """x [P, T, model], pos [P * T] -> everything the two memories take, rows in x's order."""
+    def rows(self, x, pos):
+        """x [P, T, model], pos [P * T] -> what the two memories take before slots are chosen, rows in x's order: q, k, v, their
+        gates, the score rows (score_rows), and the bank's gate, beta and values."""
         P, T = x.shape[:2]
-        q, k, v, wa, wb, ra, rb, u, g = (t[:, :c] for t, c in zip((x.flatten(0, 1) @ self.w).split(self.padded, 1), self.split))
+        parts = self.padded[:3] + [sum(self.padded[3:7])] + self.padded[7:]      # the four score rows stay side by side
+        q, k, v, scores, u, g = (x.flatten(0, 1) @ self.w).split(parts, 1)
+        q, k, v, u, g = (t[:, :c] for t, c in zip((q, k, v, u, g), self.split[:3] + self.split[7:]))
         heads = lambda t, h: t.view(P * T, h, self.d)  # noqa: E731
         q, k = norm_rope(heads(q, self.key_heads), heads(k, self.key_heads), self.q_norm, self.k_norm, pos, self.table)
-        k_idx, k_val = slot_topk(wa, wb, self.W)
-        q_idx, q_val = slot_topk(ra, rb, self.R)
         g = g.float()
         gates, gate, beta = torch.nn.functional.logsigmoid(g[:, :self.heads] + 3), torch.nn.functional.logsigmoid(g[:, -2] + 3), g[:, -1].sigmoid()
-        return q, k, heads(v, self.heads), gates, k_idx, k_val, q_idx, q_val, gate, beta, u.float()
+        return q, k, heads(v, self.heads), gates, scores, gate, beta, u.float()
+
+    def score_rows(self, scores):
+        """a and b of the writes, then of the reads."""
+        return [t[:, :self.n] for t in scores.split(self.padded[3], 1)]
+
+    def project(self, x, pos):
+        """The same with the slots of every row, ids within its stream, in place of the scores."""
+        q, k, v, gates, scores, gate, beta, u = self.rows(x, pos)
+        wa, wb, ra, rb = self.score_rows(scores)
+        return q, k, v, gates, *slot_topk(wa, wb, self.W), *slot_topk(ra, rb, self.R), gate, beta, u
 
     def bank(self, P, dtype=torch.float32, device="cuda"):
         return torch.zeros((P * self.n * self.n, self.hd), dtype=dtype, device=device)
 
-    def sparse(self, bank, P, T, C, k_idx, k_val, q_idx, q_val, gate, beta, u):
+    def sparse(self, bank, P, T, C, scores, gate, beta, u):
         """The bank over T tokens of P streams, in chunks of C: reads [P * T, hd], the bank updated in place."""
         steps, S = T // C, self.n * self.n
         # Chunk ti * P + p holds the tokens ti * C .. of stream p.
-        chunks = lambda t: t.view(P, steps, C, *t.shape[1:]).transpose(0, 1).contiguous()  # noqa: E731
-        stream = (torch.arange(P, dtype=torch.int32, device=bank.device) * S).view(1, P, 1, 1)
+        chunks = lambda t: t.unflatten(0, (P, steps, C)).transpose(0, 1).reshape(-1, *t.shape[1:])  # noqa: E731
         N = steps * P
         shape = make_shape(N, C, self.W, self.R, P=P, key_bits=max(1, (S - 1).bit_length()), stream_offset=S)
-        ki, qi = ((chunks(t) + stream).view(N, C, -1) for t in (k_idx, q_idx))
-        kv, qv, g, b = (chunks(t).view(N, C, *t.shape[1:]) for t in (k_val, q_val, gate, beta))
+        # Slots in Phase 1's layouts and absolute ids, from the score rows in the chunks' order.
+        wa, wb, ra, rb = self.score_rows(chunks(scores))
+        (ki, kv), (qi, qv) = ([t.view(N, C, K) for t in slot_topk(a, b, K, shape=shape)] for a, b, K in ((wa, wb, self.W), (ra, rb, self.R)))
+        g, b = chunks(gate).view(N, C), chunks(beta).view(N, C)
         out = phase1(shape, ki, qi, kv, qv, g)
-        v = chunks(u).view(N * C, self.hd)
+        v = chunks(u).contiguous()
         dv, pred, read = torch.empty_like(v), torch.empty_like(v), torch.empty_like(v)
         ws = alloc_dw_workspace(shape, self.hd, bank.device)
         for ti in range(steps):
@@ -81,7 +93,7 @@ class Mixer:
         if T % self.C:
             raise ValueError("Mixer.prompt: %d tokens are no whole chunks of %d" % (T, self.C))
         pos = (torch.arange(start, start + T, dtype=torch.int32, device=x.device)).repeat(P)
-        q, k, v, gates, *sparse = self.project(x, pos)
+        q, k, v, gates, *sparse = self.rows(x, pos)
         seq = lambda t: t.unflatten(0, (P, T))  # noqa: E731
         o, state = glr_forward(seq(q), seq(k), seq(v), seq(gates), state=state)
         read = self.sparse(bank, P, T, self.C, *sparse)
@@ -90,7 +102,7 @@ class Mixer:
     def token(self, x, bank, state, pos):
         """One token of every stream: x [P, model] -> y [P, heads * d + hd]; the bank and the state are updated in place."""
         P = x.shape[0]
-        q, k, v, gates, *sparse = self.project(x[:, None], torch.full((P,), pos, dtype=torch.int32, device=x.device))
+        q, k, v, gates, *sparse = self.rows(x[:, None], torch.full((P,), pos, dtype=torch.int32, device=x.device))
         o = glr_step(q, k, v, gates, state)
         return torch.cat([o.flatten(1).float(), self.sparse(bank, P, 1, 1, *sparse)], 1)
 

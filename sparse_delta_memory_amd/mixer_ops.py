@@ -234,6 +234,8 @@ def _slot_io(fn, a, b, K, idx, val, scale, shape):
         raise ValueError("%s: a and b must be 2-D or contiguous" % fn)
     ra, rb = (a.stride(0), b.stride(0)) if a.dim() == 2 else (n1, n2)
     C, P, off = (0, 1, 0) if shape is None else (shape.C, shape.P, shape.stream_offset)
+    if shape is not None and a.shape[:-1].numel() != shape.N * C:
+        raise ValueError("%s: %d rows of scores, the shape has %d chunks of %d tokens" % (fn, a.shape[:-1].numel(), shape.N, C))
     return dev, _lib.pack_slot_topk(a.data_ptr(), b.data_ptr(), ra, rb, _ptr(idx), _ptr(val), idx.numel() // K if K else 0, n1, n2, K, _code(fn, a),
                                     0 if val is None else _code(fn, val), 8 if idx.dtype is torch.int64 else 4, float(scale), C, P, off)
 
@@ -244,7 +246,7 @@ def slot_topk(a, b, K, scale=1.0, shape=None, idx=None, val=None, idx_dtype=torc
     best sums of those, the best first (of equal ones the lower column; of equal sums the better a, then the better
     b), and the softmax of the K sums times scale. NaN counts as -infinity, and a sum of -infinity weighs 0.
 
-    shape: a Phase-1 shape whose chunks the tokens are ([N, C, n]): ids are then absolute, chunk c's plus
+    shape: a Phase-1 shape whose chunks the tokens are ([N, C, n], or N * C rows): ids are then absolute, chunk c's plus
     (c % P) * stream_offset, and idx, val can be Phase 1's k_idx, k_val (or q_idx, q_val)."""
     K = int(K)
     out = a.shape[:-1] + (K,)

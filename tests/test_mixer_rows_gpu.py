@@ -39,3 +39,16 @@ def test_every_part_of_the_projection_is_aligned(monkeypatch, dtype, kw):
     assert len(seen) >= 2 * (2 + 4 + 3)      # heads, scores of the writes and reads, q k v (and a float32 table)
     for t in seen:
         assert t.data_ptr() % 16 == 0 and all(s % unit == 0 for s, n in zip(t.stride()[:-1], t.shape) if n > 1), (t.shape, t.stride())
+
+
+def test_rows_of_another_count_than_the_shape():
+    """slot_topk with a Phase-1 shape takes that shape's tokens."""
+    import sparse_delta_memory_amd as sdm
+    shape = sdm.make_shape(6, 8, 4, 4, P=3, key_bits=8, stream_offset=256)
+    a = torch.randn(48, 16, device="cuda")
+    idx, _ = sdm.slot_topk(a, a, 4, shape=shape)
+    for rows in (a[:40], a[:40].view(5, 8, 16)):
+        with pytest.raises(ValueError):
+            sdm.slot_topk(rows, rows, 4, shape=shape)
+    with pytest.raises(ValueError):
+        sdm.slot_topk_backward(torch.zeros(40, 4, device="cuda"), idx[:40].contiguous(), a[:40], a[:40], shape=shape)
