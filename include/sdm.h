@@ -574,7 +574,8 @@ typedef struct sdm_glr_io {
     const void* v;          /* [B, T, H, dv] */
     const float* g;         /* [B, T, H] log gates (<= 0; -infinity, or anything at or below -10000, resets the state) */
     int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, g_b, g_t, g_h;
-    const float* state;     /* [B, H, dk, dv] contiguous, the state before the first token (NULL: zero) */
+    const float* state;     /* [B, H, dk, dv] contiguous, the state before the first token (NULL: zero). States are 16-byte
+                               aligned, or 4-byte where dk dv is no multiple of 4 */
     const int32_t* lens;    /* [B] tokens of each stream (NULL: T); a value outside 0..T is taken to the nearest.
                                Later tokens are not read, leave the state alone and get zero outputs */
     void* o;                /* OUT of sdm_glr_forward [B, T, H, dv], strided */

@@ -88,6 +88,10 @@ sdm_status check_slots(const sdm_slot_topk_io* io, const char* fn) {
     return SDM_OK;
 }
 
+// Alignment of states: 16 bytes where that holds for every row of a pool, else an element's (the rows of odd widths are
+// read and written element by element).
+uintptr_t state_align(int32_t dk, int32_t dv) { return static_cast<int64_t>(dk) * dv % 4 == 0 ? 16 : 4; }
+
 sdm_status check_heads(int32_t H, int32_t Hk, int32_t dk, int32_t dv, int32_t dtype, float scale, const char* fn) {
     if (H < 1 || Hk < 1 || H % Hk != 0) return fail(SDM_ESHAPE, "%s: H = %d must be a multiple of Hk = %d (both >= 1)", fn, H, Hk);
     if (dk < 1 || dk > 128 || dv < 1 || dv > 128) return fail(SDM_ESHAPE, "%s: dk = %d, dv = %d outside 1..128", fn, dk, dv);
@@ -112,7 +116,8 @@ sdm_status check_glr(const sdm_glr_io* io, bool backward, const char* fn) {
         if (!aligned(p, es)) return fail(SDM_EALIGN, "%s: q, k or v is not element-aligned", fn);
     }
     if (!aligned(io->g, 4) || !aligned(io->lens, 4)) return fail(SDM_EALIGN, "%s: g or lens is misaligned", fn);
-    if (!aligned(io->state, 16)) return fail(SDM_EALIGN, "%s: state must be 16-byte aligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(io->state, sa)) return fail(SDM_EALIGN, "%s: state must be %d-byte aligned", fn, static_cast<int>(sa));
     const size_t need = sdm::glr_workspace_bytes(io, backward);
     if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
         return fail(SDM_EWORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, io->workspace == nullptr ? size_t(0) : io->workspace_bytes);
@@ -199,7 +204,8 @@ sdm_status sdm_glr_forward(const sdm_glr_io* io, hipStream_t st) {
     if (rc != SDM_OK || io->B == 0) return rc;
     if (io->T > 0 && io->o == nullptr) return fail(SDM_EINVAL, "%s: o is required", fn);
     if (!aligned(io->o, size_of(io->dtype))) return fail(SDM_EALIGN, "%s: o is not element-aligned", fn);
-    if (!aligned(io->last, 16)) return fail(SDM_EALIGN, "%s: last must be 16-byte aligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(io->last, sa)) return fail(SDM_EALIGN, "%s: last must be %d-byte aligned", fn, static_cast<int>(sa));
     if (io->last != nullptr && io->last == io->state) return fail(SDM_EINVAL, "%s: last must not be state", fn);
     rc = set_up(fn, sdm::KernelFamily::recurrence);
     if (rc != SDM_OK) return rc;
@@ -217,9 +223,10 @@ sdm_status sdm_glr_backward(const sdm_glr_io* io, const sdm_glr_grad* g, hipStre
         return fail(SDM_EINVAL, "%s: d_o, dq, dk, dv and dg are required", fn);
     const uintptr_t es = size_of(io->dtype);
     if (!aligned(g->d_o, es)) return fail(SDM_EALIGN, "%s: d_o is not element-aligned", fn);
-    if (!aligned(g->dq, 16) || !aligned(g->dk, 16) || !aligned(g->dv, 16) || !aligned(g->dg, 4) || !aligned(g->d_last, 16) ||
-        !aligned(g->d_state, 16))
-        return fail(SDM_EALIGN, "%s: dq, dk, dv, d_last and d_state must be 16-byte aligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(g->dq, 16) || !aligned(g->dk, 16) || !aligned(g->dv, 16) || !aligned(g->dg, 4) || !aligned(g->d_last, sa) ||
+        !aligned(g->d_state, sa))
+        return fail(SDM_EALIGN, "%s: dq, dk and dv must be 16-byte aligned, d_last and d_state %d", fn, static_cast<int>(sa));
     if (g->d_state != nullptr && (g->d_state == g->d_last || g->d_state == io->state))
         return fail(SDM_EINVAL, "%s: d_state must not be d_last or state", fn);   // every segment starts from those
     rc = set_up(fn, sdm::KernelFamily::recurrence);
@@ -246,7 +253,9 @@ sdm_status sdm_glr_step(const sdm_glr_step_io* io, hipStream_t st) {
         if (!aligned(p, es)) return fail(SDM_EALIGN, "%s: q, k, v or o is not element-aligned", fn);
     }
     if (!aligned(io->g, 4) || !aligned(io->slots, 4)) return fail(SDM_EALIGN, "%s: g or slots is misaligned", fn);
-    if (!aligned(io->state, 16) || !aligned(io->new_state, 16)) return fail(SDM_EALIGN, "%s: state and new_state must be 16-byte aligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(io->state, sa) || !aligned(io->new_state, sa))
+        return fail(SDM_EALIGN, "%s: state and new_state must be %d-byte aligned", fn, static_cast<int>(sa));
     return launched(sdm::glr_step_launch(io, st), fn);
 }
 

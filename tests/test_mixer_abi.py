@@ -212,3 +212,16 @@ def test_slot_ids_that_fit():
     for kw in (dict(P=2, stream_offset=(1 << 31) - 4096), dict(P=(1 << 23) - 1, stream_offset=1 << 40, idx_bytes=8), dict(P=1 << 30, stream_offset=0)):
         io = fill(_lib.SlotTopkIO, {**ST, "chunk_rows": 8, "N": 0}, kw)
         assert lib.sdm_slot_topk(ctypes.byref(io), None) == _lib.SDM_OK
+
+
+@built
+def test_states_of_odd_widths_are_aligned_by_element():
+    """Rows of a pool whose states are no whole 16-byte pieces; B = 0 and missing outputs keep everything on the host."""
+    lib = _lib.load()
+    for dv, status in ((24, _lib.SDM_EALIGN), (25, _lib.SDM_EINVAL)):      # EINVAL: o is missing, found after the alignment
+        io = fill(_lib.GlrIO, GL, dict(dk=15, dv=dv, state=FAKE + 4, o=None))
+        assert lib.sdm_glr_forward(ctypes.byref(io), None) == status
+    odd = fill(_lib.GlrIO, GL, dict(dk=15, dv=25, state=FAKE + 2))
+    assert lib.sdm_glr_forward(ctypes.byref(odd), None) == _lib.SDM_EALIGN
+    for kw, status in ((dict(dk=15, dv=25, state=FAKE + 2), _lib.SDM_EALIGN), (dict(dk=16, dv=25, new_state=FAKE + 4), _lib.SDM_EALIGN)):
+        assert lib.sdm_glr_step(ctypes.byref(fill(_lib.GlrStepIO, GS, kw)), None) == status
