@@ -224,15 +224,23 @@ def norm_rope_backward(d_q, d_k, q, k, q_weight=None, k_weight=None, positions=N
 
 # ------------------------------------------------------------------------------------- slot selection
 
+def _row_stride(fn, t):
+    """The stride between the rows of t [.., n], whose leading dimensions must fold into one (those of a view of a packed
+    projection do)."""
+    dims = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    for (_, s), (n, inner) in zip(dims, dims[1:]):
+        if s != n * inner and t.numel() > 0:
+            raise ValueError("%s: the rows of %s with strides %s are not evenly spaced" % (fn, tuple(t.shape), tuple(t.stride())))
+    return dims[-1][1] if dims else t.shape[-1]
+
+
 def _slot_io(fn, a, b, K, idx, val, scale, shape):
     dev = _same(fn, a, b, idx, val)
     if a.dim() < 2 or a.shape[:-1] != b.shape[:-1] or a.dtype is not b.dtype:
         raise ValueError("%s: a %s and b %s must be [.., n1] and [.., n2] of one dtype" % (fn, tuple(a.shape), tuple(b.shape)))
     _columns(fn, a, b)
     n1, n2 = a.shape[-1], b.shape[-1]
-    if a.dim() > 2 and not (a.is_contiguous() and b.is_contiguous()):   # leading dimensions that fold into one row stride
-        raise ValueError("%s: a and b must be 2-D or contiguous" % fn)
-    ra, rb = (a.stride(0), b.stride(0)) if a.dim() == 2 else (n1, n2)
+    ra, rb = (a.stride(0), b.stride(0)) if a.dim() == 2 else (_row_stride(fn, a), _row_stride(fn, b))
     C, P, off = (0, 1, 0) if shape is None else (shape.C, shape.P, shape.stream_offset)
     if shape is not None and a.shape[:-1].numel() != shape.N * C:
         raise ValueError("%s: %d rows of scores, the shape has %d chunks of %d tokens" % (fn, a.shape[:-1].numel(), shape.N, C))
@@ -242,8 +250,8 @@ def _slot_io(fn, a, b, K, idx, val, scale, shape):
 
 def slot_topk(a, b, K, scale=1.0, shape=None, idx=None, val=None, idx_dtype=torch.int32, val_dtype=torch.float32, stream=None):
     """(idx, val) [.., K]: ids and weights of each token's K best slots of a bank of n1 x n2, from its scores
-    a [.., n1] and b [.., n2]; a slot's score is a[i] + b[j], its id i * n2 + j. The K best of each row, then the K
-    best sums of those, the best first (of equal ones the lower column; of equal sums the better a, then the better
+    a [.., n1] and b [.., n2] (each with evenly spaced rows); a slot's score is a[i] + b[j], its id i * n2 + j. The
+    K best of each row, then the K best sums of those, the best first (of equal ones the lower column; of equal sums the better a, then the better
     b), and the softmax of the K sums times scale. NaN counts as -infinity, and a sum of -infinity weighs 0.
 
     shape: a Phase-1 shape whose chunks the tokens are ([N, C, n], or N * C rows): ids are then absolute, chunk c's plus
