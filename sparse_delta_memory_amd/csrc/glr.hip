@@ -970,6 +970,9 @@ struct GateGrad {
     int64_t waves;
 };
 
+// Whether a gate leaves nothing: its factor is 0 as the chunks and the step compute it.
+__device__ __forceinline__ bool resets(float g) { return __builtin_amdgcn_exp2f(g * static_cast<float>(kLog2E)) == 0.0f; }
+
 // dg: one wave per (stream, head, segment), 256 tokens at a time from the segment's end, in float64. A token that
 // resets has a gradient of 0, and with it the sums start afresh: nothing of a later sequence, be it large
 // or not finite, is in an earlier one's. Where the sum from the end is not finite, that from the front,
@@ -1004,20 +1007,20 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
         for (int u = 0; u < kU; ++u) {
             const int t = t1 - 1 - lane - u * kWave;
             const double x = t >= t_lo ? static_cast<double>(q[u]) - static_cast<double>(k[u]) : 0.0;
-            const uint64_t resets = __ballot(t >= t_lo && g[u] <= kGateMin);
+            const uint64_t cuts = __ballot(t >= t_lo && resets(g[u]));
             double y;
-            if (resets == 0) {
+            if (cuts == 0) {
                 const double sum = scan_d(x);
                 y = carry + sum;
                 carry += uniform_d(sum, kWave - 1);
             } else {
                 // A piece ends with the token that resets, the first one in time: the next starts behind it, from 0.
                 y = 0.0;
-                pieces(resets << 1, x, lane, [&](int from, int to, double sum) {
+                pieces(cuts << 1, x, lane, [&](int from, int to, double sum) {
                     if (lane >= from && lane < to) y = carry + sum;
-                    carry = to < kWave || (resets >> (kWave - 1)) != 0 ? 0.0 : carry + uniform_d(sum, kWave - 1);
+                    carry = to < kWave || (cuts >> (kWave - 1)) != 0 ? 0.0 : carry + uniform_d(sum, kWave - 1);
                 });
-                if ((resets >> lane) & 1) y = 0.0;
+                if ((cuts >> lane) & 1) y = 0.0;
             }
             const float d = t < len ? static_cast<float>(y) : 0.0f;
             lost |= t >= t_lo && !(fabsf(d) < INFINITY);
@@ -1041,10 +1044,10 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
     for (int t0 = t_lo; t0 < end; t0 += kWave) {
         const int t = t0 + lane, at = min(t, end - 1);
         const double x = t < end ? static_cast<double>(p.dk[bh * T + at]) - static_cast<double>(p.dq[bh * T + at]) : 0.0;
-        const uint64_t resets = __ballot(t < end && gates[at * p.g_t] <= kGateMin);
+        const uint64_t cuts = __ballot(t < end && resets(gates[at * p.g_t]));
         double y = 0.0;
-        if (resets & 1) start = 0.0;
-        pieces(resets, x, lane, [&](int from, int to, double sum) {   // a piece starts with the token that resets, from 0
+        if (cuts & 1) start = 0.0;
+        pieces(cuts, x, lane, [&](int from, int to, double sum) {   // a piece starts with the token that resets, from 0
             if (from > 0) start = 0.0;
             const double before = dpp_d<0x138, 0xF>(sum);   // wave_shr:1: the sum of the tokens before the lane's
             if (lane >= from && lane < to) y = start + (lane == from ? 0.0 : before);

@@ -188,3 +188,17 @@ def test_gate_gradients_of_packed_sequences(T):
     both = run(T)
     assert (both[:, T // 2] == 0).all()
     assert torch.allclose(both[:, :T // 2], alone, rtol=0, atol=1e-5 * float(alone.abs().max()))
+
+
+def test_gates_whose_factor_is_zero():
+    """exp(g) below float32's range cuts like a reset: a gradient of 0, and nothing of the later tokens before it."""
+    x = make(1, 300, 2, 1, 16, 24, torch.float32, gate=6.0)
+    x["g"][:, 150] = -90.0
+    x["g"][:, 151] = -200.0
+    x["g"][:, 40] = -9999.0
+    x["v"][0, 200, :, 3] = INF
+    got, want, mag = gate_gradients(x, torch.float32)
+    assert (got[:, [40, 150, 151]] == 0).all()
+    assert torch.isfinite(got[:, :200]).all()
+    n = 16 + 24 + 96 + 4
+    near("dg", got[:, :150], want[:, :150], mag[:, :150], n, False)
