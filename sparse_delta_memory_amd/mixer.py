@@ -63,6 +63,11 @@ class Mixer:
         wa, wb, ra, rb = self.score_rows(scores)
         return q, k, v, gates, *slot_topk(wa, wb, self.W), *slot_topk(ra, rb, self.R), gate, beta, u
 
+    def check_positions(self, fn, start, T):
+        """norm_rope takes a position outside its table to the nearest row: tokens there would turn by the wrong angles."""
+        if start < 0 or start + T > self.table.shape[0]:
+            raise ValueError("Mixer.%s: positions %d .. %d of a table of %d" % (fn, start, start + T - 1, self.table.shape[0]))
+
     def bank(self, P, dtype=torch.float32, device="cuda"):
         return torch.zeros((P * self.n * self.n, self.hd), dtype=dtype, device=device)
 
@@ -92,6 +97,7 @@ class Mixer:
         P, T = x.shape[:2]
         if T % self.C:
             raise ValueError("Mixer.prompt: %d tokens are no whole chunks of %d" % (T, self.C))
+        self.check_positions("prompt", start, T)
         pos = (torch.arange(start, start + T, dtype=torch.int32, device=x.device)).repeat(P)
         q, k, v, gates, *sparse = self.rows(x, pos)
         seq = lambda t: t.unflatten(0, (P, T))  # noqa: E731
@@ -102,6 +108,7 @@ class Mixer:
     def token(self, x, bank, state, pos):
         """One token of every stream: x [P, model] -> y [P, heads * d + hd]; the bank and the state are updated in place."""
         P = x.shape[0]
+        self.check_positions("token", pos, 1)
         q, k, v, gates, *sparse = self.rows(x[:, None], torch.full((P,), pos, dtype=torch.int32, device=x.device))
         o = glr_step(q, k, v, gates, state)
         return torch.cat([o.flatten(1).float(), self.sparse(bank, P, 1, 1, *sparse)], 1)

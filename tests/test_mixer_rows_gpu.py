@@ -52,3 +52,14 @@ def test_rows_of_another_count_than_the_shape():
             sdm.slot_topk(rows, rows, 4, shape=shape)
     with pytest.raises(ValueError):
         sdm.slot_topk_backward(torch.zeros(40, 4, device="cuda"), idx[:40].contiguous(), a[:40], a[:40], shape=shape)
+
+
+def test_positions_past_the_table():
+    m = mixer.Mixer(C=8, positions=32)
+    x = torch.randn(1, 40, m.w.shape[0], device="cuda").bfloat16()
+    bank = m.bank(1)
+    _, state = m.prompt(x[:, :32], bank)
+    for bad in (lambda: m.prompt(x, bank), lambda: m.prompt(x[:, :8], bank, start=25), lambda: m.token(x[:, 0], bank, state, 32),
+                lambda: m.token(x[:, 0], bank, state, -1)):
+        with pytest.raises(ValueError):
+            bad()
