@@ -47,13 +47,13 @@
 // state, and the main kernel starts every segment from the state before it, made up of the start and the
 // segments before (by itself when they are few, else a kernel chains them).
 //
-// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): o in 213 us, 2.6 TB/s of its 547 MB: 146 us
-// of main kernel and 70 of the segments' states, which read k and v once more. Per chunk and compute unit
-// the main kernel's 776 matrix instructions take 3100 cycles, its vector instructions (cutting states and z
-// into parts, scaling, addresses) about 3600, its LDS reads and writes about 4000, and a chunk passes in
-// 6500: no one of them alone, but what is left of them beside each other with four waves per unit of the
-// vector hardware. The backward (718 us) is three such passes and two of states; dq and dk take three
-// parts everywhere and read a fourth row for the dots, 262 us each.
+// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): o in 232 us, 2.4 TB/s of its 547 MB: about 165 us
+// of main kernel and 65 of the segments' states, which read k and v once more. Counted per chunk and compute unit, the main
+// kernel's 968 matrix instructions keep the matrix units busy for 3900 cycles, its 4980 other vector instructions
+// (cutting states, scores and z into parts, scaling, addresses) take 5000 cycles of issue and LDS is busy for 4400 (1600 of
+// them bank conflicts); a chunk passes in 11200. So the three overlap little: with two blocks per unit, each between
+// the same barriers, they mostly follow each other. The backward (736 us) is three such passes and two of states; dq
+// and dk read a fourth row for the dots, 215 us each beside 166 for dv.
 #include <hip/hip_runtime.h>
 
 #include "mixer_device.hpp"
@@ -1166,15 +1166,15 @@ Rows rows_of(const void* p, int64_t b, int64_t t, int64_t h, int width, int per,
 
 // Segments of the time axis: 256 blocks of (stream, head, segment), one per compute unit, if there are that many chunks. A
 // second block per unit fills the first one's waits but doubles the states that the first kernel writes and the others read:
-// it pays where segments stay long. Forward, microseconds at 512 and at 256 blocks, heads of 128: 8 x 4096 tokens x 16 heads
-// 236 and 253 (segments of 1024 and 2048 tokens); 1 x 16384 x 8 82 and 75 (256 and 512); 1 x 4096 x 16 61 and 57 (128 and
-// 256); 16 x 256 x 16, whole rows at 256 blocks, 36 and 26. Down to single chunks: 4 x 1000 x 4 (width 100) with segments
-// of 64, 128 and 256 tokens at least 53, 62 and 114.
+// it pays where segments stay long. Microseconds at 512 and at 256 blocks, forward / backward, heads of 128: 8 x 4096 tokens
+// x 16 heads 230 / 722 and 258 / 803 (segments of 1024 and 2048 tokens); 1 x 16384 x 8 87 / 264 and 84 / 262 (256 and 512);
+// 1 x 4096 x 16 63 / 191 and 60 / 174 (128 and 256); 16 x 256 x 16, whole rows at 256 blocks, 37 / 133 and 29 / 97. Down to
+// single chunks: 4 x 1000 x 4 (width 100) with segments of 64, 128 and 256 tokens at least 45 / 125, 56 / 180 and 85 / 287.
 constexpr int kGlrUnits = 256;
 constexpr int kGlrLongSeg = 1024;
 // Up to so many segments, each block adds up the segments before it by itself (half of them on average); past that a kernel
-// chains the states in place. 8 x 4096 x 16, 4 segments: 236 by themselves, 264 chained; 2 x 2048 x 16 backward, 16
-// segments: 531 and 179.
+// chains the states in place. 8 x 4096 x 16, 4 segments: 230 by themselves, 248 chained; 2 x 2048 x 16 backward, 8
+// segments: 230 and 174.
 constexpr int kGlrOwnChain = 4;
 struct SegPlan {
     int nseg, seg;
