@@ -617,7 +617,7 @@ typedef struct sdm_glr_grad {
 
 /* The backward of sdm_glr_forward (io's o and last are not used; its workspace is of the backward size). Heads that
  * share a query and key head add their gradients in head order. No atomics: the bits are the same every run. A gate whose
- * factor is 0 in float32 has a gradient of 0. dg is a sum over one side of its token, of q . dq - k . dk between two resets or a row's ends:
+ * factor is 0 in float32 has a gradient of 0, and so has the first one when there is no `state`. dg is a sum over one side of its token, of q . dq - k . dk between two resets or a row's ends:
  * where values that are not finite lie on both sides, it is NaN. (With d_state NULL also before the first key or
  * value that is not finite, up to a reset.) Its error is that of float32 values of the size of what is added up there. */
 sdm_status sdm_glr_backward(const sdm_glr_io* io, const sdm_glr_grad* grad, hipStream_t st);

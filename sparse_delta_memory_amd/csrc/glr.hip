@@ -974,7 +974,7 @@ struct GateGrad {
 __device__ __forceinline__ bool resets(float g) { return __builtin_amdgcn_exp2f(g * static_cast<float>(kLog2E)) == 0.0f; }
 
 // dg: one wave per (stream, head, segment), 256 tokens at a time from the segment's end, in float64. A token that
-// resets has a gradient of 0, and with it the sums start afresh: nothing of a later sequence, be it large
+// resets, or has no state before it, has a gradient of 0, and with it the sums start afresh: nothing of a later sequence, be it large
 // or not finite, is in an earlier one's. Where the sum from the end is not finite, that from the front,
 //     dg_t = dg_{t0} - sum_{t0 <= s < t} (q_s . dq_s - k_s . dk_s),
 // may be, since what makes q . dq infinite or NaN is a key or value behind t; dg_{t0} is <S, R> of the segment before,
@@ -992,6 +992,7 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
     const int t_lo = si * p.seg, t_hi = min(T, t_lo + p.seg);
     const float* gates = p.g + b * p.g_b + h * p.g_h;
     float* out = p.dg + b * T * p.H + h;
+    const int nothing = p.state == nullptr ? 0 : -1;   // the token with no state before it, whatever its gate
     double carry = p.cross[bh * p.nseg + si];
     bool lost = false;
     for (int t1 = t_hi; t1 > t_lo; t1 -= kU * kWave) {   // lane l takes tokens t1 - 1 - l - 64 u
@@ -1007,7 +1008,7 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
         for (int u = 0; u < kU; ++u) {
             const int t = t1 - 1 - lane - u * kWave;
             const double x = t >= t_lo ? static_cast<double>(q[u]) - static_cast<double>(k[u]) : 0.0;
-            const uint64_t cuts = __ballot(t >= t_lo && resets(g[u]));
+            const uint64_t cuts = __ballot(t >= t_lo && (resets(g[u]) || t == nothing));
             double y;
             if (cuts == 0) {
                 const double sum = scan_d(x);
@@ -1044,7 +1045,7 @@ __global__ __launch_bounds__(256) void glr_gate_grad_kernel(GateGrad p) {
     for (int t0 = t_lo; t0 < end; t0 += kWave) {
         const int t = t0 + lane, at = min(t, end - 1);
         const double x = t < end ? static_cast<double>(p.dk[bh * T + at]) - static_cast<double>(p.dq[bh * T + at]) : 0.0;
-        const uint64_t cuts = __ballot(t < end && resets(gates[at * p.g_t]));
+        const uint64_t cuts = __ballot(t < end && (resets(gates[at * p.g_t]) || t == nothing));
         double y = 0.0;
         if (cuts & 1) start = 0.0;
         pieces(cuts, x, lane, [&](int from, int to, double sum) {   // a piece starts with the token that resets, from 0

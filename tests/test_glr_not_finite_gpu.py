@@ -202,3 +202,13 @@ def test_gates_whose_factor_is_zero():
     assert torch.isfinite(got[:, :200]).all()
     n = 16 + 24 + 96 + 4
     near("dg", got[:, :150], want[:, :150], mag[:, :150], n, False)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 64, 333])
+def test_the_first_gate_without_a_state(dtype, T):
+    """From no state the first gate scales nothing: its gradient is 0, not the rounding of the sums behind it."""
+    x = make(3, T, 4, 2, 32, 40, DT[dtype], state=False, gate=6.0, lens=[T, 0, T])
+    got, want, mag = gate_gradients(x, DT[dtype])
+    assert (got[:, 0] == 0).all() and (want[:, 0] == 0).all()
+    same("dg", got, want, mag, 32 + 40 + 96 + T // 64, False)
