@@ -83,6 +83,11 @@ def _output(stream, shape, dtype, dev):
     return t
 
 
+def _output_like(stream, t):
+    """The same with t's shape and type (on the current stream by the shortest way: small calls are this side's time)."""
+    return t.new_empty(t.shape) if stream is None else _output(stream, t.shape, t.dtype, t.device)
+
+
 def _call(fn, dev, stream, *packed, workspace=None):
     """Enqueues fn. workspace: the caller's, which the stream still needs when the call returns."""
     if stream is not None:
@@ -182,9 +187,9 @@ def norm_rope(q, k, q_weight=None, k_weight=None, positions=None, table=None, in
     if q is None and k is None:
         raise TypeError("norm_rope: q or k is required")
     if q_out is None and q is not None:
-        q_out = _output(stream, q.shape, q.dtype, q.device)
+        q_out = _output_like(stream, q)
     if k_out is None and k is not None:
-        k_out = _output(stream, k.shape, k.dtype, k.device)
+        k_out = _output_like(stream, k)
     dev, io = _norm_rope_io("norm_rope", q, k, q_weight, k_weight, positions, table, interleaved, eps, q_out, k_out)
     _call(_lib.load().sdm_norm_rope, dev, stream, io)
     return q_out, k_out
@@ -197,8 +202,8 @@ def norm_rope_backward(d_q, d_k, q, k, q_weight=None, k_weight=None, positions=N
     fn = "norm_rope_backward"
     if q is None and k is None:
         raise TypeError("%s: q or k is required" % fn)
-    dq = None if q is None else _output(stream, q.shape, q.dtype, q.device)
-    dk = None if k is None else _output(stream, k.shape, k.dtype, k.device)
+    dq = None if q is None else _output_like(stream, q)
+    dk = None if k is None else _output_like(stream, k)
     dev, io = _norm_rope_io(fn, q, k, q_weight, k_weight, positions, table, interleaved, eps, dq, dk)
     one = q if q is not None else k
     grads = []
@@ -285,7 +290,7 @@ def slot_topk_backward(d_val, idx, a, b, scale=1.0, shape=None, stream=None):
     _shape(fn, "d_val", d_val, idx.shape)
     _same(fn, a, d_val)
     dev, io = _slot_io(fn, a, b, K, idx, None, scale, shape)
-    da, db = _output(stream, a.shape, a.dtype, dev), _output(stream, b.shape, b.dtype, dev)
+    da, db = _output_like(stream, a), _output_like(stream, b)
     g = _lib.pack_slot_topk_grad(d_val.data_ptr(), da.data_ptr(), db.data_ptr(), a.shape[-1], b.shape[-1])
     _call(_lib.load().sdm_slot_topk_backward, dev, stream, io, g)
     return da, db
@@ -347,7 +352,7 @@ def glr_forward(q, k, v, g, scale=None, state=None, lens=None, out=None, last=No
     glr_workspace_bytes (allocated per call by default)."""
     if q.dim() == 4 and v.dim() == 4:
         if out is None:
-            out = _output(stream, v.shape, v.dtype, v.device)
+            out = _output_like(stream, v)
         if last is None:
             last = _output(stream, (q.shape[0], v.shape[2], q.shape[3], v.shape[3]), torch.float32, v.device)
     dev, io, keep = _glr_io("glr_forward", q, k, v, g, scale, state, lens, out, last, 0, workspace, stream)
@@ -391,7 +396,7 @@ def glr_step(q, k, v, g, state, scale=None, new_state=None, slots=None, out=None
     B, Hk, dk = q.shape
     H, dv = v.shape[1], v.shape[2]
     if out is None:
-        out = _output(stream, v.shape, v.dtype, v.device)
+        out = _output_like(stream, v)
     if new_state is None:
         new_state = state
     dev = _same(fn, q, k, v, g, state, new_state, slots, out)
