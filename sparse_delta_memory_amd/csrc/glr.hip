@@ -26,16 +26,17 @@
 // 4096 tokens x 16 heads of 128, then at one block per compute unit.) The products are formed transposed,
 // so that a lane holds four consecutive columns of a result row: 8-byte stores, and row dots that need two
 // lane exchanges. Tiles of x, y and z go from global memory to LDS without registers between, 16-byte
-// pieces permuted per row against bank conflicts; x's next tile is loaded once the scores are done, y's and z's at the chunk's end, and the
-// second block of the compute unit works meanwhile. That takes 128 registers (205 with a chunk's loads
+// pieces permuted per row against bank conflicts; x's next tile is loaded once the scores are done, y's and
+// z's at the chunk's end, and the second block of the compute unit works meanwhile. That takes 128 registers (205 with a chunk's loads
 // held in registers and one block: 253 us; 151 so).
 //
 // Numbers. Products of bfloat16 inputs are exact; a float32 factor (decayed score, state, decayed z) is
 // cut into three bfloat16 parts by truncation, which hold all 24 bits, and multiplied part by part. (For o and dv,
 // which are rounded to bfloat16 in the end, two parts of the scores and of the state that meets x take 6 % less,
-// 8 x 4096 x 16 forward 218 against 233 us, but sums that cancel show their error of up to 2^-15.) float32 inputs go through the float32 matrix instructions. Gates are summed in float64 per
-// chunk (one wave, one token per lane) and only differences of a chunk's sums are rounded to float32, so
-// neither long rows nor a reset (a gate of -infinity counts as -10000) cost digits.
+// 8 x 4096 x 16 forward 218 against 233 us, but sums that cancel show their error of up to 2^-15.) float32
+// inputs go through the float32 matrix instructions. Gates are summed in float64 per chunk (one wave, one token
+// per lane) and only differences of a chunk's sums are rounded to float32, so neither long rows nor a reset (a
+// gate of -infinity counts as -10000) cost digits.
 //
 // What is not finite reaches what it is part of by the recurrence and nothing else: no token before it, nothing past a
 // reset, although a tile product multiplies it by zeros there. Factors of 0 are applied by a multiplication

@@ -13,10 +13,10 @@
 // do, so one sweep of ballots moves the few entries at or above it to LDS, and sorting networks over the 64
 // lanes (compare-exchange across lanes, no LDS for most steps) order them; a bfloat16 entry and its place
 // are one 32-bit word there. Reading the scores would take 105 us at 65536 tokens of 2 x 2048 bfloat16
-// scores, K = 32; it takes 152, the issue of about 1400 vector instructions per token. Rows of equal scores are ordered 64
-// entries at a time, the whole row swept again for each: both rows constant 2500 us, one row all -infinity 1360
-// (scores cut off at 0, half of them equal but not among the best, 141). (With 32-bit keys, 64-bit
-// networks and the ordering inside the unrolled sweep, so that it did not fit the instruction cache: 283.)
+// scores, K = 32; it takes 152, the issue of about 1400 vector instructions per token. (With 32-bit keys, 64-bit
+// networks and the ordering inside the unrolled sweep, so that it did not fit the instruction cache: 283.) Rows
+// of equal scores are ordered 64 entries at a time, the whole row swept again for each: both rows constant
+// 2500 us, one row all -infinity 1360 (scores cut off at 0, half of them equal but not among the best, 141).
 #include <hip/hip_runtime.h>
 
 #include <climits>
