@@ -645,6 +645,82 @@ typedef struct sdm_glr_step_io {
  * finite or not). One kernel on st. */
 sdm_status sdm_glr_step(const sdm_glr_step_io* io, hipStream_t st);
 
+/* The gated delta rule: a dense state per stream and head that takes of every value what it does not predict yet. */
+typedef struct sdm_gdr_io {
+    const void* q;          /* [B, T, Hk, dk]: element (b, t, h) at q + b q_b + t q_t + h q_h, dk contiguous columns */
+    const void* k;          /* [B, T, Hk, dk] */
+    const void* v;          /* [B, T, H, dv] */
+    const float* g;         /* [B, T, H] log gates (<= 0; -infinity, or anything at or below -10000, resets the state) */
+    const float* beta;      /* [B, T, H] what share of the missing part a token writes (0..1; up to 2 / |k|^2 is stable) */
+    int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, g_b, g_t, g_h, e_b, e_t, e_h;   /* e: of beta */
+    const float* state;     /* [B, H, dk, dv] contiguous, the state before the first token (NULL: zero), aligned as in sdm_glr_io */
+    const int32_t* lens;    /* [B] tokens of each stream (NULL: T); a value outside 0..T is taken to the nearest.
+                               Later tokens are not read, leave the state alone and get zero outputs */
+    void* o;                /* OUT of sdm_gdr_forward [B, T, H, dv], strided */
+    int64_t o_b, o_t, o_h;
+    float* last;            /* OUT of sdm_gdr_forward [B, H, dk, dv] contiguous: the state after the last token (NULL: skipped;
+                               must not be `state`) */
+    int32_t B, T;           /* >= 0 */
+    int32_t H, Hk;          /* value heads, and query / key heads: H a multiple of Hk; value head h uses head h / (H / Hk) */
+    int32_t dk, dv;         /* 1..128 */
+    int32_t dtype;          /* sdm_dtype of q, k, v, o and their gradients */
+    float scale;
+    void* workspace;        /* sdm_gdr_workspace() bytes, 256-byte aligned (may be NULL when that is 0) */
+    size_t workspace_bytes;
+} sdm_gdr_io;
+
+/*
+ * Per stream and head, from S = state:
+ *   u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),  S_t = exp(g_t) S_{t-1} + k_t u_t^T,  o_t = scale S_t^T q_t.
+ * States and sums are float32; of bfloat16 inputs every product is exact, and a float32 factor enters a matrix product as
+ * three bfloat16 parts, all its 24 bits. A gate that resets, and gates whose product is 0 in float32, leave nothing of the
+ * state before them, finite or not. A value that is not finite makes what the rule takes it into infinity or NaN and
+ * nothing else: no earlier token, stream or head, nothing past a reset.
+ * Requires B * H <= 2^20, T <= 2^30, B * T * H <= 2^31 - 1.
+ */
+sdm_status sdm_gdr_forward(const sdm_gdr_io* io, hipStream_t st);
+size_t sdm_gdr_workspace(const sdm_gdr_io* io, int32_t backward);
+
+typedef struct sdm_gdr_grad {
+    const void* d_o;        /* [B, T, H, dv] gradients of o, strided */
+    int64_t do_b, do_t, do_h;
+    const float* d_last;    /* [B, H, dk, dv] contiguous gradient of the last state (NULL: zero) */
+    void* dq;               /* OUT [B, T, Hk, dk] contiguous, in dtype */
+    void* dk;               /* OUT [B, T, Hk, dk] */
+    void* dv;               /* OUT [B, T, H, dv] */
+    float* dg;              /* OUT [B, T, H] float32 */
+    float* dbeta;           /* OUT [B, T, H] float32 */
+    float* d_state;         /* OUT [B, H, dk, dv] float32: the gradient of `state` (NULL: skipped; must not be d_last or
+                               `state`) */
+} sdm_gdr_grad;
+
+/* The backward of sdm_gdr_forward (io's o and last are not used; its workspace is of the backward size). */
+sdm_status sdm_gdr_backward(const sdm_gdr_io* io, const sdm_gdr_grad* grad, hipStream_t st);
+
+/* One token of many requests. */
+typedef struct sdm_gdr_step_io {
+    const void* q;          /* [B, Hk, dk]: element (b, h) at q + b q_b + h q_h */
+    const void* k;
+    const void* v;          /* [B, H, dv] */
+    const float* g;         /* [B, H] */
+    const float* beta;      /* [B, H] */
+    int64_t q_b, q_h, k_b, k_h, v_b, v_h, g_b, g_h, e_b, e_h;
+    const float* state;     /* [rows, H, dk, dv] contiguous */
+    float* new_state;       /* OUT, laid out the same; may be `state` */
+    int64_t rows;
+    const int32_t* slots;   /* [B] row of each request (NULL: row b). A request whose row is outside 0..rows-1 is left
+                               out: its output is 0 and no state is read or written. Rows must be distinct */
+    void* o;                /* OUT [B, H, dv], strided */
+    int64_t o_b, o_h;
+    int32_t B, H, Hk, dk, dv;   /* as in sdm_gdr_io; dk, dv 1..128 */
+    int32_t dtype;
+    float scale;
+} sdm_gdr_step_io;
+
+/* The rule by one token: the state is read once and written once (a gate that resets leaves nothing of it, finite or
+ * not). One kernel on st. */
+sdm_status sdm_gdr_step(const sdm_gdr_step_io* io, hipStream_t st);
+
 /* Static text for a status code. */
 const char* sdm_status_string(sdm_status s);
 

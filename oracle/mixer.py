@@ -186,3 +186,125 @@ def slot_topk_backward(d_val, idx, a, b, scale):
             out[2][t, x] += m[c]
             out[3][t, z] += m[c]
     return out
+
+
+def _heads(x, H):
+    """Query or key heads [.., Hk, d] of every value head."""
+    return np.repeat(x.astype(np.float64), H // x.shape[-2], axis=-2)
+
+
+def _kept(a, x):
+    """a x for a factor per row and head; 0 where the factor is 0, whatever x."""
+    return np.where(a[..., None, None] > 0, a[..., None, None] * np.where(a[..., None, None] > 0, x, 0.0), 0.0)
+
+
+def gdr_forward(q, k, v, g, beta, scale, state=None, lens=None, chunk=64):
+    """(o, last, |o|, |last|) of u = beta (v - S'^T k), S = S' + k u^T, o = scale S^T q, with S' = exp(g) S: q, k [B, T, Hk, dk],
+    v [B, T, H, dv], g and beta [B, T, H].
+
+    The magnitudes bound what the rounding errors of an evaluation add up to, in units of one rounding: per column of a
+    state, the root of the sum of squares of the norms that every token's step handles (its errors are independent
+    in sign), decayed as the state is; later steps do not enlarge them where beta |k|^2 <= 2. (o: times |q|.) They are scaled up by
+    what solving a chunk's tokens enlarges, the square of the norm of (1 + A diag(beta))^-1, A_ij = exp(g_{j+1} + .. + g_i) k_i . k_j."""
+    B, T, _, dk = q.shape
+    H, dv = v.shape[2:]
+    live = _live(lens, B, T)
+    q, k, v = _heads(q, H), _heads(k, H), v.astype(np.float64)
+    S = np.zeros((B, H, dk, dv)) if state is None else np.array(state, dtype=np.float64)
+    E2 = (S * S).sum(2)                                       # [B, H, dv]
+    amp = np.ones((B, H))
+    o, mo = np.zeros((B, T, H, dv)), np.zeros((B, T, H, dv))
+    for t in range(T):
+        on = live[:, t]
+        a, be = np.exp(g[:, t].astype(np.float64)), beta[:, t].astype(np.float64)
+        kk = k[:, t]
+        S1 = _kept(a, S)
+        pred = np.einsum("bhk,bhkv->bhv", kk, S1)
+        u = be[..., None] * (v[:, t] - pred)
+        S1 = S1 + kk[..., None] * u[:, :, None]
+        n = np.sqrt((kk * kk).sum(-1))[..., None]
+        local = np.abs(be)[..., None] * n * (np.abs(v[:, t]) + n * np.sqrt((S1 * S1).sum(2)) + np.abs(u))
+        E1 = _kept(a * a, E2[..., None])[..., 0] + local ** 2 + (S1 * S1).sum(2)
+        S, E2 = np.where(on[:, None, None, None], S1, S), np.where(on[:, None, None], E1, E2)
+        o[:, t] = np.where(on[:, None, None], scale * np.einsum("bhk,bhkv->bhv", q[:, t], S), 0.0)
+        mo[:, t] = np.where(on[:, None, None], abs(scale) * np.sqrt((q[:, t] ** 2).sum(-1))[..., None] * np.sqrt(E2), 0.0)
+        if t % chunk == chunk - 1 or t == T - 1:
+            amp = np.maximum(amp, _solve_norm(k, g, beta, live, t - t % chunk, t + 1))
+    amp = amp[:, None, :, None]
+    return o, S, mo * amp, np.sqrt(E2)[:, :, None] * amp[:, 0, :, :, None] * np.ones((1, 1, dk, 1))
+
+
+def _solve_norm(k, g, beta, live, t0, t1):
+    on = live[:, t0:t1, None]
+    kk = np.where(on[..., None], k[:, t0:t1], 0.0).transpose(0, 2, 1, 3)
+    G = np.cumsum(np.where(on, np.maximum(g[:, t0:t1].astype(np.float64), -1e4), 0.0), 1).transpose(0, 2, 1)
+    be = np.where(on, beta[:, t0:t1], 0.0).transpose(0, 2, 1).astype(np.float64)
+    n = t1 - t0
+    D = np.exp(np.minimum(G[..., :, None] - G[..., None, :], 0.0)) * np.tril(np.ones((n, n)), -1)
+    A = D * np.einsum("bhik,bhjk->bhij", kk, kk) * be[..., None, :]
+    return np.maximum(np.abs(np.linalg.inv(np.eye(n) + A)).sum(-1).max(-1) ** 2, 1.0)
+
+
+def gdr_backward(d_o, q, k, v, g, beta, scale, state=None, d_last=None, lens=None, chunk=64):
+    """Gradients from the chain rule, token by token: (grads, magnitudes), dicts of dq, dk, dv, dg, dbeta and dstate. Magnitudes
+    as in gdr_forward; dg's are of the sums a chunked evaluation adds up to it, q . dq and v . dv of the later tokens of its chunk."""
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    live = _live(lens, B, T)
+    fold = lambda x: x.reshape(B, T, Hk, H // Hk, dk).sum(3)  # noqa: E731
+    q, k, v, d_o = _heads(q, H), _heads(k, H), v.astype(np.float64), d_o.astype(np.float64)
+    S = np.zeros((B, H, dk, dv)) if state is None else np.array(state, dtype=np.float64)
+    E2, amp = (S * S).sum(2), np.ones((B, H))
+    seen = []
+    for t in range(T):
+        on = live[:, t]
+        a, be, kk = np.exp(g[:, t].astype(np.float64)), beta[:, t].astype(np.float64), k[:, t]
+        S1 = _kept(a, S)
+        r = v[:, t] - np.einsum("bhk,bhkv->bhv", kk, S1)
+        S2 = S1 + kk[..., None] * (be[..., None] * r)[:, :, None]
+        n = np.sqrt((kk * kk).sum(-1))[..., None]
+        local = np.abs(be)[..., None] * n * (np.abs(v[:, t]) + n * np.sqrt((S2 * S2).sum(2)) + np.abs(be[..., None] * r))
+        E1 = _kept(a * a, E2[..., None])[..., 0] + local ** 2 + (S2 * S2).sum(2)
+        seen.append((S1, S2, r, np.sqrt(E2), np.sqrt(E1)))
+        S, E2 = np.where(on[:, None, None, None], S2, S), np.where(on[:, None, None], E1, E2)
+        if t % chunk == chunk - 1 or t == T - 1:
+            amp = np.maximum(amp, _solve_norm(k, g, beta, live, t - t % chunk, t + 1))
+    z = lambda *s: np.zeros(s)  # noqa: E731
+    r_ = dict(dq=z(B, T, H, dk), dk=z(B, T, H, dk), dv=z(B, T, H, dv), dg=z(B, T, H), dbeta=z(B, T, H))
+    m = {n: np.zeros_like(x) for n, x in r_.items()}
+    R = z(B, H, dk, dv) if d_last is None else np.array(d_last, dtype=np.float64)
+    F2 = (R * R).sum(2)
+    rest = z(B, H)
+    for t in range(T - 1, -1, -1):
+        on = live[:, t]
+        a, be, kk, qq, do = np.exp(g[:, t].astype(np.float64)), beta[:, t].astype(np.float64), k[:, t], q[:, t], d_o[:, t] * scale
+        S1, S2, r, E0, E = seen[t]
+        norm = lambda x: np.sqrt((x * x).sum(2))  # noqa: E731
+        nk, nq = (np.sqrt((x * x).sum(-1))[..., None] for x in (kk, qq))
+        if t % chunk == chunk - 1 or t == T - 1:
+            rest = (E0 * np.sqrt(F2)).sum(-1) + (E * np.sqrt(F2)).sum(-1)
+        Rt = R + qq[..., None] * do[:, :, None]
+        du = np.einsum("bhk,bhkv->bhv", kk, Rt)
+        d = be[..., None] * du
+        u = be[..., None] * r
+        F = np.sqrt(F2 + (nq * np.abs(do)) ** 2 + (nk * np.abs(d)) ** 2 + (Rt * Rt).sum(2))
+        new = dict(dq=np.einsum("bhkv,bhv->bhk", S2, do), dk=np.einsum("bhkv,bhv->bhk", Rt, u) - np.einsum("bhkv,bhv->bhk", S1, d),
+                   dv=d, dbeta=(du * r).sum(-1))
+        ab = np.abs(be)[..., None]
+        one = np.ones((1, 1, dk))
+        mags = dict(dq=(E * np.abs(do)).sum(-1)[..., None] * one, dv=ab * nk * F, dbeta=(nk * F * np.abs(r) + np.abs(du) * (np.abs(v[:, t]) + nk * E)).sum(-1),
+                    dk=(F * np.abs(u) + E * np.abs(d) + 2 * ab * nk * E * F).sum(-1)[..., None] * one)
+        rest = rest + nq[..., 0] * mags["dq"][..., 0] + (np.abs(v[:, t]) * mags["dv"]).sum(-1)
+        mags["dg"] = rest
+        R1 = Rt - kk[..., None] * d[:, :, None]
+        new["dg"] = (R1 * S1).sum((2, 3))   # S1 is already decayed; 0 past a reset
+        for n, x in new.items():
+            w = on.reshape((B,) + (1,) * (x.ndim - 1))
+            r_[n][:, t], m[n][:, t] = np.where(w, x, 0.0), np.where(w, mags[n], 0.0)
+        R = np.where(on[:, None, None, None], _kept(a, R1), R)
+        F2 = np.where(on[:, None, None], _kept(a * a, (F ** 2)[..., None])[..., 0], F2)
+    for n in ("dq", "dk"):
+        r_[n], m[n] = fold(r_[n]), fold(m[n] * amp[:, None, :, None])
+    m["dv"], m["dg"], m["dbeta"] = m["dv"] * amp[:, None, :, None], m["dg"] * amp[:, None], m["dbeta"] * amp[:, None]
+    r_["dstate"], m["dstate"] = R, np.sqrt(F2)[:, :, None] * amp[..., None, None] * np.ones((1, 1, dk, 1))
+    return r_, m

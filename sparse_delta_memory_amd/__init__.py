@@ -28,7 +28,7 @@ __all__ = ["P1Shape", "phase1", "phase1_pairs", "phase1_workspace_bytes", "alloc
            "alloc_dw_workspace", "DwPlan", "ReadPlan", "read_step", "gds_step", "gds_workspace_bytes", "alloc_gds_workspace", "gwr_step", "pa_step", "pa_workspace_bytes",
            "alloc_pa_workspace", "SdmError", "make_shape",
            "timing_events", "norm_rope", "norm_rope_backward", "rope_table", "slot_topk", "slot_topk_backward", "glr_forward",
-           "glr_backward", "glr_step", "glr_workspace_bytes"]
+           "glr_backward", "glr_step", "glr_workspace_bytes", "gdr_forward", "gdr_backward", "gdr_step", "gdr_workspace_bytes"]
 
 
 def make_shape(N, C, W, R, P=1, key_bits=16, stream_offset=0, first_partial=None, valid_last=None, tile_len=128,
@@ -464,4 +464,4 @@ def pa_step(grad, snap, p1, beta, d_dva, shape: P1Shape, ti: int, step_rows: int
 
 
 from .mixer_ops import (  # noqa: E402,F401
-    glr_backward, glr_forward, glr_step, glr_workspace_bytes, norm_rope, norm_rope_backward, rope_table, slot_topk, slot_topk_backward)
+    gdr_backward, gdr_forward, gdr_step, gdr_workspace_bytes, glr_backward, glr_forward, glr_step, glr_workspace_bytes, norm_rope, norm_rope_backward, rope_table, slot_topk, slot_topk_backward)

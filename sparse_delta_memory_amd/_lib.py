@@ -169,14 +169,37 @@ class GlrStepIO(ctypes.Structure):
         (f, ctypes.c_int32) for f in ("B", "H", "Hk", "dk", "dv", "dtype")] + [("scale", ctypes.c_float)]
 
 
+class GdrIO(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v", "g", "beta")] + [
+        (f, ctypes.c_int64) for f in ("q_b", "q_t", "q_h", "k_b", "k_t", "k_h", "v_b", "v_t", "v_h", "g_b", "g_t", "g_h", "e_b", "e_t", "e_h")] + [
+        ("state", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("o", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("o_b", "o_t", "o_h")] + [("last", ctypes.c_void_p)] + [
+        (f, ctypes.c_int32) for f in ("B", "T", "H", "Hk", "dk", "dv", "dtype")] + [
+        ("scale", ctypes.c_float), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GdrGrad(ctypes.Structure):
+    _fields_ = [("d_o", ctypes.c_void_p)] + [(f, ctypes.c_int64) for f in ("do_b", "do_t", "do_h")] + [
+        (f, ctypes.c_void_p) for f in ("d_last", "dq", "dk", "dv", "dg", "dbeta", "d_state")]
+
+
+class GdrStepIO(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v", "g", "beta")] + [
+        (f, ctypes.c_int64) for f in ("q_b", "q_h", "k_b", "k_h", "v_b", "v_h", "g_b", "g_h", "e_b", "e_h")] + [
+        ("state", ctypes.c_void_p), ("new_state", ctypes.c_void_p), ("rows", ctypes.c_int64), ("slots", ctypes.c_void_p),
+        ("o", ctypes.c_void_p), ("o_b", ctypes.c_int64), ("o_h", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("B", "H", "Hk", "dk", "dv", "dtype")] + [("scale", ctypes.c_float)]
+
+
 pack_norm_rope, pack_norm_rope_grad = packer(NormRopeIO), packer(NormRopeGrad)
 pack_slot_topk, pack_slot_topk_grad = packer(SlotTopkIO), packer(SlotTopkGrad)
 pack_glr, pack_glr_grad, pack_glr_step = packer(GlrIO), packer(GlrGrad), packer(GlrStepIO)
+pack_gdr, pack_gdr_grad, pack_gdr_step = packer(GdrIO), packer(GdrGrad), packer(GdrStepIO)
 
 EXPORTS = ["sdm_phase1_workspace", "sdm_phase1", "sdm_phase1_pairs", "sdm_dw_workspace", "sdm_dw_step", "sdm_dw_step_noalloc", "sdm_read_step",
            "sdm_gds_workspace", "sdm_gds_step", "sdm_gwr_step", "sdm_pa_workspace", "sdm_pa_step", "sdm_norm_rope",
            "sdm_norm_rope_workspace", "sdm_norm_rope_backward", "sdm_slot_topk", "sdm_slot_topk_backward", "sdm_glr_workspace",
-           "sdm_glr_forward", "sdm_glr_backward", "sdm_glr_step", "sdm_status_string", "sdm_last_error"]
+           "sdm_glr_forward", "sdm_glr_backward", "sdm_glr_step", "sdm_gdr_workspace", "sdm_gdr_forward", "sdm_gdr_backward", "sdm_gdr_step", "sdm_status_string", "sdm_last_error"]
 
 _lock = threading.Lock()
 _lib = None
@@ -225,7 +248,8 @@ def load() -> ctypes.CDLL:
         lib.sdm_pa_step.restype = ctypes.c_int
         for name, args in (("sdm_norm_rope", [NormRopeIO]), ("sdm_norm_rope_backward", [NormRopeIO, NormRopeGrad]),
                            ("sdm_slot_topk", [SlotTopkIO]), ("sdm_slot_topk_backward", [SlotTopkIO, SlotTopkGrad]),
-                           ("sdm_glr_forward", [GlrIO]), ("sdm_glr_backward", [GlrIO, GlrGrad]), ("sdm_glr_step", [GlrStepIO])):
+                           ("sdm_glr_forward", [GlrIO]), ("sdm_glr_backward", [GlrIO, GlrGrad]), ("sdm_glr_step", [GlrStepIO]),
+                           ("sdm_gdr_forward", [GdrIO]), ("sdm_gdr_backward", [GdrIO, GdrGrad]), ("sdm_gdr_step", [GdrStepIO])):
             fn = getattr(lib, name)
             fn.argtypes = [ctypes.c_void_p] * (len(args) + 1)   # the structure's bytes or a reference to it, and the stream
             fn.restype = ctypes.c_int
@@ -233,6 +257,8 @@ def load() -> ctypes.CDLL:
         lib.sdm_norm_rope_workspace.restype = ctypes.c_size_t
         lib.sdm_glr_workspace.argtypes = [ctypes.c_void_p, ctypes.c_int32]
         lib.sdm_glr_workspace.restype = ctypes.c_size_t
+        lib.sdm_gdr_workspace.argtypes = [ctypes.c_void_p, ctypes.c_int32]
+        lib.sdm_gdr_workspace.restype = ctypes.c_size_t
         lib.sdm_status_string.argtypes = [ctypes.c_int]
         lib.sdm_status_string.restype = ctypes.c_char_p
         lib.sdm_last_error.argtypes = []

@@ -61,7 +61,7 @@ struct DeviceSetup {
     hipError_t err = hipSuccess;
     int lds_max = 0;
 };
-DeviceSetup g_setup[3][kMaxDevices];
+DeviceSetup g_setup[4][kMaxDevices];
 
 int bank_kernels(const void** fns, int cap) {
     const int n = sdm::p1_lds_kernels(fns, cap);
@@ -81,8 +81,9 @@ hipError_t sdm::device_setup(int* lds_max, KernelFamily family) {
         d.err = hipDeviceGetAttribute(&lds, hipDeviceAttributeMaxSharedMemoryPerBlock, dev);
         if (d.err != hipSuccess) return;
         const void* fns[128];
-        const int n = family == KernelFamily::slots ? sdm::slot_lds_kernels(fns, 128)
+        const int n = family == KernelFamily::slots        ? sdm::slot_lds_kernels(fns, 128)
                       : family == KernelFamily::recurrence ? sdm::glr_lds_kernels(fns, 128)
+                      : family == KernelFamily::delta      ? sdm::gdr_lds_kernels(fns, 128)
                                                            : bank_kernels(fns, 128);
         for (int i = 0; i < n && d.err == hipSuccess; ++i) {
             // The dynamic limit is what the device holds beside the kernel's static LDS.

@@ -125,6 +125,31 @@ sdm_status check_glr(const sdm_glr_io* io, bool backward, const char* fn) {
     return SDM_OK;
 }
 
+sdm_status check_gdr(const sdm_gdr_io* io, bool backward, const char* fn) {
+    if (io == nullptr) return fail(SDM_EINVAL, "%s: io is NULL", fn);
+    if (io->B < 0 || io->T < 0 || io->T > (1 << 30)) return fail(SDM_ESHAPE, "%s: B = %d, T = %d (at most 2^30)", fn, io->B, io->T);
+    const sdm_status rc = check_heads(io->H, io->Hk, io->dk, io->dv, io->dtype, io->scale, fn);
+    if (rc != SDM_OK) return rc;
+    const int64_t bh = static_cast<int64_t>(io->B) * io->H;
+    if (bh > (1 << 20) || (io->T > 0 && bh > INT32_MAX / io->T))
+        return fail(SDM_ESHAPE, "%s: B H = %lld (at most 2^20), B T H at most 2^31 - 1", fn, static_cast<long long>(bh));
+    if (io->B == 0) return SDM_OK;
+    if (io->T > 0 && (io->q == nullptr || io->k == nullptr || io->v == nullptr || io->g == nullptr || io->beta == nullptr))
+        return fail(SDM_EINVAL, "%s: q, k, v, g and beta are required", fn);
+    const uintptr_t es = size_of(io->dtype);
+    for (const void* p : {io->q, io->k, io->v}) {
+        if (!aligned(p, es)) return fail(SDM_EALIGN, "%s: q, k or v is not element-aligned", fn);
+    }
+    if (!aligned(io->g, 4) || !aligned(io->beta, 4) || !aligned(io->lens, 4)) return fail(SDM_EALIGN, "%s: g, beta or lens is misaligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(io->state, sa)) return fail(SDM_EALIGN, "%s: state must be %d-byte aligned", fn, static_cast<int>(sa));
+    const size_t need = sdm::gdr_workspace_bytes(io, backward);
+    if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
+        return fail(SDM_EWORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, io->workspace == nullptr ? size_t(0) : io->workspace_bytes);
+    if (!aligned(io->workspace, 256)) return fail(SDM_EALIGN, "%s: workspace must be 256-byte aligned", fn);
+    return SDM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -257,6 +282,57 @@ sdm_status sdm_glr_step(const sdm_glr_step_io* io, hipStream_t st) {
     if (!aligned(io->state, sa) || !aligned(io->new_state, sa))
         return fail(SDM_EALIGN, "%s: state and new_state must be %d-byte aligned", fn, static_cast<int>(sa));
     return launched(sdm::glr_step_launch(io, st), fn);
+}
+
+size_t sdm_gdr_workspace(const sdm_gdr_io* io, int32_t backward) {
+    if (io == nullptr || io->B < 1 || io->T < 0 || io->T > (1 << 30) || io->H < 1 || io->Hk < 1 || io->H % io->Hk != 0 || io->dk < 1 || io->dk > 128 ||
+        io->dv < 1 || io->dv > 128 || !known(io->dtype))
+        return 0;
+    const int64_t bh = static_cast<int64_t>(io->B) * io->H;
+    if (bh > (1 << 20) || (io->T > 0 && bh > INT32_MAX / io->T)) return 0;
+    return sdm::gdr_workspace_bytes(io, backward != 0);
+}
+
+sdm_status sdm_gdr_forward(const sdm_gdr_io* io, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_gdr_forward";
+    sdm_status rc = check_gdr(io, false, fn);
+    if (rc != SDM_OK || io->B == 0) return rc;
+    if (io->T > 0 && io->o == nullptr) return fail(SDM_EINVAL, "%s: o is required", fn);
+    if (!aligned(io->o, size_of(io->dtype))) return fail(SDM_EALIGN, "%s: o is not element-aligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(io->last, sa)) return fail(SDM_EALIGN, "%s: last must be %d-byte aligned", fn, static_cast<int>(sa));
+    if (io->last != nullptr && io->last == io->state) return fail(SDM_EINVAL, "%s: last must not be state", fn);
+    rc = set_up(fn, sdm::KernelFamily::delta);
+    if (rc != SDM_OK) return rc;
+    return launched(sdm::gdr_forward_launch(io, st), fn);
+}
+
+sdm_status sdm_gdr_backward(const sdm_gdr_io*, const sdm_gdr_grad*, hipStream_t) { return fail(SDM_EUNSUPPORTED, "sdm_gdr_backward: not built yet"); }
+
+sdm_status sdm_gdr_step(const sdm_gdr_step_io* io, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_gdr_step";
+    if (io == nullptr) return fail(SDM_EINVAL, "%s: io is NULL", fn);
+    if (io->B < 0) return fail(SDM_ESHAPE, "%s: B = %d < 0", fn, io->B);
+    const sdm_status rc = check_heads(io->H, io->Hk, io->dk, io->dv, io->dtype, io->scale, fn);
+    if (rc != SDM_OK) return rc;
+    if (static_cast<int64_t>(io->B) * io->H > (1 << 20)) return fail(SDM_ESHAPE, "%s: B H exceeds 2^20", fn);
+    if (io->rows < 0 || (io->slots == nullptr && io->rows < io->B))
+        return fail(SDM_EINVAL, "%s: %lld state rows for %d requests", fn, static_cast<long long>(io->rows), io->B);
+    if (io->B == 0) return SDM_OK;
+    if (io->q == nullptr || io->k == nullptr || io->v == nullptr || io->g == nullptr || io->beta == nullptr || io->o == nullptr ||
+        (io->rows > 0 && (io->state == nullptr || io->new_state == nullptr)))
+        return fail(SDM_EINVAL, "%s: q, k, v, g, beta, o, state and new_state are required", fn);
+    const uintptr_t es = size_of(io->dtype);
+    for (const void* p : {io->q, io->k, io->v, static_cast<const void*>(io->o)}) {
+        if (!aligned(p, es)) return fail(SDM_EALIGN, "%s: q, k, v or o is not element-aligned", fn);
+    }
+    if (!aligned(io->g, 4) || !aligned(io->beta, 4) || !aligned(io->slots, 4)) return fail(SDM_EALIGN, "%s: g, beta or slots is misaligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(io->state, sa) || !aligned(io->new_state, sa))
+        return fail(SDM_EALIGN, "%s: state and new_state must be %d-byte aligned", fn, static_cast<int>(sa));
+    return launched(sdm::gdr_step_launch(io, st), fn);
 }
 
 }  // extern "C"

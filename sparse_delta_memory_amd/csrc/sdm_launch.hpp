@@ -139,7 +139,7 @@ PaWorkspace pa_workspace_layout(const sdm_pa_io* io);
 sdm_status fail(sdm_status s, const char* fmt, ...);
 void clear_error();
 // Once per device and family of kernels, before the family's first launch there: its dynamic-LDS limits (see api.cpp).
-enum class KernelFamily { bank, slots, recurrence };
+enum class KernelFamily { bank, slots, recurrence, delta };
 hipError_t device_setup(int* lds_max, KernelFamily family = KernelFamily::bank);
 
 // Head norms with rotation (validated by sdm_norm_rope and sdm_norm_rope_backward). workspace: bytes of the
@@ -159,5 +159,12 @@ hipError_t glr_backward_launch(const sdm_glr_io* io, const sdm_glr_grad* g, hipS
 hipError_t glr_step_launch(const sdm_glr_step_io* io, hipStream_t st);
 size_t glr_workspace_bytes(const sdm_glr_io* io, bool backward);
 int glr_lds_kernels(const void** fns, int cap);
+
+// The gated delta rule (validated by its entry points).
+hipError_t gdr_forward_launch(const sdm_gdr_io* io, hipStream_t st);
+hipError_t gdr_backward_launch(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st);
+hipError_t gdr_step_launch(const sdm_gdr_step_io* io, hipStream_t st);
+size_t gdr_workspace_bytes(const sdm_gdr_io* io, bool backward);
+int gdr_lds_kernels(const void** fns, int cap);
 
 }  // namespace sdm

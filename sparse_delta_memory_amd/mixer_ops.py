@@ -420,3 +420,130 @@ def glr_step(q, k, v, g, state, scale=None, new_state=None, slots=None, out=None
         _code(fn, q), float(dk ** -0.5 if scale is None else scale))
     _call(_lib.load().sdm_glr_step, dev, stream, io)
     return out
+
+
+# --------------------------------------------------------------------------------- the gated delta rule
+
+def _gdr_io(fn, q, k, v, g, beta, scale, state, lens, o, last, backward, workspace, stream):
+    """The call's device and structure, and the workspace to keep until it is enqueued."""
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError("%s: q, k are [B, T, Hk, dk] and v is [B, T, H, dv]" % fn)
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    dev = _same(fn, q, k, v, g, beta, state, lens, o, last, workspace)
+    _shape(fn, "k", k, q.shape)
+    _shape(fn, "v", v, (B, T, H, dv))
+    _shape(fn, "g", g, (B, T, H))
+    _shape(fn, "beta", beta, (B, T, H))
+    if k.dtype is not q.dtype or v.dtype is not q.dtype or g.dtype is not torch.float32 or beta.dtype is not torch.float32:
+        raise TypeError("%s: q, k and v must have one dtype, and g and beta must be float32" % fn)
+    _columns(fn, q, k, v, o)
+    _dense(fn, torch.float32, state, last)
+    _dense(fn, torch.int32, lens)
+    for name, t in (("state", state), ("last", last)):
+        if t is not None:
+            _shape(fn, name, t, (B, H, dk, dv))
+    if lens is not None:
+        _shape(fn, "lens", lens, (B,))
+    if o is not None:
+        _shape(fn, "out", o, v.shape)
+        if o.dtype is not v.dtype:
+            raise TypeError("%s: out must have v's dtype" % fn)
+    if workspace is not None and not workspace.is_contiguous():
+        raise TypeError("%s: workspace must be contiguous" % fn)
+    fields = (q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), *q.stride()[:3], *k.stride()[:3], *v.stride()[:3],
+              *g.stride(), *beta.stride(), _ptr(state), _ptr(lens), _ptr(o), *((0, 0, 0) if o is None else o.stride()[:3]), _ptr(last), B, T,
+              H, Hk, dk, dv, _code(fn, q), float(dk ** -0.5 if scale is None else scale))
+    if workspace is None:
+        need = int(_lib.load().sdm_gdr_workspace(_lib.pack_gdr(*fields, 0, 0), backward))
+        workspace = _own(stream, need, torch.uint8, dev) if need else None
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return dev, _lib.pack_gdr(*fields, _ptr(workspace), size), workspace
+
+
+def gdr_workspace_bytes(B, T, H, Hk, dk, dv, dtype=torch.bfloat16, backward=False):
+    """Bytes of the workspace of gdr_forward (or gdr_backward) for these sizes; 0 when it needs none."""
+    io = _lib.GdrIO()
+    io.B, io.T, io.H, io.Hk, io.dk, io.dv, io.dtype = int(B), int(T), int(H), int(Hk), int(dk), int(dv), _CODE[dtype]
+    return int(_lib.load().sdm_gdr_workspace(ctypes.byref(io), int(bool(backward))))
+
+
+def gdr_forward(q, k, v, g, beta, scale=None, state=None, lens=None, out=None, last=None, workspace=None, stream=None):
+    """(out, last) of the gated delta rule: per stream and head, from S = state,
+        u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),    S_t = exp(g_t) S_{t-1} + k_t u_t^T,    out_t = scale S_t^T q_t.
+
+    q, k [B, T, Hk, dk], v [B, T, H, dv] float32 or bfloat16, g [B, T, H] float32 log gates (<= 0; -infinity resets the state,
+    whatever it held: sequences packed into one row start with it), beta [B, T, H] float32 (0..1; with keys of norm 1 the rule is
+    stable up to 2). H is a multiple of Hk: value head h uses query and key head h // (H // Hk). dk, dv: 1..128. scale: dk^-0.5 by
+    default. state [B, H, dk, dv] float32 (None: zero). lens [B] int32 on the device: tokens of each stream, whose later tokens are
+    not read and get zero outputs (None: T). last: the state after the last token. workspace: a uint8 tensor of gdr_workspace_bytes
+    (allocated per call by default)."""
+    if q.dim() == 4 and v.dim() == 4:
+        if out is None:
+            out = _output_like(stream, v)
+        if last is None:
+            last = _output(stream, (q.shape[0], v.shape[2], q.shape[3], v.shape[3]), torch.float32, v.device)
+    dev, io, keep = _gdr_io("gdr_forward", q, k, v, g, beta, scale, state, lens, out, last, 0, workspace, stream)
+    _call(_lib.load().sdm_gdr_forward, dev, stream, io, workspace=workspace)
+    return out, last
+
+
+def gdr_backward(d_out, q, k, v, g, beta, scale=None, state=None, d_last=None, lens=None, workspace=None, stream=None):
+    """The backward of gdr_forward at its inputs, from the gradients d_out of out and d_last [B, H, dk, dv] float32 of the
+    last state (None: zero): a dict of dq, dk, dv (contiguous, like q, k, v), dg and dbeta [B, T, H] float32 and dstate (the
+    gradient of the first state, [B, H, dk, dv] float32). Nothing of the forward is needed but its inputs."""
+    fn = "gdr_backward"
+    dev, io, keep = _gdr_io(fn, q, k, v, g, beta, scale, state, lens, None, None, 1, workspace, stream)
+    _same(fn, q, d_out, d_last)
+    _shape(fn, "d_out", d_out, v.shape)
+    if d_out.dtype is not v.dtype:
+        raise TypeError("%s: d_out must have v's dtype" % fn)
+    _columns(fn, d_out)
+    _dense(fn, torch.float32, d_last)
+    B, T, Hk, dk = q.shape
+    H, dv = v.shape[2:]
+    if d_last is not None:
+        _shape(fn, "d_last", d_last, (B, H, dk, dv))
+    new = lambda shape, dtype: _output(stream, shape, dtype, dev)  # noqa: E731
+    r = dict(dq=new(q.shape, q.dtype), dk=new(k.shape, q.dtype), dv=new(v.shape, q.dtype), dg=new((B, T, H), torch.float32),
+             dbeta=new((B, T, H), torch.float32), dstate=new((B, H, dk, dv), torch.float32))
+    grad = _lib.pack_gdr_grad(d_out.data_ptr(), *d_out.stride()[:3], _ptr(d_last), *[t.data_ptr() for t in r.values()])
+    _call(_lib.load().sdm_gdr_backward, dev, stream, io, grad, workspace=workspace)
+    return r
+
+
+def gdr_step(q, k, v, g, beta, state, scale=None, new_state=None, slots=None, out=None, stream=None):
+    """One token of B requests: their states updated in place (or into new_state, laid out the same) and the outputs.
+
+    q, k [B, Hk, dk], v [B, H, dv], g and beta [B, H] float32, state [rows, H, dk, dv] float32 contiguous. slots [B] int32 on the
+    device: the row of each request (None: row b); rows must be distinct, and a request whose row is outside the
+    tensor is left out (output 0). A gate of -infinity starts from nothing, whatever the row held. Returns out [B, H, dv]."""
+    fn = "gdr_step"
+    if q.dim() != 3 or v.dim() != 3:
+        raise ValueError("%s: q, k are [B, Hk, dk] and v is [B, H, dv]" % fn)
+    B, Hk, dk = q.shape
+    H, dv = v.shape[1], v.shape[2]
+    if out is None:
+        out = _output_like(stream, v)
+    if new_state is None:
+        new_state = state
+    dev = _same(fn, q, k, v, g, beta, state, new_state, slots, out)
+    if k.shape != q.shape or v.shape[0] != B or g.shape != (B, H) or beta.shape != (B, H) or out.shape != v.shape:
+        raise ValueError("%s: q %s, k %s, v %s, g %s, beta %s, out %s do not fit" % (fn, *(tuple(t.shape) for t in (q, k, v, g, beta, out))))
+    dt = q.dtype
+    if k.dtype is not dt or v.dtype is not dt or out.dtype is not dt or g.dtype is not torch.float32 or beta.dtype is not torch.float32:
+        raise TypeError("%s: q, k, v and out must have one dtype, and g and beta must be float32" % fn)
+    _columns(fn, q, k, v, out)
+    _dense(fn, torch.float32, state, new_state)
+    if state.shape[1:] != (H, dk, dv) or new_state.shape != state.shape:
+        raise ValueError("%s: state is %s, expected [rows, %d, %d, %d]" % (fn, tuple(state.shape), H, dk, dv))
+    if slots is not None:
+        _dense(fn, torch.int32, slots)
+        _shape(fn, "slots", slots, (B,))
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), out.stride()
+    io = _lib.pack_gdr_step(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], *g.stride(),
+        *beta.stride(), state.data_ptr(), new_state.data_ptr(), state.shape[0], _ptr(slots), out.data_ptr(), os[0], os[1], B, H, Hk, dk, dv,
+        _code(fn, q), float(dk ** -0.5 if scale is None else scale))
+    _call(_lib.load().sdm_gdr_step, dev, stream, io)
+    return out
