@@ -308,7 +308,27 @@ sdm_status sdm_gdr_forward(const sdm_gdr_io* io, hipStream_t st) {
     return launched(sdm::gdr_forward_launch(io, st), fn);
 }
 
-sdm_status sdm_gdr_backward(const sdm_gdr_io*, const sdm_gdr_grad*, hipStream_t) { return fail(SDM_EUNSUPPORTED, "sdm_gdr_backward: not built yet"); }
+sdm_status sdm_gdr_backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_gdr_backward";
+    sdm_status rc = check_gdr(io, true, fn);
+    if (rc != SDM_OK) return rc;
+    if (g == nullptr) return fail(SDM_EINVAL, "%s: grad is NULL", fn);
+    if (io->B == 0) return SDM_OK;
+    if (io->T > 0 && (g->d_o == nullptr || g->dq == nullptr || g->dk == nullptr || g->dv == nullptr || g->dg == nullptr || g->dbeta == nullptr))
+        return fail(SDM_EINVAL, "%s: d_o, dq, dk, dv, dg and dbeta are required", fn);
+    const uintptr_t es = size_of(io->dtype);
+    if (!aligned(g->d_o, es)) return fail(SDM_EALIGN, "%s: d_o is not element-aligned", fn);
+    const uintptr_t sa = state_align(io->dk, io->dv);
+    if (!aligned(g->dq, 16) || !aligned(g->dk, 16) || !aligned(g->dv, 16) || !aligned(g->dg, 4) || !aligned(g->dbeta, 4) || !aligned(g->d_last, sa) ||
+        !aligned(g->d_state, sa))
+        return fail(SDM_EALIGN, "%s: dq, dk and dv must be 16-byte aligned, d_last and d_state %d", fn, static_cast<int>(sa));
+    if (g->d_state != nullptr && (g->d_state == g->d_last || g->d_state == io->state))
+        return fail(SDM_EINVAL, "%s: d_state must not be d_last or state", fn);
+    rc = set_up(fn, sdm::KernelFamily::delta);
+    if (rc != SDM_OK) return rc;
+    return launched(sdm::gdr_backward_launch(io, g, st), fn);
+}
 
 sdm_status sdm_gdr_step(const sdm_gdr_step_io* io, hipStream_t st) {
     sdm::clear_error();

@@ -9,6 +9,8 @@
 // N is strictly lower triangular and has no division by beta; the gradient of u goes through its transpose.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "mixer_device.hpp"
 #include "sdm_launch.hpp"
 #include "tiles.hpp"
@@ -583,6 +585,786 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
     if (p.last != nullptr) place.write(p.last + bh * one, S);
 }
 
+// ------------------------------------------------------------------------------------------ backward
+//
+// With R the gradient of the state after a chunk and E_i the gradient of o_i times scale,
+//     z_i = exp(G_L - G_i) R^T k_i + sum_{j >= i} D_ji (q_j . k_i) E_j,    du = z - N^T (beta z),    dv = beta du,
+//     R before the chunk = exp(G_L) R + sum_i exp(G_i) (q_i E_i^T - k_i dv_i^T),
+// the same shape of work as forward, back in time. The rest is local to a chunk, given S before it, R behind it, r and du:
+//     dq_i = exp(G_i) S E_i + sum_{j <= i} D_ij (E_i . u_j) k_j,
+//     dk_i = exp(G_L - G_i) R u_i + sum_{j >= i} D_ji (E_j . u_i) q_j
+//            - exp(G_i) S dv_i - sum_{j < i} D_ij (dv_i . u_j) k_j - sum_{j > i} D_ji (dv_j . u_i) k_j,
+//     dbeta_i = du_i . r_i,    dg_i = sum_{j >= i in the chunk} (q_j . dq_j - v_j . dv_j) + <S behind the chunk, R>,
+// the last because a gate scales all that reaches its token or a later one from an earlier one; the sum starts afresh from
+// 0 at every reset.
+struct BackArgs {
+    Rows q, k, d;             // d: the gradients of o
+    const int32_t* lens;
+    int T, H, chunks, cols;
+    int kd, vd;
+    float scale;
+    const char* rec;
+    const float* start;       // [B H] gradients of the last states (NULL: zero)
+    float* first;             // [B H] gradients of the first states (NULL: not kept)
+    float* grads;             // [B H, chunks] the gradients of the states behind every chunk
+    float* du;                // [B H, T, vd]
+};
+
+template <typename T, int KD>
+__global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
+    constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
+    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
+    constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
+    constexpr int kN = kFragBytes<T> / 1024;
+    constexpr int kBuf = 2 * kTile + kTileV + 2 * kFragBytes<T> + kFacBytes;
+    extern __shared__ __align__(16) char lds[];
+
+    const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+    const int bh = blk / p.cols, cb = blk - bh * p.cols, b = bh / p.H, h = bh - b * p.H;
+    const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int i16 = lane & 15, qd = lane >> 4;
+    const int c0 = 64 * cb, n0 = 16 * wave, vw = min(64, p.vd - c0);
+    const int len = __builtin_amdgcn_readfirstlane(live_tokens(p.lens, b, p.T)), chunks = (len + kL - 1) / kL;
+
+    Rows dr = p.d;
+    dr.width = vw;
+    const T* qb = static_cast<const T*>(p.q.p) + b * p.q.b + (h / p.q.per) * p.q.h;
+    const T* kb_ = static_cast<const T*>(p.k.p) + b * p.k.b + (h / p.k.per) * p.k.h;
+    const T* db = static_cast<const T*>(p.d.p) + b * p.d.b + h * p.d.h + c0;
+    const int64_t one = static_cast<int64_t>(p.kd) * p.vd;
+    const StateAt<KT> place(c0 + n0 + i16, qd, p.kd, p.vd);
+
+    f32x4 R[KT];
+#pragma unroll
+    for (int d = 0; d < KT; ++d) R[d] = f32x4{0, 0, 0, 0};
+    if (p.start != nullptr) place.read(p.start + bh * one, R);
+
+    Stage<T, KD, 256> sq, sk;
+    Stage<T, 64, 256> sd;
+    sq.init(p.q);
+    sk.init(p.k);
+    sd.init(dr);
+    auto fill = [&](int c, int buf) {
+        const int64_t t0 = static_cast<int64_t>(c) * kL;
+        const int left = len - c * kL;
+        char* at = lds + buf * kBuf;
+        sk.fill(p.k, kb_ + t0 * p.k.t, left, reinterpret_cast<T*>(at), wave, tid);
+        sd.fill(dr, db + t0 * p.d.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
+        sq.fill(p.q, qb + t0 * p.q.t, left, reinterpret_cast<T*>(at + kTile + kTileV), wave, tid);
+        record_fill(p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<T, true> + kFragBytes<T>, 2 * kN, 2 * kFragBytes<T>,
+                    at + 2 * kTile + kTileV, wave, lane);
+    };
+    if (chunks > 0) fill(chunks - 1, 0);
+
+    for (int cc = 0; cc < chunks; ++cc) {
+        const int c = chunks - 1 - cc, buf = kBufs == 2 ? __builtin_amdgcn_readfirstlane(cc & 1) : 0, t0 = c * kL, left = len - t0;
+        char* const at = lds + buf * kBuf;
+        T* const kt = reinterpret_cast<T*>(at);
+        T* const dt = reinterpret_cast<T*>(at + kTile);
+        T* const qt = reinterpret_cast<T*>(at + kTile + kTileV);
+        const char* const nf = at + 2 * kTile + kTileV;
+        const char* const pf = nf + kFragBytes<T>;
+        const Factors& fac = *reinterpret_cast<const Factors*>(nf + 2 * kFragBytes<T>);
+        tile_barrier();
+        if (kBufs == 2 && c > 0) fill(c - 1, buf ^ 1);
+        place.write(p.grads + (static_cast<int64_t>(bh) * p.chunks + c) * one, R);
+
+        f32x4 Z[4];   // tile it: tokens 16 it + 4 quarter + r down, column n0 + lane % 16
+#pragma unroll
+        for (int it = 0; it < 4; ++it) Z[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            Parts<T, NP> rp;
+            float s[8];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) { s[r] = R[2 * kb][r]; s[4 + r] = R[2 * kb + 1][r]; }
+            cut(s, rp);
+            Frag<T> kf[4];
+#pragma unroll
+            for (int it = 0; it < 4; ++it) kf[it] = row_frag<KD>(kt, 16 * it + i16, kb, qd);
+#pragma unroll
+            for (int n = NP - 1; n >= 0; --n) {
+#pragma unroll
+                for (int it = 0; it < 4; ++it) mma(kf[it], rp.p[n], Z[it]);
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const f32x4 u = *reinterpret_cast<const f32x4*>(&fac.u[16 * it + 4 * qd]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) Z[it][r] = sdm_decayed(u[r], Z[it][r]);
+        }
+#pragma unroll
+        for (int jb = 0; jb < 2; ++jb) {
+            const Frag<T> df = col_frag<64, 4>(dt, jb, n0, i16, qd);
+#pragma unroll
+            for (int pr = 0; pr < 6; ++pr) {
+                if (Pairs<true>::kJb[pr] != jb) continue;
+                Parts<T, NP> pp;
+                frag_read(pf, pr, lane, pp);
+#pragma unroll
+                for (int n = NP - 1; n >= 0; --n) mma(pp.p[n], df, Z[Pairs<true>::kIt[pr]]);
+            }
+        }
+        f32x4 X[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) X[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int jb = 0; jb < 2; ++jb) {
+            float w[8];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const f32x4 be = *reinterpret_cast<const f32x4*>(&fac.beta[32 * jb + 16 * s + 4 * qd]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r) w[4 * s + r] = be[r] * Z[2 * jb + s][r];
+            }
+            Parts<T, NP> zp;
+            cut(w, zp);
+#pragma unroll
+            for (int pr = 0; pr < 6; ++pr) {
+                if (Pairs<true>::kJb[pr] != jb) continue;
+                Parts<T, NP> np;
+                frag_read(nf, pr, lane, np);
+                mma_parts(np, zp, X[Pairs<true>::kIt[pr]]);
+            }
+        }
+        float odd = 0.0f;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            Z[it] -= X[it];   // du
+#pragma unroll
+            for (int r = 0; r < 4; ++r) odd = fmaf(Z[it][r], 0.0f, odd);
+        }
+        float* const du = p.du + (static_cast<int64_t>(bh) * p.T + t0) * p.vd + c0 + n0 + i16;
+        if (__builtin_expect(__ballot(odd != odd) != 0, 0)) {   // token by token, as forward
+            for (int t = min(left, kL) - 1; t >= 0; --t) {
+                const float e = p.scale * tile_at(dt, t, n0 + i16), a = fac.one[t];
+                float sum = 0.0f, k[KB][8], q[8];
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    widen8(row_frag<KD>(kt, t, kb, qd), k[kb]);
+                    widen8(row_frag<KD>(qt, t, kb, qd), q);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const float s = 32 * kb + 8 * qd + n < p.kd ? fmaf(q[n], e, R[2 * kb + (n >> 2)][n & 3]) : 0.0f;
+                        R[2 * kb + (n >> 2)][n & 3] = s;
+                        sum = fmaf(s, k[kb][n], sum);
+                    }
+                }
+                sum += lane_xor_f<16>(sum);
+                sum += lane_xor_f<32>(sum);
+                const float dv = fac.beta[t] * sum;
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const float s = 32 * kb + 8 * qd + n < p.kd ? fmaf(-k[kb][n], dv, R[2 * kb + (n >> 2)][n & 3]) : 0.0f;
+                        R[2 * kb + (n >> 2)][n & 3] = sdm_decayed(a, s);
+                    }
+                }
+                if (qd == 0 && n0 + i16 < vw) du[static_cast<int64_t>(t) * p.vd] = sum;
+            }
+        } else {
+            const float all = fac.f[kL - 1];
+#pragma unroll
+            for (int d = 0; d < KT; ++d) R[d] = decayed(all, R[d]);
+#pragma unroll
+            for (int jb = 0; jb < 2; ++jb) {
+                float e[8], w[8];
+                widen8(col_frag<64, 4>(dt, jb, n0, i16, qd), e);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const f32x4 be = *reinterpret_cast<const f32x4*>(&fac.beta[32 * jb + 16 * s + 4 * qd]);
+                    const f32x4 f = *reinterpret_cast<const f32x4*>(&fac.f[32 * jb + 16 * s + 4 * qd]);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        e[4 * s + r] = sdm_decayed(f[r] * p.scale, e[4 * s + r]);
+                        w[4 * s + r] = sdm_decayed(-f[r] * be[r], Z[2 * jb + s][r]);
+                    }
+                }
+                Parts<T, NP> ep, wp;
+                cut(e, ep);
+                cut(w, wp);
+#pragma unroll
+                for (int d = 0; d < KT; d += 4) {
+                    Frag<T> qf[4], kf[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        qf[m] = col_frag<KD, 8>(qt, jb, 32 * ((d + m) >> 1) + 4 * (m & 1), i16, qd);
+                        kf[m] = col_frag<KD, 8>(kt, jb, 32 * ((d + m) >> 1) + 4 * (m & 1), i16, qd);
+                    }
+#pragma unroll
+                    for (int n = NP - 1; n >= 0; --n) {
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) mma(qf[m], ep.p[n], R[d + m]);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m) mma(kf[m], wp.p[n], R[d + m]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int t = 16 * it + 4 * qd + r;
+                    if (t < left && n0 + i16 < vw) du[static_cast<int64_t>(t) * p.vd] = Z[it][r];
+                }
+            }
+        }
+        if (kBufs == 1) {
+            lds_barrier();
+            if (c > 0) fill(c - 1, 0);
+        }
+    }
+    if (p.first != nullptr) place.write(p.first + bh * one, R);
+}
+
+// What is local to a chunk: a block per chunk, 16 key columns for each of its waves.
+struct GradArgs {
+    Rows q, k, v, d;
+    const float *g, *beta;
+    int64_t g_b, g_t, g_h, e_b, e_t, e_h;
+    const int32_t* lens;
+    int T, H, chunks, kd, vd;
+    float scale;
+    const float *states, *grads;   // [B H, chunks] before and behind every chunk
+    const float *miss, *du;        // [B H, T, vd]
+    int stateless;                 // no state before the first token
+    void *dq, *dk;                 // [B, T, H or Hk, kd]: narrowed, or float32 per value head (FOLD)
+    int key_wide;
+    void* dv;                      // [B, T, H, vd]
+    float *dg, *dbeta;             // [B, T, H]
+};
+
+// Tile of a 64-row operand in parts: part s at tile + s 64 VD.
+template <typename T, int VD, int NP>
+__device__ __forceinline__ void row_parts(T* tile, int row, int kb, int quarter, Parts<T, NP>& o) {
+#pragma unroll
+    for (int s = 0; s < NP; ++s) o.p[s] = row_frag<VD>(tile + s * kL * VD, row, kb, quarter);
+}
+
+// Four consecutive columns (a multiple of four) of a row.
+template <int W>
+__device__ __forceinline__ f32x4 tile_four(bf16_t* tile, int row, int col) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(piece<bf16_t, W>(tile, row, col >> 3) + 2 * (col & 7));
+    return f32x4{__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16), __uint_as_float(w[1] & 0xFFFF0000u)};
+}
+template <int W>
+__device__ __forceinline__ f32x4 tile_four(float* tile, int row, int col) {
+    return *reinterpret_cast<const f32x4*>(piece<float, W>(tile, row, col >> 2));
+}
+
+// Half of a score operand: tokens 16 jt + 4 quarter + r (half jt % 2) of row 16 it + lane % 16.
+template <typename T, int NP>
+__device__ __forceinline__ void score_write(char* at, int pr, int half, int lane, float (&s)[4]) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            *reinterpret_cast<u32x2*>(at + ((pr * NP + k) * kWave + lane) * 16 + 8 * half) =
+                u32x2{__builtin_amdgcn_perm(__float_as_uint(s[1]), __float_as_uint(s[0]), 0x07060302u),
+                      __builtin_amdgcn_perm(__float_as_uint(s[3]), __float_as_uint(s[2]), 0x07060302u)};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] -= __uint_as_float(__float_as_uint(s[r]) & 0xFFFF0000u);
+        }
+    } else {
+        *reinterpret_cast<f32x4*>(at + (pr * kWave + lane) * 32 + 16 * half) = f32x4{s[0], s[1], s[2], s[3]};
+    }
+}
+
+// Scores a[r] (token 16 jt + 4 quarter + r, for row 16 it + lane % 16) times m and the decay between the two; REV: of later
+// tokens (jt >= it), else of earlier ones; STRICT: without the token itself.
+template <bool REV, bool STRICT>
+__device__ __forceinline__ void decay_scores(const Gates& gates, int it, int jt, int i16, int qd, float m, const f32x4& a, float (&s)[4]) {
+    if (jt == it) {
+        const float lhi = gates.lhi[16 * it + i16], llo = gates.llo[16 * it + i16];
+        const f32x4 jh = *reinterpret_cast<const f32x4*>(&gates.lhi[16 * jt + 4 * qd]);
+        const f32x4 jl = *reinterpret_cast<const f32x4*>(&gates.llo[16 * jt + 4 * qd]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int j = 4 * qd + r;
+            const float d = (lhi - jh[r]) + (llo - jl[r]);
+            const float w = __builtin_amdgcn_exp2f(REV ? -d : d);
+            s[r] = (REV ? (STRICT ? j > i16 : j >= i16) : STRICT ? j < i16 : j <= i16) ? sdm_decayed(w * m, a[r]) : 0.0f;
+        }
+    } else {
+        const float ot = (REV ? gates.down : gates.up)[16 * it + i16] * (m * gates.tau[4 * it + jt]);
+        const f32x4 d = *reinterpret_cast<const f32x4*>(&(REV ? gates.up : gates.down)[16 * jt + 4 * qd]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[r] = sdm_decayed(ot * d[r], a[r]);
+    }
+}
+
+template <typename T, int KD, int VD>
+struct GradLds {   // bytes
+    static constexpr int kD = kL * (KD > VD ? KD : VD) * static_cast<int>(sizeof(T));      // d_o's tile, then q's
+    static constexpr int kK = kL * KD * static_cast<int>(sizeof(T));
+    static constexpr int kU = kParts<T> * kL * VD * static_cast<int>(sizeof(T));           // u's parts; and dv's
+    static constexpr int kS = 8 * kParts<T> * kWave * 8 * static_cast<int>(sizeof(T));     // score operands
+    static constexpr int kWaves = KD / 16;
+    static constexpr int kTotal = kD + kK + 2 * kU + kS + static_cast<int>(sizeof(Gates)) + (3 + kWaves) * kL * 4 + 64;
+};
+
+template <typename T, int KD, int VD, bool FOLD>
+__global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(GradArgs p) {
+    constexpr int VB = VD / 32, kThreads = 4 * KD, kWaves = KD / 16, NP = kParts<T>;
+    using Lds = GradLds<T, KD, VD>;
+    extern __shared__ __align__(16) char lds[];
+    T* const dt = reinterpret_cast<T*>(lds);
+    T* const qt = dt;
+    T* const kt = reinterpret_cast<T*>(lds + Lds::kD);
+    T* const ut = reinterpret_cast<T*>(lds + Lds::kD + Lds::kK);
+    T* const wt = ut + NP * kL * VD;
+    char* const scores = lds + Lds::kD + Lds::kK + 2 * Lds::kU;
+    Gates& gates = *reinterpret_cast<Gates*>(scores + Lds::kS);
+    float* const beta = reinterpret_cast<float*>(reinterpret_cast<char*>(&gates) + sizeof(Gates));
+    float* const one_gate = beta + kL;
+    float* const vdv = one_gate + kL;
+    float* const dots = vdv + kL;           // [waves][64]
+    float* const cross = dots + kWaves * kL;   // [waves]
+
+    const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+    const int bh = blk / p.chunks, c = blk - bh * p.chunks, b = bh / p.H, h = bh - b * p.H;
+    const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int i16 = lane & 15, qd = lane >> 4, n0 = 16 * wave;
+    const int t0 = c * kL, left = __builtin_amdgcn_readfirstlane(live_tokens(p.lens, b, p.T)) - t0, all = min(kL, p.T - t0);
+    const int64_t row0 = (static_cast<int64_t>(b) * p.T + t0) * p.H + h;   // of [B, T, H]; a token's next one is p.H on
+    using Out = typename std::conditional<FOLD, float, T>::type;
+    // Key heads are added up later where they are shared; where not, H is Hk.
+    Out* const dq = static_cast<Out*>(p.dq) + row0 * p.kd;
+    Out* const dk = static_cast<Out*>(p.dk) + row0 * p.kd;
+    T* const dv = static_cast<T*>(p.dv) + row0 * p.vd;
+    if (left <= 0) {
+        for (int e = tid; e < all * p.kd; e += kThreads) {
+            const int64_t at = static_cast<int64_t>(e / p.kd) * p.H * p.kd + e % p.kd;
+            dq[at] = narrow<Out>(0.0f);
+            dk[at] = narrow<Out>(0.0f);
+        }
+        for (int e = tid; e < all * p.vd; e += kThreads) dv[static_cast<int64_t>(e / p.vd) * p.H * p.vd + e % p.vd] = narrow<T>(0.0f);
+        if (tid < all) p.dg[row0 + static_cast<int64_t>(tid) * p.H] = p.dbeta[row0 + static_cast<int64_t>(tid) * p.H] = 0.0f;
+        return;
+    }
+
+    Stage<T, KD, kThreads> sq, sk;
+    Stage<T, VD, kThreads> sd;
+    sq.init(p.q);
+    sk.init(p.k);
+    sd.init(p.d);
+    const T* const db = static_cast<const T*>(p.d.p) + b * p.d.b + h * p.d.h + static_cast<int64_t>(t0) * p.d.t;
+    sk.fill(p.k, static_cast<const T*>(p.k.p) + b * p.k.b + (h / p.k.per) * p.k.h + static_cast<int64_t>(t0) * p.k.t, left, kt, wave, tid);
+    sd.fill(p.d, db, left, dt, wave, tid);
+    if (wave == kWaves - 1) {
+        const int64_t t = t0 + min(lane, left - 1);
+        const bool live = lane < left;
+        const float g = live ? p.g[b * p.g_b + t * p.g_t + h * p.g_h] : 0.0f;
+        gate_factors<false>(g, 1.0f, 1.0f, gates, lane);
+        one_gate[lane] = g;
+        beta[lane] = live ? p.beta[b * p.e_b + t * p.e_t + h * p.e_h] : 0.0f;
+    }
+    lds_barrier();   // beta
+
+    // u and dv in parts; dbeta, dv and v . dv of every token. A thread takes 8 columns of a token at a time.
+    const int64_t vrow = (static_cast<int64_t>(bh) * p.T + t0) * p.vd;
+    {
+        constexpr int kUnits = VD / 8;
+        static_assert(kThreads % kUnits == 0, "a token's columns are neighbouring lanes'");
+        const T* const vb = static_cast<const T*>(p.v.p) + b * p.v.b + h * p.v.h + static_cast<int64_t>(t0) * p.v.t;
+        const bool wide = p.vd % 8 == 0;
+        for (int at = tid; at < kL * kUnits; at += kThreads) {
+            const int t = at / kUnits, col = 8 * (at % kUnits);
+            float r[8], d[8], v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r[e] = d[e] = v[e] = 0.0f;
+            if (t < left && col < p.vd) {
+                const float* rp = p.miss + vrow + t * p.vd + col;
+                const float* dp = p.du + vrow + t * p.vd + col;
+                const T* vp = vb + t * p.v.t + col;
+                if (wide) {
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) {
+                        const f32x4 x = *reinterpret_cast<const f32x4*>(rp + 4 * s), y = *reinterpret_cast<const f32x4*>(dp + 4 * s);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) { r[4 * s + e] = x[e]; d[4 * s + e] = y[e]; }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (col + e < p.vd) { r[e] = rp[e]; d[e] = dp[e]; }
+                    }
+                }
+                if (wide && p.v.wide) {
+                    Frag<T> f;
+                    __builtin_memcpy(&f, __builtin_assume_aligned(vp, 16), sizeof(f));
+                    widen8(f, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = col + e < p.vd ? widen(vp[e]) : 0.0f;
+                }
+            }
+            float db_ = 0.0f, vd_ = 0.0f, u[8], w[8];
+            const float be = beta[t];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                db_ = fmaf(d[e], r[e], db_);
+                u[e] = be * r[e];
+                w[e] = be * d[e];
+                vd_ = fmaf(v[e], w[e], vd_);
+            }
+            if (t < all && col < p.vd) {
+                T* o = dv + static_cast<int64_t>(t) * p.H * p.vd + col;
+                const f32x4 w0 = {w[0], w[1], w[2], w[3]}, w1 = {w[4], w[5], w[6], w[7]};
+                store_four<T>(o, 0, w0, p.vd - col, wide);
+                if (col + 4 < p.vd) store_four<T>(o, 4, w1, p.vd - col - 4, wide);
+            }
+            db_ = group_sum<kUnits>(db_);
+            vd_ = group_sum<kUnits>(vd_);
+            if (col == 0) {
+                vdv[t] = vd_;
+                if (t < all) p.dbeta[row0 + static_cast<int64_t>(t) * p.H] = db_;
+            }
+            Parts<T, NP> up, wp;
+            cut(u, up);
+            cut(w, wp);
+#pragma unroll
+            for (int s = 0; s < NP; ++s) {
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<u32x4*>(piece<T, VD>(ut + s * kL * VD, t, col >> 3)) = up.p[s].w;
+                    *reinterpret_cast<u32x4*>(piece<T, VD>(wt + s * kL * VD, t, col >> 3)) = wp.p[s].w;
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        *reinterpret_cast<f32x4*>(piece<T, VD>(ut, t, (col >> 2) + n)) = f32x4{u[4 * n], u[4 * n + 1], u[4 * n + 2], u[4 * n + 3]};
+                        *reinterpret_cast<f32x4*>(piece<T, VD>(wt, t, (col >> 2) + n)) = f32x4{w[4 * n], w[4 * n + 1], w[4 * n + 2], w[4 * n + 3]};
+                    }
+                }
+            }
+        }
+    }
+    // The wave's rows n0 + lane % 16 of the state and of its gradient: columns 32 kb + 8 quarter + ..
+    float S[VB][8], R[VB][8];
+    const int64_t one = static_cast<int64_t>(p.kd) * p.vd, at_state = (static_cast<int64_t>(bh) * p.chunks + c) * one;
+    auto state_rows = [&](const float* from, float (&x)[VB][8]) {
+        const auto s = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(from), 0, static_cast<int>(one) * 4, 0x00027000);
+        const uint32_t at = 4u * static_cast<uint32_t>((n0 + i16) * p.vd + 8 * qd);
+        const bool on = n0 + i16 < p.kd, four = p.vd % 4 == 0;
+#pragma unroll
+        for (int kb = 0; kb < VB; ++kb) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const int col = 32 * kb + 8 * qd + 4 * n;
+                if (four) {
+                    const f32x4 w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                                  s, static_cast<int>(on && col < p.vd ? at + 128u * kb + 16u * n : 0xC0000000u), 0, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[kb][4 * n + e] = w[e];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[kb][4 * n + e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+                            s, static_cast<int>(on && col + e < p.vd ? at + 128u * kb + 16u * n + 4u * e : 0xC0000000u), 0, 0));
+                }
+            }
+        }
+    };
+    state_rows(p.states + at_state, S);
+    state_rows(p.grads + at_state, R);
+    tile_barrier();
+
+    // E_i . u_j for dq
+    for (int e = wave; e < 12; e += kWaves) {
+        const int pr = e >> 1;
+        int it = 0, jb = 0;
+#pragma unroll
+        for (int k = 0; k < 6; ++k) {
+            if (k == pr) { it = Pairs<false>::kIt[k]; jb = Pairs<false>::kJb[k]; }
+        }
+        const int jt = 2 * jb + (e & 1);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (jt <= it) {
+            f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < VB; ++kb) {
+                const Frag<T> df = row_frag<VD>(dt, 16 * it + i16, kb, qd);
+                Parts<T, NP> up;
+                row_parts<T, VD>(ut, 16 * jt + i16, kb, qd, up);
+#pragma unroll
+                for (int n = NP - 1; n >= 0; --n) mma(up.p[n], df, a);
+            }
+            decay_scores<false, false>(gates, it, jt, i16, qd, p.scale, a, s);
+        }
+        score_write<T, NP>(scores, pr, e & 1, lane, s);
+    }
+    // S E and S dv
+    f32x4 Q[4], K[4];   // tile it: columns n0 + 4 quarter + r down, token 16 it + lane % 16
+#pragma unroll
+    for (int it = 0; it < 4; ++it) Q[it] = K[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int kb = 0; kb < VB; ++kb) {
+        Parts<T, NP> sp;
+        cut(S[kb], sp);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const Frag<T> df = row_frag<VD>(dt, 16 * it + i16, kb, qd);
+#pragma unroll
+            for (int n = NP - 1; n >= 0; --n) mma(sp.p[n], df, Q[it]);
+            Parts<T, NP> wp;
+            row_parts<T, VD>(wt, 16 * it + i16, kb, qd, wp);
+            mma_parts(sp, wp, K[it]);
+        }
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const float f = gates.f[16 * it + i16];
+        Q[it] = decayed(f * p.scale, Q[it]);
+        K[it] = decayed(-f, K[it]);
+    }
+    Frag<T> kf[2];
+#pragma unroll
+    for (int jb = 0; jb < 2; ++jb) kf[jb] = col_frag<KD, 4>(kt, jb, n0, i16, qd);
+    lds_barrier();   // the scores are complete
+#pragma unroll
+    for (int pr = 0; pr < 6; ++pr) {
+        Parts<T, NP> pp;
+        frag_read(scores, pr, lane, pp);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) mma(kf[Pairs<false>::kJb[pr]], pp.p[n], Q[Pairs<false>::kIt[pr]]);
+    }
+    lds_barrier();   // and read
+    // E_j . u_i for dk
+    for (int e = wave; e < 12; e += kWaves) {
+        const int pr = e >> 1;
+        int it = 0, jb = 0;
+#pragma unroll
+        for (int k = 0; k < 6; ++k) {
+            if (k == pr) { it = Pairs<true>::kIt[k]; jb = Pairs<true>::kJb[k]; }
+        }
+        const int jt = 2 * jb + (e & 1);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (jt >= it) {
+            f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+            for (int kb = 0; kb < VB; ++kb) {
+                const Frag<T> df = row_frag<VD>(dt, 16 * jt + i16, kb, qd);
+                Parts<T, NP> up;
+                row_parts<T, VD>(ut, 16 * it + i16, kb, qd, up);
+#pragma unroll
+                for (int n = NP - 1; n >= 0; --n) mma(df, up.p[n], a);
+            }
+            decay_scores<true, false>(gates, it, jt, i16, qd, p.scale, a, s);
+        }
+        score_write<T, NP>(scores, pr, e & 1, lane, s);
+    }
+    lds_barrier();   // complete, and d_o's tile is free
+    sq.fill(p.q, static_cast<const T*>(p.q.p) + b * p.q.b + (h / p.q.per) * p.q.h + static_cast<int64_t>(t0) * p.q.t, left, qt, wave, tid);
+    // R u; <S behind the chunk, R> = exp(G_L) <S, R> + sum_j exp(G_L - G_j) k_j . R u_j
+    float x = 0.0f;
+    {
+        f32x4 A[4];
+#pragma unroll
+        for (int it = 0; it < 4; ++it) A[it] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < VB; ++kb) {
+            Parts<T, NP> rp;
+            cut(R[kb], rp);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                Parts<T, NP> up;
+                row_parts<T, VD>(ut, 16 * it + i16, kb, qd, up);
+                mma_parts(rp, up, A[it]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x = fmaf(S[kb][e], R[kb][e], x);
+        }
+        x = sdm_decayed(gates.all, x);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            A[it] = decayed(gates.u[16 * it + i16], A[it]);
+            const f32x4 k = tile_four<KD>(kt, 16 * it + i16, n0 + 4 * qd);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) x = fmaf(k[r], A[it][r], x);
+            K[it] += A[it];
+        }
+    }
+    tile_barrier();   // q's tile
+    {
+        Frag<T> qf[2];
+#pragma unroll
+        for (int jb = 0; jb < 2; ++jb) qf[jb] = col_frag<KD, 4>(qt, jb, n0, i16, qd);
+#pragma unroll
+        for (int pr = 0; pr < 6; ++pr) {
+            Parts<T, NP> pp;
+            frag_read(scores, pr, lane, pp);
+#pragma unroll
+            for (int n = NP - 1; n >= 0; --n) mma(qf[Pairs<true>::kJb[pr]], pp.p[n], K[Pairs<true>::kIt[pr]]);
+        }
+    }
+    lds_barrier();   // the scores are read
+    // - (dv_i . u_j) of earlier tokens j and of later ones the other way round
+    for (int e = wave; e < 16; e += kWaves) {
+        const int it = e >> 2, jt = e & 3;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s2[4];
+        f32x4 a = {0, 0, 0, 0}, a2 = {0, 0, 0, 0};
+#pragma unroll
+        for (int kb = 0; kb < VB; ++kb) {
+            Parts<T, NP> xp, yp;
+            row_parts<T, VD>(jt <= it ? wt : ut, 16 * it + i16, kb, qd, xp);
+            row_parts<T, VD>(jt <= it ? ut : wt, 16 * jt + i16, kb, qd, yp);
+            mma_parts(yp, xp, a);
+            if (jt == it) mma_parts(xp, yp, a2);
+        }
+        if (jt <= it) decay_scores<false, true>(gates, it, jt, i16, qd, -1.0f, a, s);
+        else decay_scores<true, true>(gates, it, jt, i16, qd, -1.0f, a, s);
+        if (jt == it) {
+            decay_scores<true, true>(gates, it, jt, i16, qd, -1.0f, a2, s2);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] += s2[r];   // one of the two is 0
+        }
+        score_write<T, NP>(scores, e >> 1, e & 1, lane, s);
+    }
+    lds_barrier();
+#pragma unroll
+    for (int pr = 0; pr < 8; ++pr) {
+        Parts<T, NP> pp;
+        frag_read(scores, pr, lane, pp);
+#pragma unroll
+        for (int n = NP - 1; n >= 0; --n) mma(kf[pr & 1], pp.p[n], K[pr >> 1]);
+    }
+    // Results.
+    float odd = 0.0f;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) odd = fmaf(Q[it][r], 0.0f, fmaf(K[it][r], 0.0f, odd));
+    }
+    if (__builtin_expect(__ballot(odd != odd) != 0, 0)) {
+        // Something is not finite: the wave's columns token by token, forwards with the state, then backwards with its gradient.
+        // u's and dv's tiles are not read any more; they take what dk is given forwards.
+        float* const kept = reinterpret_cast<float*>(ut) + wave * (kL * 16);
+        const int n = min(left, kL), col = n0 + i16;
+        const float* const rp = p.miss + vrow;
+        const float* const dp = p.du + vrow;
+        constexpr int kElems = 16 / static_cast<int>(sizeof(T));
+        auto key = [&](T* tile, int t) {   // column `col` of a token's row
+            return widen(*reinterpret_cast<const T*>(piece<T, KD>(tile, t, col / kElems) + (col % kElems) * static_cast<int>(sizeof(T))));
+        };
+        for (int t = 0; t < n; ++t) {
+            const float a = exp2_of(static_cast<double>(one_gate[t] < kGateMin ? kGateMin : one_gate[t]) * kLog2E), be = beta[t], k = key(kt, t);
+            float sq_ = 0.0f, sk_ = 0.0f;
+#pragma unroll
+            for (int kb = 0; kb < VB; ++kb) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 32 * kb + 8 * qd + e;
+                    if (j >= p.vd) continue;
+                    const float s = sdm_decayed(a, S[kb][e]);
+                    sk_ = fmaf(s, be * dp[t * p.vd + j], sk_);
+                    S[kb][e] = fmaf(k, be * rp[t * p.vd + j], s);
+                    sq_ = fmaf(S[kb][e], widen(db[t * p.d.t + j]), sq_);
+                }
+            }
+            sq_ += lane_xor_f<16>(sq_);
+            sq_ += lane_xor_f<32>(sq_);
+            sk_ += lane_xor_f<16>(sk_);
+            sk_ += lane_xor_f<32>(sk_);
+            sq_ *= p.scale;
+            if (qd == 0) {
+                kept[t * 16 + i16] = sk_;
+                if (col < p.kd) dq[static_cast<int64_t>(t) * p.H * p.kd + col] = narrow<Out>(sq_);
+            }
+            const float dot = group_sum<16>(col < p.kd ? key(qt, t) * sq_ : 0.0f);
+            if (lane == 0) dots[wave * kL + t] = dot;
+        }
+        x = 0.0f;
+#pragma unroll
+        for (int kb = 0; kb < VB; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (col < p.kd && 32 * kb + 8 * qd + e < p.vd) x = fmaf(S[kb][e], R[kb][e], x);
+            }
+        }
+        for (int t = n - 1; t >= 0; --t) {
+            const float a = exp2_of(static_cast<double>(one_gate[t] < kGateMin ? kGateMin : one_gate[t]) * kLog2E), be = beta[t], k = key(kt, t),
+                        q = p.scale * key(qt, t);
+            float sum = 0.0f;
+#pragma unroll
+            for (int kb = 0; kb < VB; ++kb) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int j = 32 * kb + 8 * qd + e;
+                    if (j >= p.vd) continue;
+                    const float s = fmaf(q, widen(db[t * p.d.t + j]), R[kb][e]);
+                    sum = fmaf(s, be * rp[t * p.vd + j], sum);
+                    R[kb][e] = sdm_decayed(a, fmaf(-k, be * dp[t * p.vd + j], s));
+                }
+            }
+            sum += lane_xor_f<16>(sum);
+            sum += lane_xor_f<32>(sum);
+            if (qd == 0 && col < p.kd) dk[static_cast<int64_t>(t) * p.H * p.kd + col] = narrow<Out>(sum - kept[t * 16 + i16]);
+        }
+        for (int e = lane; e < (all - n) * 16; e += kWave) {
+            const int t = n + e / 16;
+            if (n0 + e % 16 >= p.kd) continue;
+            const int64_t at = static_cast<int64_t>(t) * p.H * p.kd + n0 + e % 16;
+            dq[at] = narrow<Out>(0.0f);
+            dk[at] = narrow<Out>(0.0f);
+        }
+    } else {
+        const int n = n0 + 4 * qd;
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+            const int t = 16 * it + i16;
+            const f32x4 q = tile_four<KD>(qt, t, n);
+            float dot = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) dot = fmaf(q[r], Q[it][r], dot);
+            dot += lane_xor_f<16>(dot);
+            dot += lane_xor_f<32>(dot);
+            if (qd == 0) dots[wave * kL + t] = dot;
+            if (t >= all || n >= p.kd) continue;
+            if (t >= left) Q[it] = K[it] = f32x4{0, 0, 0, 0};
+            const int64_t at = static_cast<int64_t>(t) * p.H * p.kd + n;
+            store_four<Out>(dq, at, Q[it], p.kd - n, p.key_wide);
+            store_four<Out>(dk, at, K[it], p.kd - n, p.key_wide);
+        }
+    }
+    x = group_sum<kWave>(x);
+    if (lane == 0) cross[wave] = x;
+    lds_barrier();
+    if (wave == 0) {
+        const int t = kL - 1 - lane;   // lanes go back in time
+        double carry = 0.0, y = 0.0, d = 0.0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) carry += static_cast<double>(cross[w]);
+        if (t < left) {
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) d += static_cast<double>(dots[w * kL + t]);
+            d -= static_cast<double>(vdv[t]);
+        }
+        // A piece ends with the token that resets, the first one in time: the next starts behind it, from 0.
+        const uint64_t cuts = __ballot(t < left && (resets(one_gate[t]) || (p.stateless && t0 + t == 0)));
+        pieces(cuts << 1, d, lane, [&](int from, int to, double sum) {
+            if (lane >= from && lane < to) y = carry + sum;
+            carry = 0.0;
+        });
+        if ((cuts >> lane) & 1) y = 0.0;
+        if (t < all) p.dg[row0 + static_cast<int64_t>(t) * p.H] = t < left ? static_cast<float>(y) : 0.0f;
+    }
+}
+
+// The gradients of shared heads: the sum of `per` value heads' float32 rows, in head order (dq, then dk).
+template <typename T>
+__global__ __launch_bounds__(256) void gdr_fold_kernel(const float* fq, const float* fk, T* dq, T* dk, int64_t total, int d, int per) {
+    const float* in = blockIdx.y ? fk : fq;
+    T* out = blockIdx.y ? dk : dq;
+    for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < total; e += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = e / d, c = e - row * d;
+        float s = 0.0f;
+        for (int r = 0; r < per; ++r) s += in[(row * per + r) * d + c];
+        out[e] = narrow<T>(s);
+    }
+}
+
 // ------------------------------------------------------------------------------------------ one token
 //
 // A block owns up to 64 columns of one request's state, all their rows in its lanes' registers: read once, with both
@@ -709,14 +1491,34 @@ size_t main_lds(bool out) {
 
 int chunks_of(int T) { return (T + kL - 1) / kL; }
 
+// Byte offsets in the workspace.
 struct GdrLayout {
-    size_t rec, total;
+    size_t rec, states, grads, miss, du, fq, fk, total;
 };
-GdrLayout gdr_layout(const sdm_gdr_io* io) {
-    const size_t n = static_cast<size_t>(io->B) * io->H * chunks_of(io->T);
+GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
+    const size_t bh = static_cast<size_t>(io->B) * io->H, n = bh * chunks_of(io->T), rows = bh * io->T;
+    const bool bf = io->dtype == SDM_BF16;
     GdrLayout l{};
-    l.rec = 0;
-    l.total = up256(n * (io->dtype == SDM_BF16 ? kRecBytes<bf16_t, false> : kRecBytes<float, false>));
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += up256(bytes);
+        return o;
+    };
+    if (backward) {
+        l.rec = take(n * (bf ? kRecBytes<bf16_t, true> : kRecBytes<float, true>));
+        l.states = take(n * io->dk * io->dv * 4);
+        l.grads = take(n * io->dk * io->dv * 4);
+        l.miss = take(rows * io->dv * 4);
+        l.du = take(rows * io->dv * 4);
+        if (io->H > io->Hk) {
+            l.fq = take(rows * io->dk * 4);
+            l.fk = take(rows * io->dk * 4);
+        }
+    } else {
+        l.rec = take(n * (bf ? kRecBytes<bf16_t, false> : kRecBytes<float, false>));
+    }
+    l.total = at;
     return l;
 }
 
@@ -742,7 +1544,7 @@ hipError_t main_go(const sdm_gdr_io* io, const MainArgs& a, hipStream_t st) {
 template <typename T>
 hipError_t forward(const sdm_gdr_io* io, hipStream_t st) {
     const int per = io->H / io->Hk, es = sizeof(T);
-    char* rec = static_cast<char*>(io->workspace) + gdr_layout(io).rec;
+    char* rec = static_cast<char*>(io->workspace) + gdr_layout(io, false).rec;
     if (io->T > 0) {
         const hipError_t e = chunk_go<T, false>(io, rec, st);
         if (e != hipSuccess) return e;
@@ -770,8 +1572,83 @@ hipError_t forward(const sdm_gdr_io* io, hipStream_t st) {
     return main_go<T, true>(io, a, st);
 }
 
+template <typename T, int KD, bool FOLD>
+hipError_t grad_go2(const GradArgs& a, unsigned grid, hipStream_t st) {
+    if (padded(a.vd) == 64) gdr_grad_kernel<T, KD, 64, FOLD><<<grid, 4 * KD, GradLds<T, KD, 64>::kTotal, st>>>(a);
+    else gdr_grad_kernel<T, KD, 128, FOLD><<<grid, 4 * KD, GradLds<T, KD, 128>::kTotal, st>>>(a);
+    return hipGetLastError();
+}
+template <typename T, bool FOLD>
+hipError_t grad_go(const GradArgs& a, unsigned grid, hipStream_t st) {
+    return padded(a.kd) == 64 ? grad_go2<T, 64, FOLD>(a, grid, st) : grad_go2<T, 128, FOLD>(a, grid, st);
+}
+
+template <typename T>
+hipError_t backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st) {
+    const int per = io->H / io->Hk, es = sizeof(T);
+    const GdrLayout l = gdr_layout(io, true);
+    char* ws = static_cast<char*>(io->workspace);
+    const Rows q = rows_of(io->q, io->q_b, io->q_t, io->q_h, io->dk, per, es), k = rows_of(io->k, io->k_b, io->k_t, io->k_h, io->dk, per, es),
+               v = rows_of(io->v, io->v_b, io->v_t, io->v_h, io->dv, 1, es), d = rows_of(g->d_o, g->do_b, g->do_t, g->do_h, io->dv, 1, es);
+    const int chunks = chunks_of(io->T), cols = (io->dv + 63) / 64;
+    const int64_t bh = static_cast<int64_t>(io->B) * io->H;
+    hipError_t e = hipSuccess;
+    MainArgs m{};
+    m.k = k;
+    m.v = v;
+    m.lens = io->lens;
+    m.T = io->T;
+    m.H = io->H;
+    m.chunks = chunks;
+    m.cols = cols;
+    m.kd = io->dk;
+    m.vd = io->dv;
+    m.scale = io->scale;
+    m.rec = ws + l.rec;
+    m.start = io->state;
+    m.states = reinterpret_cast<float*>(ws + l.states);
+    m.miss = reinterpret_cast<float*>(ws + l.miss);
+    if (io->T > 0) {
+        if ((e = chunk_go<T, true>(io, ws + l.rec, st)) != hipSuccess) return e;
+        if ((e = main_go<T, false>(io, m, st)) != hipSuccess) return e;
+    }
+    const BackArgs b{q, k, d, io->lens, io->T, io->H, chunks, cols, io->dk, io->dv, io->scale, ws + l.rec, g->d_last, g->d_state,
+                     reinterpret_cast<float*>(ws + l.grads), reinterpret_cast<float*>(ws + l.du)};
+    const unsigned grid = static_cast<unsigned>(bh * cols);
+    if (padded(io->dk) == 64) gdr_back_kernel<T, 64><<<grid, 256, main_lds<T, 64>(true), st>>>(b);
+    else gdr_back_kernel<T, 128><<<grid, 256, main_lds<T, 128>(true), st>>>(b);
+    if ((e = hipGetLastError()) != hipSuccess || io->T == 0) return e;
+    const bool fold = per > 1;
+    GradArgs a{q, k, v, d, io->g, io->beta, io->g_b, io->g_t, io->g_h, io->e_b, io->e_t, io->e_h, io->lens, io->T, io->H, chunks, io->dk, io->dv,
+               io->scale, m.states, b.grads, m.miss, b.du, io->state == nullptr, g->dq, g->dk, io->dk % 4 == 0, g->dv, g->dg, g->dbeta};
+    if (!fold) return grad_go<T, false>(a, static_cast<unsigned>(bh * chunks), st);
+    float *fq = reinterpret_cast<float*>(ws + l.fq), *fk = reinterpret_cast<float*>(ws + l.fk);
+    a.dq = fq;
+    a.dk = fk;
+    if ((e = grad_go<T, true>(a, static_cast<unsigned>(bh * chunks), st)) != hipSuccess) return e;
+    const int64_t total = static_cast<int64_t>(io->B) * io->T * io->Hk * io->dk, need = (total + 255) / 256;
+    gdr_fold_kernel<T><<<dim3(static_cast<unsigned>(need < (1 << 20) ? need : 1 << 20), 2), 256, 0, st>>>(fq, fk, static_cast<T*>(g->dq),
+                                                                                                          static_cast<T*>(g->dk), total, io->dk, per);
+    return hipGetLastError();
+}
+
+template <typename T, int KD>
+void list_grad(const void** all, int& n) {
+    all[n++] = reinterpret_cast<const void*>(&gdr_grad_kernel<T, KD, 64, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_grad_kernel<T, KD, 64, true>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_grad_kernel<T, KD, 128, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_grad_kernel<T, KD, 128, true>);
+}
 template <typename T>
 void list(const void** all, int& n) {
+    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 64, true>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 128, true>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 64, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 128, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_back_kernel<T, 64>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_back_kernel<T, 128>);
+    list_grad<T, 64>(all, n);
+    list_grad<T, 128>(all, n);
     all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 64, false>);
     all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 128, false>);
     all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 64, true>);
@@ -781,7 +1658,7 @@ void list(const void** all, int& n) {
 }  // namespace
 
 int gdr_lds_kernels(const void** fns, int cap) {
-    const void* all[32];
+    const void* all[64];
     int n = 0;
     list<bf16_t>(all, n);
     list<float>(all, n);
@@ -791,12 +1668,15 @@ int gdr_lds_kernels(const void** fns, int cap) {
 }
 
 size_t gdr_workspace_bytes(const sdm_gdr_io* io, bool backward) {
-    (void)backward;
-    return io->B < 1 || io->T < 1 ? 0 : gdr_layout(io).total;
+    return io->B < 1 || io->T < 1 ? 0 : gdr_layout(io, backward).total;
 }
 
 hipError_t gdr_forward_launch(const sdm_gdr_io* io, hipStream_t st) {
     return io->dtype == SDM_BF16 ? forward<bf16_t>(io, st) : forward<float>(io, st);
+}
+
+hipError_t gdr_backward_launch(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st) {
+    return io->dtype == SDM_BF16 ? backward<bf16_t>(io, g, st) : backward<float>(io, g, st);
 }
 
 hipError_t gdr_step_launch(const sdm_gdr_step_io* io, hipStream_t st) {

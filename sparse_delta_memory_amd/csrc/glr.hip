@@ -581,18 +581,6 @@ __global__ __launch_bounds__(256) void glr_chain_kernel(float* states, const flo
     }
 }
 
-// The lanes [from, to) of a wave's 64 tokens, in pieces that no reset cuts: per piece its inclusive sums of x, which start
-// afresh in each. cuts: the lanes that start a piece of their own. f(piece's first lane, its end, the lane's sum).
-template <typename F>
-__device__ __forceinline__ void pieces(uint64_t cuts, double x, int lane, F f) {
-    for (int from = 0; from < kWave;) {
-        const uint64_t rest = from + 1 < kWave ? cuts >> (from + 1) << (from + 1) : 0;
-        const int to = rest != 0 ? __builtin_ctzll(rest) : kWave;
-        f(from, to, scan_d(lane >= from && lane < to ? x : 0.0));
-        from = to;
-    }
-}
-
 struct GateGrad {
     const float *dq, *dk;     // [B H, T] the row dots q . dq and k . dk
     const float* cross;       // [B H, nseg]
@@ -605,9 +593,6 @@ struct GateGrad {
     int T, H, nseg, seg;
     int64_t waves;
 };
-
-// Whether a gate leaves nothing: its factor is 0 as the chunks and the step compute it.
-__device__ __forceinline__ bool resets(float g) { return __builtin_amdgcn_exp2f(g * static_cast<float>(kLog2E)) == 0.0f; }
 
 // dg: one wave per (stream, head, segment), 256 tokens at a time from the segment's end, in float64. A token that
 // resets, or has no state before it, has a gradient of 0, and with it the sums start afresh: nothing of a later sequence, be it large

@@ -366,6 +366,21 @@ __device__ __forceinline__ void gate_factors(float g, float m_o, float m_s, Gate
     }
 }
 
+// The lanes [from, to) of a wave's 64 tokens, in pieces that no reset cuts: per piece its inclusive sums of x, which start
+// afresh in each. cuts: the lanes that start a piece of their own. f(piece's first lane, its end, the lane's sum).
+template <typename F>
+__device__ __forceinline__ void pieces(uint64_t cuts, double x, int lane, F f) {
+    for (int from = 0; from < kWave;) {
+        const uint64_t rest = from + 1 < kWave ? cuts >> (from + 1) << (from + 1) : 0;
+        const int to = rest != 0 ? __builtin_ctzll(rest) : kWave;
+        f(from, to, scan_d(lane >= from && lane < to ? x : 0.0));
+        from = to;
+    }
+}
+
+// Whether a gate leaves nothing: its factor is 0 as the chunks and the step compute it.
+__device__ __forceinline__ bool resets(float g) { return __builtin_amdgcn_exp2f(g * static_cast<float>(kLog2E)) == 0.0f; }
+
 // The score operands of a chunk, computed once and shared by the waves: pair n is (it, jb), the tiles of tokens
 // 16 it across and 32 jb down; its two halves are the score tiles jt = 2 jb and 2 jb + 1. Of the 16 tiles the
 // 6 pairs below hold all that the direction needs (and two that are zero).

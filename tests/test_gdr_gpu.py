@@ -138,3 +138,47 @@ def test_step_matches_oracle(dtype, B, H, Hk, dk, dv):
     assert torch.equal(o2[keep], o[keep]) and (o2[~keep] == 0).all()
     assert torch.equal(pool[slots[keep].long()], new[keep])
     assert (pool[0::2] == 7.0).all() and torch.equal(pool[2 * (B // 2) + 1], d["state"][B // 2])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,H,Hk,dk,dv", SHAPES)
+def test_backward_matches_oracle(dtype, B, T, H, Hk, dk, dv):
+    say("gdr backward", dtype, B, T, H, Hk, dk, dv)
+    backward(make(B, T, H, Hk, dk, dv, dtype), dtype, dk ** -0.5)
+    backward(make(B, T, H, Hk, dk, dv, dtype, state=False, seed=4), dtype, 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,lens", [(150, [0, 150, 1, 64]), (300, [300, 0, 70, 129]), (100, [-3, 900, 100, 99])])
+def test_backward_lengths(dtype, T, lens):
+    say("gdr backward lens", dtype, T, lens)
+    x = make(4, T, 2, 1, 24, 40, dtype, lens=lens)
+    d = cuda(x)
+    for b, n in enumerate(lens):
+        for name in ("q", "k", "v", "g", "beta", "d_o"):
+            d[name][b, max(0, min(n, T)):] = NAN
+    r = backward(x, dtype, 0.5, dev=d)
+    for b, n in enumerate(lens):
+        for name in ("dq", "dk", "dv", "dg", "dbeta"):
+            assert (r[name][b, max(0, min(n, T)):] == 0).all(), name
+        if n <= 0:
+            assert torch.equal(r["dstate"][b], d["d_last"][b])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_resets_and_strong_gates(dtype):
+    """Gates of -infinity (a new sequence starts), gates that leave almost nothing, gates of 0, and beta of 0 and of 1."""
+    say("gdr resets", dtype)
+    x = make(1, 333, 2, 2, 32, 64, dtype)
+    x["g"][0, 0, 0] = x["g"][0, 70] = x["g"][0, 71, 1] = -INF
+    x["g"][0, 127, 0] = -1e30
+    x["g"][0, 128:140] = -90.0
+    x["g"][0, 200:300] = 0.0
+    x["beta"][0, 100:130] = 0.0
+    x["beta"][0, 130:150, 1] = 1.0
+    forward(x, dtype, 0.3)
+    r = backward(x, dtype, 0.3)
+    assert (r["dg"][0, 70] == 0).all() and r["dg"][0, 0, 0] == 0 and r["dg"][0, 127, 0] == 0 and (r["dstate"][0, 0] == 0).all()
+    assert not (r["dg"][0, 1:70] == 0).any() and not (r["dbeta"][0, 100:130] == 0).any()
+    x["state"] = x["d_last"] = None
+    assert (backward(x, dtype, 0.3)["dg"][0, 0] == 0).all()
