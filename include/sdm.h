@@ -721,6 +721,77 @@ typedef struct sdm_gdr_step_io {
  * not). One kernel on st. */
 sdm_status sdm_gdr_step(const sdm_gdr_step_io* io, hipStream_t st);
 
+/* RMS norm of heads and their gate. */
+typedef struct sdm_gate_norm_io {
+    const void* x;          /* head h of token t at x + t * x_row + h * x_head, D contiguous columns */
+    const void* z;          /* the gates, the same way */
+    int64_t x_row, x_head, z_row, z_head;
+    void* out;              /* OUT of sdm_gate_norm, the same way; may be x or z (same strides) */
+    int64_t o_row, o_head;
+    const void* w;          /* [D] norm weights (NULL: ones) */
+    int64_t N;              /* tokens, >= 0; N * H at most 2^31 - 1 */
+    int32_t H;              /* heads of a token, >= 1 */
+    int32_t D;              /* columns of a head, 1..8192 */
+    int32_t dtype;          /* sdm_dtype of the heads (inputs, outputs and gradients) */
+    int32_t w_dtype;        /* sdm_dtype of w */
+    float eps;              /* added to the mean of squares, >= 0 */
+} sdm_gate_norm_io;
+
+/* Per head: out = x w / sqrt(mean(x^2) + eps) * z / (1 + exp(-z)). One kernel on st; float32 inside, rounded once. */
+sdm_status sdm_gate_norm(const sdm_gate_norm_io* io, hipStream_t st);
+
+typedef struct sdm_gate_norm_grad {
+    const void* d;          /* gradients of out, laid out like x with strides of their own */
+    int64_t d_row, d_head;
+    void* dx;               /* OUT [N, H, D] contiguous, in dtype (none may overlap an input) */
+    void* dz;               /* OUT [N, H, D] */
+    float* dw;              /* OUT [D] float32 (NULL: skipped) */
+    void* workspace;        /* sdm_gate_norm_workspace() bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} sdm_gate_norm_grad;
+
+/* The backward of sdm_gate_norm (io's out is not used). The weights' gradient is summed in a fixed order. Two kernels on st. */
+sdm_status sdm_gate_norm_backward(const sdm_gate_norm_io* io, const sdm_gate_norm_grad* grad, hipStream_t st);
+size_t sdm_gate_norm_workspace(const sdm_gate_norm_io* io);
+
+/* A block's residual with the norms behind it and before the next block. */
+typedef struct sdm_residual_norm_io {
+    const void* x;          /* [N, D] the residual, row t at x + t * x_row, D contiguous columns */
+    const void* y;          /* [N, D] the block's outputs */
+    void* h;                /* OUT of sdm_residual_norm (may be x or y, same strides); input of its backward */
+    void* n;                /* OUT of sdm_residual_norm (may be x or y, but not h) */
+    int64_t x_row, y_row, h_row, n_row;
+    const void* w;          /* [D] weights of h's norm (NULL: ones) */
+    const void* wy;         /* [D] weights of y's norm (NULL: ones; only with norm_y) */
+    const void* a;          /* [D] scales of what is added (NULL: ones) */
+    int64_t N;              /* rows, 0..2^31 - 1 */
+    int32_t D;              /* 1..8192 */
+    int32_t norm_y;         /* 1: y is normed before it is added */
+    int32_t dtype;          /* sdm_dtype of the rows (inputs, outputs and gradients) */
+    int32_t w_dtype;        /* sdm_dtype of w, wy and a */
+    float eps;              /* added to the means of squares, >= 0 */
+} sdm_residual_norm_io;
+
+/* Per row: h = x + a y, or x + a (y wy / sqrt(mean(y^2) + eps)), rounded to dtype; n = h w / sqrt(mean(h^2) + eps) of the
+ * rounded h. One kernel on st; float32 inside. */
+sdm_status sdm_residual_norm(const sdm_residual_norm_io* io, hipStream_t st);
+
+typedef struct sdm_residual_norm_grad {
+    const void* dh;         /* [N, D] gradients of h from elsewhere (NULL: zero), row t at dh + t * dh_row */
+    const void* dn;         /* [N, D] gradients of n */
+    int64_t dh_row, dn_row;
+    void* dx;               /* OUT [N, D] contiguous, in dtype (NULL: skipped; none may overlap an input) */
+    void* dy;               /* OUT [N, D] */
+    float *dw, *dwy, *da;   /* OUT [D] float32 (NULL: skipped; dwy only with norm_y) */
+    void* workspace;        /* sdm_residual_norm_workspace() bytes, 16-byte aligned */
+    size_t workspace_bytes;
+} sdm_residual_norm_grad;
+
+/* The backward of sdm_residual_norm at its h and y (io's x and n are not used; y is only read with norm_y or da). The
+ * weights' gradients are summed in a fixed order. Two kernels on st. */
+sdm_status sdm_residual_norm_backward(const sdm_residual_norm_io* io, const sdm_residual_norm_grad* grad, hipStream_t st);
+size_t sdm_residual_norm_workspace(const sdm_residual_norm_io* io);
+
 /* Static text for a status code. */
 const char* sdm_status_string(sdm_status s);
 

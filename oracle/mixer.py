@@ -308,3 +308,63 @@ def gdr_backward(d_o, q, k, v, g, beta, scale, state=None, d_last=None, lens=Non
     m["dv"], m["dg"], m["dbeta"] = m["dv"] * amp[:, None, :, None], m["dg"] * amp[:, None], m["dbeta"] * amp[:, None]
     r_["dstate"], m["dstate"] = R, np.sqrt(F2)[:, :, None] * amp[..., None, None] * np.ones((1, 1, dk, 1))
     return r_, m
+
+
+def _rms(x, eps):
+    return 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
+
+
+def _norm_back(d, x, w, eps):
+    """(dx, dw, |dx|, |dw|) of y = x / rms(x) w per row [.., D], and of the sums over absolute values."""
+    w = np.ones(x.shape[-1]) if w is None else w.astype(np.float64)
+    r = _rms(x, eps)
+    n, dn = x * r, d * w
+    lead = tuple(range(x.ndim - 1))
+    dx = r * (dn - n * (dn * n).mean(-1, keepdims=True))
+    return dx, (d * n).sum(lead), r * (np.abs(dn) + np.abs(n) * (np.abs(dn * n)).mean(-1, keepdims=True)), np.abs(d * n).sum(lead)
+
+
+def _sigmoid(z):
+    return np.exp(-np.logaddexp(0.0, -z))
+
+
+def gate_norm(x, z, w, eps):
+    x, z = x.astype(np.float64), z.astype(np.float64)
+    return x * _rms(x, eps) * (1.0 if w is None else w.astype(np.float64)) * z * _sigmoid(z)
+
+
+def gate_norm_backward(d, x, z, w, eps):
+    """(grads, magnitudes), dicts of dx, dz and dw."""
+    d, x, z = (t.astype(np.float64) for t in (d, x, z))
+    s = _sigmoid(z)
+    dx, dw, mx, mw = _norm_back(d * z * s, x, w, eps)
+    n = x * _rms(x, eps) * (1.0 if w is None else w.astype(np.float64))
+    dz = d * n * s * (1.0 + z * (1.0 - s))
+    return dict(dx=dx, dz=dz, dw=dw), dict(dx=mx, dz=np.abs(d * n * s) * (1.0 + np.abs(z) * (1.0 - s)), dw=mw)
+
+
+def residual_norm(x, y, w, a, norm_y, wy, eps, rounded):
+    """(h, n, |h|): n is that of `rounded`, the h that was returned."""
+    x, y = x.astype(np.float64), y.astype(np.float64)
+    if norm_y:
+        y = y * _rms(y, eps) * (1.0 if wy is None else wy.astype(np.float64))
+    y = y * (1.0 if a is None else a.astype(np.float64))
+    f = rounded.astype(np.float64)
+    return x + y, f * _rms(f, eps) * (1.0 if w is None else w.astype(np.float64)), np.abs(x) + np.abs(y)
+
+
+def residual_norm_backward(dh, dn, h, y, w, a, norm_y, wy, eps):
+    """(grads, magnitudes), dicts of dx, dy, dw, dscale and dwy."""
+    h, y, dn = (t.astype(np.float64) for t in (h, y, dn))
+    aa = np.ones(h.shape[-1]) if a is None else a.astype(np.float64)
+    dx, dw, mx, mw = _norm_back(dn, h, w, eps)
+    if dh is not None:
+        dx, mx = dx + dh.astype(np.float64), mx + np.abs(dh)
+    part = y * _rms(y, eps) * (1.0 if wy is None else wy.astype(np.float64)) if norm_y else y
+    r, m = dict(dx=dx, dw=dw, dscale=(dx * part).sum(0)), dict(dx=mx, dw=mw, dscale=(mx * np.abs(part)).sum(0))
+    if norm_y:
+        r["dy"], r["dwy"], _, _ = _norm_back(dx * aa, y, wy, eps)
+        _, _, m["dy"], m["dwy"] = _norm_back(mx * np.abs(aa), np.abs(y), None if wy is None else np.abs(wy), eps)
+    else:
+        r["dy"], m["dy"] = dx * aa, mx * np.abs(aa)
+    return r, m

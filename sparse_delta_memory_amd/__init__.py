@@ -15,6 +15,9 @@ and the dense state that stands next to the sparse one, each with its backward p
     q, k = norm_rope(q, k, wq, wk, positions, rope_table(rows, rot))
     k_idx, k_val = slot_topk(scores_a, scores_b, W)
     o, last = glr_forward(q, k, v, g)                            # glr_step: one token of many requests
+    o, last = gdr_forward(q, k, v, g, beta)                      # the delta rule in its place; gdr_step
+    y = gate_norm(o, z, w)                                       # the heads' norm and gate, before the output projection
+    h, n = residual_norm(x, block, w)                            # the residual, and the next block's norm of it
 """
 
 from __future__ import annotations
@@ -28,7 +31,8 @@ __all__ = ["P1Shape", "phase1", "phase1_pairs", "phase1_workspace_bytes", "alloc
            "alloc_dw_workspace", "DwPlan", "ReadPlan", "read_step", "gds_step", "gds_workspace_bytes", "alloc_gds_workspace", "gwr_step", "pa_step", "pa_workspace_bytes",
            "alloc_pa_workspace", "SdmError", "make_shape",
            "timing_events", "norm_rope", "norm_rope_backward", "rope_table", "slot_topk", "slot_topk_backward", "glr_forward",
-           "glr_backward", "glr_step", "glr_workspace_bytes", "gdr_forward", "gdr_backward", "gdr_step", "gdr_workspace_bytes"]
+           "glr_backward", "glr_step", "glr_workspace_bytes", "gdr_forward", "gdr_backward", "gdr_step", "gdr_workspace_bytes", "gate_norm",
+           "gate_norm_backward", "residual_norm", "residual_norm_backward"]
 
 
 def make_shape(N, C, W, R, P=1, key_bits=16, stream_offset=0, first_partial=None, valid_last=None, tile_len=128,
@@ -464,4 +468,5 @@ def pa_step(grad, snap, p1, beta, d_dva, shape: P1Shape, ti: int, step_rows: int
 
 
 from .mixer_ops import (  # noqa: E402,F401
-    gdr_backward, gdr_forward, gdr_step, gdr_workspace_bytes, glr_backward, glr_forward, glr_step, glr_workspace_bytes, norm_rope, norm_rope_backward, rope_table, slot_topk, slot_topk_backward)
+    gate_norm, gate_norm_backward, gdr_backward, gdr_forward, gdr_step, gdr_workspace_bytes, glr_backward, glr_forward, glr_step, glr_workspace_bytes, norm_rope, norm_rope_backward, residual_norm,
+    residual_norm_backward, rope_table, slot_topk, slot_topk_backward)

@@ -191,15 +191,40 @@ class GdrStepIO(ctypes.Structure):
         (f, ctypes.c_int32) for f in ("B", "H", "Hk", "dk", "dv", "dtype")] + [("scale", ctypes.c_float)]
 
 
+class GateNormIO(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("z", ctypes.c_void_p)] + [(f, ctypes.c_int64) for f in ("x_row", "x_head", "z_row", "z_head")] + [
+        ("out", ctypes.c_void_p), ("o_row", ctypes.c_int64), ("o_head", ctypes.c_int64), ("w", ctypes.c_void_p), ("N", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("H", "D", "dtype", "w_dtype")] + [("eps", ctypes.c_float)]
+
+
+class GateNormGrad(ctypes.Structure):
+    _fields_ = [("d", ctypes.c_void_p), ("d_row", ctypes.c_int64), ("d_head", ctypes.c_int64)] + [
+        (f, ctypes.c_void_p) for f in ("dx", "dz", "dw", "workspace")] + [("workspace_bytes", ctypes.c_size_t)]
+
+
+class ResidualNormIO(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("x", "y", "h", "n")] + [(f, ctypes.c_int64) for f in ("x_row", "y_row", "h_row", "n_row")] + [
+        (f, ctypes.c_void_p) for f in ("w", "wy", "a")] + [("N", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("D", "norm_y", "dtype", "w_dtype")] + [("eps", ctypes.c_float)]
+
+
+class ResidualNormGrad(ctypes.Structure):
+    _fields_ = [("dh", ctypes.c_void_p), ("dn", ctypes.c_void_p), ("dh_row", ctypes.c_int64), ("dn_row", ctypes.c_int64)] + [
+        (f, ctypes.c_void_p) for f in ("dx", "dy", "dw", "dwy", "da", "workspace")] + [("workspace_bytes", ctypes.c_size_t)]
+
+
 pack_norm_rope, pack_norm_rope_grad = packer(NormRopeIO), packer(NormRopeGrad)
 pack_slot_topk, pack_slot_topk_grad = packer(SlotTopkIO), packer(SlotTopkGrad)
 pack_glr, pack_glr_grad, pack_glr_step = packer(GlrIO), packer(GlrGrad), packer(GlrStepIO)
 pack_gdr, pack_gdr_grad, pack_gdr_step = packer(GdrIO), packer(GdrGrad), packer(GdrStepIO)
+pack_gate_norm, pack_gate_norm_grad = packer(GateNormIO), packer(GateNormGrad)
+pack_residual_norm, pack_residual_norm_grad = packer(ResidualNormIO), packer(ResidualNormGrad)
 
 EXPORTS = ["sdm_phase1_workspace", "sdm_phase1", "sdm_phase1_pairs", "sdm_dw_workspace", "sdm_dw_step", "sdm_dw_step_noalloc", "sdm_read_step",
            "sdm_gds_workspace", "sdm_gds_step", "sdm_gwr_step", "sdm_pa_workspace", "sdm_pa_step", "sdm_norm_rope",
            "sdm_norm_rope_workspace", "sdm_norm_rope_backward", "sdm_slot_topk", "sdm_slot_topk_backward", "sdm_glr_workspace",
-           "sdm_glr_forward", "sdm_glr_backward", "sdm_glr_step", "sdm_gdr_workspace", "sdm_gdr_forward", "sdm_gdr_backward", "sdm_gdr_step", "sdm_status_string", "sdm_last_error"]
+           "sdm_glr_forward", "sdm_glr_backward", "sdm_glr_step", "sdm_gdr_workspace", "sdm_gdr_forward", "sdm_gdr_backward", "sdm_gdr_step", "sdm_gate_norm", "sdm_gate_norm_workspace",
+           "sdm_gate_norm_backward", "sdm_residual_norm", "sdm_residual_norm_workspace", "sdm_residual_norm_backward", "sdm_status_string", "sdm_last_error"]
 
 _lock = threading.Lock()
 _lib = None
@@ -249,7 +274,9 @@ def load() -> ctypes.CDLL:
         for name, args in (("sdm_norm_rope", [NormRopeIO]), ("sdm_norm_rope_backward", [NormRopeIO, NormRopeGrad]),
                            ("sdm_slot_topk", [SlotTopkIO]), ("sdm_slot_topk_backward", [SlotTopkIO, SlotTopkGrad]),
                            ("sdm_glr_forward", [GlrIO]), ("sdm_glr_backward", [GlrIO, GlrGrad]), ("sdm_glr_step", [GlrStepIO]),
-                           ("sdm_gdr_forward", [GdrIO]), ("sdm_gdr_backward", [GdrIO, GdrGrad]), ("sdm_gdr_step", [GdrStepIO])):
+                           ("sdm_gdr_forward", [GdrIO]), ("sdm_gdr_backward", [GdrIO, GdrGrad]), ("sdm_gdr_step", [GdrStepIO]),
+                           ("sdm_gate_norm", [GateNormIO]), ("sdm_gate_norm_backward", [GateNormIO, GateNormGrad]),
+                           ("sdm_residual_norm", [ResidualNormIO]), ("sdm_residual_norm_backward", [ResidualNormIO, ResidualNormGrad])):
             fn = getattr(lib, name)
             fn.argtypes = [ctypes.c_void_p] * (len(args) + 1)   # the structure's bytes or a reference to it, and the stream
             fn.restype = ctypes.c_int
@@ -259,6 +286,9 @@ def load() -> ctypes.CDLL:
         lib.sdm_glr_workspace.restype = ctypes.c_size_t
         lib.sdm_gdr_workspace.argtypes = [ctypes.c_void_p, ctypes.c_int32]
         lib.sdm_gdr_workspace.restype = ctypes.c_size_t
+        for name in ("sdm_gate_norm_workspace", "sdm_residual_norm_workspace"):
+            getattr(lib, name).argtypes = [ctypes.c_void_p]
+            getattr(lib, name).restype = ctypes.c_size_t
         lib.sdm_status_string.argtypes = [ctypes.c_int]
         lib.sdm_status_string.restype = ctypes.c_char_p
         lib.sdm_last_error.argtypes = []

@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libsdm_amd.so")
 SOURCES = ["api.cpp", "phase1.hip", "phase1_tiled.hip", "dw.hip", "read.hip", "gds.hip",
-           "api_mixer.cpp", "norm_rope.hip", "slots.hip", "glr.hip", "gdr.hip"]
+           "api_mixer.cpp", "norm_rope.hip", "slots.hip", "glr.hip", "gdr.hip", "block_norms.hip"]
 ARCH = "gfx950"
 
 

@@ -1,4 +1,5 @@
-// C ABI of the mixer operators (head norms with rotation, slot selection, the gated linear recurrence):
+// C ABI of the mixer operators (head norms with rotation, slot selection, the gated linear recurrence and delta rule, a
+// block's norms):
 // argument checks on the host, then the kernel launches.
 #include <hip/hip_runtime_api.h>
 
@@ -147,6 +148,48 @@ sdm_status check_gdr(const sdm_gdr_io* io, bool backward, const char* fn) {
     if (need > 0 && (io->workspace == nullptr || io->workspace_bytes < need))
         return fail(SDM_EWORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, io->workspace == nullptr ? size_t(0) : io->workspace_bytes);
     if (!aligned(io->workspace, 256)) return fail(SDM_EALIGN, "%s: workspace must be 256-byte aligned", fn);
+    return SDM_OK;
+}
+
+constexpr int kMaxNormColumns = 8192;   // sixteen a lane of a block of 512
+
+sdm_status check_norm(int64_t N, int64_t H, int32_t D, int32_t dtype, int32_t w_dtype, float eps, const char* fn) {
+    if (N < 0 || H < 1 || N > INT32_MAX / H) return fail(SDM_ESHAPE, "%s: %lld tokens of %lld heads (N >= 0, H >= 1, N H at most 2^31 - 1)", fn,
+                                                         static_cast<long long>(N), static_cast<long long>(H));
+    if (D < 1 || D > kMaxNormColumns) return fail(SDM_ESHAPE, "%s: D = %d outside 1..%d", fn, D, kMaxNormColumns);
+    if (!known(dtype) || !known(w_dtype)) return fail(SDM_EINVAL, "%s: dtype %d, w_dtype %d", fn, dtype, w_dtype);
+    if (!(eps >= 0.0f) || std::isinf(eps)) return fail(SDM_EINVAL, "%s: eps = %g (finite, >= 0)", fn, static_cast<double>(eps));
+    return SDM_OK;
+}
+
+sdm_status check_gate_norm(const sdm_gate_norm_io* io, const char* fn) {
+    if (io == nullptr) return fail(SDM_EINVAL, "%s: io is NULL", fn);
+    const sdm_status rc = check_norm(io->N, io->H, io->D, io->dtype, io->w_dtype, io->eps, fn);
+    if (rc != SDM_OK || io->N == 0) return rc;
+    if (io->x == nullptr || io->z == nullptr) return fail(SDM_EINVAL, "%s: x and z are required", fn);
+    const uintptr_t es = size_of(io->dtype);
+    if (!aligned(io->x, es) || !aligned(io->z, es) || !aligned(io->w, size_of(io->w_dtype)))
+        return fail(SDM_EALIGN, "%s: x, z or w is not element-aligned", fn);
+    return SDM_OK;
+}
+
+sdm_status check_residual_norm(const sdm_residual_norm_io* io, const char* fn) {
+    if (io == nullptr) return fail(SDM_EINVAL, "%s: io is NULL", fn);
+    const sdm_status rc = check_norm(io->N, 1, io->D, io->dtype, io->w_dtype, io->eps, fn);
+    if (rc != SDM_OK) return rc;
+    if (io->norm_y != 0 && io->norm_y != 1) return fail(SDM_EINVAL, "%s: norm_y = %d (0 or 1)", fn, io->norm_y);
+    if (io->norm_y == 0 && io->wy != nullptr) return fail(SDM_EINVAL, "%s: wy without norm_y", fn);
+    const uintptr_t es = size_of(io->dtype), ws = size_of(io->w_dtype);
+    if (io->N > 0 && (!aligned(io->y, es) || !aligned(io->h, es) || !aligned(io->w, ws) || !aligned(io->wy, ws) || !aligned(io->a, ws)))
+        return fail(SDM_EALIGN, "%s: y, h, w, wy or a is not element-aligned", fn);
+    return SDM_OK;
+}
+
+// A backward pass's workspace; without rows none is needed, and the weights' gradients are 0.
+sdm_status check_partials(const void* ws, size_t got, size_t need, const char* fn) {
+    if (need > 0 && (ws == nullptr || got < need))
+        return fail(SDM_EWORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, ws == nullptr ? size_t(0) : got);
+    if (!aligned(ws, 16)) return fail(SDM_EALIGN, "%s: workspace is not 16-byte aligned", fn);
     return SDM_OK;
 }
 
@@ -353,6 +396,70 @@ sdm_status sdm_gdr_step(const sdm_gdr_step_io* io, hipStream_t st) {
     if (!aligned(io->state, sa) || !aligned(io->new_state, sa))
         return fail(SDM_EALIGN, "%s: state and new_state must be %d-byte aligned", fn, static_cast<int>(sa));
     return launched(sdm::gdr_step_launch(io, st), fn);
+}
+
+sdm_status sdm_gate_norm(const sdm_gate_norm_io* io, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_gate_norm";
+    const sdm_status rc = check_gate_norm(io, fn);
+    if (rc != SDM_OK || io->N == 0) return rc;
+    if (io->out == nullptr) return fail(SDM_EINVAL, "%s: out is required", fn);
+    if (!aligned(io->out, size_of(io->dtype))) return fail(SDM_EALIGN, "%s: out is not element-aligned", fn);
+    return launched(sdm::gate_norm_launch(io, st), fn);
+}
+
+size_t sdm_gate_norm_workspace(const sdm_gate_norm_io* io) {
+    if (io == nullptr || io->N < 1 || io->H < 1 || io->N > INT32_MAX / io->H || io->D < 1 || io->D > kMaxNormColumns) return 0;
+    return sdm::gate_norm_back_workspace(io->N * io->H, io->D);
+}
+
+sdm_status sdm_gate_norm_backward(const sdm_gate_norm_io* io, const sdm_gate_norm_grad* g, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_gate_norm_backward";
+    sdm_status rc = check_gate_norm(io, fn);
+    if (rc != SDM_OK) return rc;
+    if (g == nullptr) return fail(SDM_EINVAL, "%s: grad is NULL", fn);
+    if (io->N > 0 && (g->d == nullptr || g->dx == nullptr || g->dz == nullptr)) return fail(SDM_EINVAL, "%s: d, dx and dz are required", fn);
+    const uintptr_t es = size_of(io->dtype);
+    if (!aligned(g->d, es) || !aligned(g->dx, es) || !aligned(g->dz, es) || !aligned(g->dw, 4))
+        return fail(SDM_EALIGN, "%s: a gradient is not element-aligned", fn);
+    rc = check_partials(g->workspace, g->workspace_bytes, sdm_gate_norm_workspace(io), fn);
+    if (rc != SDM_OK) return rc;
+    return launched(sdm::gate_norm_back_launch(io, g, st), fn);
+}
+
+sdm_status sdm_residual_norm(const sdm_residual_norm_io* io, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_residual_norm";
+    const sdm_status rc = check_residual_norm(io, fn);
+    if (rc != SDM_OK || io->N == 0) return rc;
+    if (io->x == nullptr || io->y == nullptr || io->h == nullptr || io->n == nullptr) return fail(SDM_EINVAL, "%s: x, y, h and n are required", fn);
+    if (io->n == io->h) return fail(SDM_EINVAL, "%s: n must not be h", fn);
+    if (!aligned(io->x, size_of(io->dtype)) || !aligned(io->n, size_of(io->dtype))) return fail(SDM_EALIGN, "%s: x or n is not element-aligned", fn);
+    return launched(sdm::residual_norm_launch(io, st), fn);
+}
+
+size_t sdm_residual_norm_workspace(const sdm_residual_norm_io* io) {
+    if (io == nullptr || io->N < 1 || io->N > INT32_MAX || io->D < 1 || io->D > kMaxNormColumns) return 0;
+    return sdm::residual_norm_back_workspace(io->N, io->D);
+}
+
+sdm_status sdm_residual_norm_backward(const sdm_residual_norm_io* io, const sdm_residual_norm_grad* g, hipStream_t st) {
+    sdm::clear_error();
+    const char* fn = "sdm_residual_norm_backward";
+    sdm_status rc = check_residual_norm(io, fn);
+    if (rc != SDM_OK) return rc;
+    if (g == nullptr) return fail(SDM_EINVAL, "%s: grad is NULL", fn);
+    if (io->N > 0 && (io->h == nullptr || g->dn == nullptr || g->dy == nullptr)) return fail(SDM_EINVAL, "%s: h, dn and dy are required", fn);
+    if (io->N > 0 && io->y == nullptr && (io->norm_y || g->da != nullptr)) return fail(SDM_EINVAL, "%s: y is required with norm_y or da", fn);
+    if (!io->norm_y && g->dwy != nullptr) return fail(SDM_EINVAL, "%s: dwy without norm_y", fn);
+    const uintptr_t es = size_of(io->dtype);
+    if (!aligned(g->dh, es) || !aligned(g->dn, es) || !aligned(g->dx, es) || !aligned(g->dy, es) || !aligned(g->dw, 4) || !aligned(g->dwy, 4) ||
+        !aligned(g->da, 4))
+        return fail(SDM_EALIGN, "%s: a gradient is not element-aligned", fn);
+    rc = check_partials(g->workspace, g->workspace_bytes, sdm_residual_norm_workspace(io), fn);
+    if (rc != SDM_OK) return rc;
+    return launched(sdm::residual_norm_back_launch(io, g, st), fn);
 }
 
 }  // extern "C"

@@ -167,4 +167,12 @@ hipError_t gdr_step_launch(const sdm_gdr_step_io* io, hipStream_t st);
 size_t gdr_workspace_bytes(const sdm_gdr_io* io, bool backward);
 int gdr_lds_kernels(const void** fns, int cap);
 
+// The block's norms (validated by their entry points). workspace: bytes of the backward's partial weight gradients.
+hipError_t gate_norm_launch(const sdm_gate_norm_io* io, hipStream_t st);
+hipError_t gate_norm_back_launch(const sdm_gate_norm_io* io, const sdm_gate_norm_grad* g, hipStream_t st);
+size_t gate_norm_back_workspace(int64_t rows, int D);
+hipError_t residual_norm_launch(const sdm_residual_norm_io* io, hipStream_t st);
+hipError_t residual_norm_back_launch(const sdm_residual_norm_io* io, const sdm_residual_norm_grad* g, hipStream_t st);
+size_t residual_norm_back_workspace(int64_t rows, int D);
+
 }  // namespace sdm

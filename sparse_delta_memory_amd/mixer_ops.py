@@ -547,3 +547,121 @@ def gdr_step(q, k, v, g, beta, state, scale=None, new_state=None, slots=None, ou
         _code(fn, q), float(dk ** -0.5 if scale is None else scale))
     _call(_lib.load().sdm_gdr_step, dev, stream, io)
     return out
+
+
+# ----------------------------------------------------------------------------------- the block's norms
+
+def _gate_norm_io(fn, x, z, weight, eps, out):
+    dev = _same(fn, x, z, weight, out)
+    if x.dim() != 3:
+        raise ValueError("%s: heads are [tokens, heads, columns]" % fn)
+    _shape(fn, "z", z, x.shape)
+    if z.dtype is not x.dtype or (out is not None and out.dtype is not x.dtype):
+        raise TypeError("%s: x, z and out must have one dtype" % fn)
+    if weight is not None:
+        _shape(fn, "weight", weight, x.shape[2:])
+    if out is not None:
+        _shape(fn, "out", out, x.shape)
+    _columns(fn, x, z, weight, out)
+    N, H, D = x.shape
+    xs, zs = x.stride(), z.stride()
+    os = (0, 0) if out is None else out.stride()
+    return dev, _lib.pack_gate_norm(x.data_ptr(), z.data_ptr(), xs[0], xs[1], zs[0], zs[1], _ptr(out), os[0], os[1], _ptr(weight), N, H, D,
+                                    _code(fn, x), _lib.SDM_F32 if weight is None else _code(fn, weight), float(eps))
+
+
+def gate_norm(x, z, weight=None, eps=1e-6, out=None, stream=None):
+    """out [N, H, D]: every head of x [N, H, D] divided by its root mean square (eps added to the mean), times weight [D]
+    (float32 or bfloat16; None: ones) and silu(z) = z / (1 + exp(-z)) of its gates z [N, H, D]. D: 1..8192. out may be x or z."""
+    if out is None:
+        out = _output_like(stream, x)
+    dev, io = _gate_norm_io("gate_norm", x, z, weight, eps, out)
+    _call(_lib.load().sdm_gate_norm, dev, stream, io)
+    return out
+
+
+def gate_norm_backward(d_out, x, z, weight=None, eps=1e-6, stream=None):
+    """The backward of gate_norm at its inputs: a dict of dx, dz (like x, contiguous) and dw ([D] float32; None without
+    weight)."""
+    fn = "gate_norm_backward"
+    dev, io = _gate_norm_io(fn, x, z, weight, eps, None)
+    _same(fn, x, d_out)
+    _shape(fn, "d_out", d_out, x.shape)
+    if d_out.dtype is not x.dtype:
+        raise TypeError("%s: d_out must have x's dtype" % fn)
+    _columns(fn, d_out)
+    lib = _lib.load()
+    ws = _own(stream, max(int(lib.sdm_gate_norm_workspace(io)), 16), torch.uint8, dev)
+    dx, dz = _output(stream, x.shape, x.dtype, dev), _output(stream, x.shape, x.dtype, dev)
+    dw = None if weight is None else _output(stream, weight.shape, torch.float32, dev)
+    g = _lib.pack_gate_norm_grad(d_out.data_ptr(), d_out.stride(0), d_out.stride(1), dx.data_ptr(), dz.data_ptr(), _ptr(dw), ws.data_ptr(), ws.numel())
+    _call(lib.sdm_gate_norm_backward, dev, stream, io, g)
+    return dict(dx=dx, dz=dz, dw=dw)
+
+
+def _residual_norm_io(fn, x, y, h, n, weight, scale, norm_y, y_weight, eps):
+    """x and n are None in the backward pass."""
+    dev = _same(fn, y, x, h, n, weight, scale, y_weight)
+    if y.dim() < 1:
+        raise ValueError("%s: rows are [.., columns]" % fn)
+    D = y.shape[-1]
+    wd = None
+    for name, t in (("x", x), ("h", h), ("norm", n)):
+        if t is not None:
+            _shape(fn, name, t, y.shape)
+            if t.dtype is not y.dtype:
+                raise TypeError("%s: the rows must have one dtype" % fn)
+    if y_weight is not None and not norm_y:
+        raise ValueError("%s: y_weight is that of y's norm (norm_y)" % fn)
+    for name, t in (("weight", weight), ("scale", scale), ("y_weight", y_weight)):
+        if t is not None:
+            _shape(fn, name, t, (D,))
+            if wd is not None and t.dtype is not wd:
+                raise TypeError("%s: weight, scale and y_weight must have one dtype" % fn)
+            wd = t.dtype
+    _columns(fn, x, y, h, n, weight, scale, y_weight)
+    one = weight if weight is not None else scale if scale is not None else y_weight
+    row = lambda t: 0 if t is None else t.stride(0) if t.dim() == 2 else _row_stride(fn, t)  # noqa: E731
+    return dev, _lib.pack_residual_norm(_ptr(x), y.data_ptr(), h.data_ptr(), _ptr(n), row(x), row(y), row(h), row(n), _ptr(weight),
+                                        _ptr(y_weight), _ptr(scale), y.numel() // D if D else 0, D, 1 if norm_y else 0, _code(fn, y),
+                                        _lib.SDM_F32 if one is None else _code(fn, one), float(eps))
+
+
+def residual_norm(x, y, weight=None, scale=None, norm_y=False, y_weight=None, eps=1e-6, out=None, norm=None, stream=None):
+    """(h, n) [.., D]: the residual h = x + scale * y of a block's outputs y (with norm_y: of y divided by its root mean square,
+    times y_weight), rounded to the rows' dtype, and the next block's norm of it, n = h / rms(h) * weight (eps is added to the means
+    of squares). weight, scale, y_weight [D] in one dtype, float32 or bfloat16 (None: ones). D: 1..8192. out (h) and norm (n) may be x
+    or y, but not the same one."""
+    if out is None:
+        out = _output_like(stream, x)
+    if norm is None:
+        norm = _output_like(stream, x)
+    dev, io = _residual_norm_io("residual_norm", x, y, out, norm, weight, scale, norm_y, y_weight, eps)
+    _call(_lib.load().sdm_residual_norm, dev, stream, io)
+    return out, norm
+
+
+def residual_norm_backward(d_h, d_n, h, y, weight=None, scale=None, norm_y=False, y_weight=None, eps=1e-6, stream=None):
+    """The backward of residual_norm, from the gradients of h by way of the residual (d_h; None: zero) and of n, at the h that the
+    forward returned and its y: a dict of dx, dy (contiguous, like y), dw, dscale and dwy ([D] float32; None without that weight)."""
+    fn = "residual_norm_backward"
+    dev, io = _residual_norm_io(fn, None, y, h, None, weight, scale, norm_y, y_weight, eps)
+    _same(fn, y, d_h, d_n)
+    rows = []
+    for name, t in (("d_h", d_h), ("d_n", d_n)):
+        if t is None and name == "d_h":
+            rows.append(0)
+            continue
+        _shape(fn, name, t, y.shape)
+        if t.dtype is not y.dtype:
+            raise TypeError("%s: %s must have the rows' dtype" % (fn, name))
+        _columns(fn, t)
+        rows.append(t.stride(0) if t.dim() == 2 else _row_stride(fn, t))
+    lib = _lib.load()
+    ws = _own(stream, max(int(lib.sdm_residual_norm_workspace(io)), 16), torch.uint8, dev)
+    dx, dy = _output(stream, y.shape, y.dtype, dev), _output(stream, y.shape, y.dtype, dev)
+    dw, dwy, ds = (None if t is None else _output(stream, t.shape, torch.float32, dev) for t in (weight, y_weight, scale))
+    g = _lib.pack_residual_norm_grad(_ptr(d_h), d_n.data_ptr(), rows[0], rows[1], dx.data_ptr(), dy.data_ptr(), _ptr(dw), _ptr(dwy), _ptr(ds),
+                                     ws.data_ptr(), ws.numel())
+    _call(lib.sdm_residual_norm_backward, dev, stream, io, g)
+    return dict(dx=dx, dy=dy, dw=dw, dwy=dwy, dscale=ds)
