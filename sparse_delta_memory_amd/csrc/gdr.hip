@@ -34,17 +34,49 @@ struct Factors {
 };
 static_assert(sizeof(Factors) == kFacBytes, "a KiB");
 
-// c += a b^T of two operands in parts: all products of 24 bits, the smallest first.
+// The parts of 8 float32 values as in cut(): what a part leaves is x - hi as a product of two pairs, (hi, other) . (-1, 0) + x in one
+// instruction (3.5 a value for the three parts, 5.5 with a mask and a subtraction; exact but for subnormal parts, which are dropped).
+__device__ __forceinline__ void split(const float (&x)[8], Parts<bf16_t, 3>& o) {
+    // Not constants to the compiler: as an instruction's own operand -1 would stand for a float32.
+    uint32_t first = 0x0000BF80u, second = 0xBF800000u;
+    __asm__("" : "+s"(first));
+    __asm__("" : "+s"(second));
+    float r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = x[e];
+#pragma unroll
+    for (int s = 0; s < 3; ++s) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t w = __builtin_amdgcn_perm(__float_as_uint(r[2 * e + 1]), __float_as_uint(r[2 * e]), 0x07060302u);
+            o.p[s].w[e] = w;
+            if (s < 2) {
+                r[2 * e] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, first), r[2 * e], false);
+                r[2 * e + 1] = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, second), r[2 * e + 1], false);
+            }
+        }
+    }
+}
+__device__ __forceinline__ void split(const float (&x)[8], Parts<float, 1>& o) { cut(x, o); }
+
+// c[n] += a[n] b^T of operands in parts, N products side by side: all of 24 bits, the smallest first.
+template <typename T, int NP, int N, bool SWAP = false>
+__device__ __forceinline__ void mma_parts(const Parts<T, NP> (&a)[N], const Parts<T, NP>& b, f32x4* const (&c)[N]) {
+    constexpr int kA[6] = {2, 0, 1, 1, 0, 0}, kB[6] = {0, 2, 1, 0, 1, 0};
+#pragma unroll
+    for (int k = NP == 3 ? 0 : 5; k < 6; ++k) {
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            if (SWAP) mma(b.p[kB[k]], a[n].p[kA[k]], *c[n]);
+            else mma(a[n].p[kA[k]], b.p[kB[k]], *c[n]);
+        }
+    }
+}
 template <typename T, int NP>
 __device__ __forceinline__ void mma_parts(const Parts<T, NP>& a, const Parts<T, NP>& b, f32x4& c) {
-    if constexpr (NP == 3) {
-        mma(a.p[2], b.p[0], c);
-        mma(a.p[0], b.p[2], c);
-        mma(a.p[1], b.p[1], c);
-        mma(a.p[1], b.p[0], c);
-        mma(a.p[0], b.p[1], c);
-    }
-    mma(a.p[0], b.p[0], c);
+    const Parts<T, NP> aa[1] = {a};
+    f32x4* const cc[1] = {&c};
+    mma_parts<T, NP, 1>(aa, b, cc);
 }
 
 // Operand `pr` of a record's operands, as the lane holds it.
@@ -57,6 +89,37 @@ template <typename T, int NP>
 __device__ __forceinline__ void frag_write(char* at, int pr, int lane, const Parts<T, NP>& o) {
 #pragma unroll
     for (int s = 0; s < NP; ++s) __builtin_memcpy(at + ((pr * NP + s) * kWave + lane) * (8 * static_cast<int>(sizeof(T))), &o.p[s], sizeof(Frag<T>));
+}
+
+// x[it] += (the triangle's operand of token tile it) times y of the token pairs jb, for the pairs that there are (SWAP: transposed).
+template <bool REV, bool SWAP, typename T, int NP>
+__device__ __forceinline__ void mma_triangle(const char* at, int jb, int lane, const Parts<T, NP>& y, f32x4 (&x)[4]) {
+    constexpr int kMany = REV ? 1 : 0;   // the jb that meets all four tiles
+    if (jb == kMany) {
+        Parts<T, NP> a[4];
+        f32x4* c[4];
+        int n = 0;
+#pragma unroll
+        for (int pr = 0; pr < 6; ++pr) {
+            if (Pairs<REV>::kJb[pr] != jb) continue;
+            frag_read(at, pr, lane, a[n]);
+            c[n++] = &x[Pairs<REV>::kIt[pr]];
+        }
+        f32x4* const cc[4] = {c[0], c[1], c[2], c[3]};
+        mma_parts<T, NP, 4, SWAP>(a, y, cc);
+    } else {
+        Parts<T, NP> a[2];
+        f32x4* c[2];
+        int n = 0;
+#pragma unroll
+        for (int pr = 0; pr < 6; ++pr) {
+            if (Pairs<REV>::kJb[pr] != jb) continue;
+            frag_read(at, pr, lane, a[n]);
+            c[n++] = &x[Pairs<REV>::kIt[pr]];
+        }
+        f32x4* const cc[2] = {c[0], c[1]};
+        mma_parts<T, NP, 2, SWAP>(a, y, cc);
+    }
 }
 
 __device__ __forceinline__ int live_tokens(const int32_t* lens, int b, int T) {
@@ -300,6 +363,9 @@ struct StateAt {
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[d][r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(s, at(d, r), 0, 0));
         }
+        // Waited for here: left to the first use, in the loop over chunks, the wait would take in every chunk's tile loads.
+#pragma unroll
+        for (int d = 0; d < KT; ++d) __asm__ volatile("" : "+v"(S[d]));
     }
     __device__ __forceinline__ void write(float* p, const f32x4 (&S)[KT]) const {
         const auto s = of(p);
@@ -338,11 +404,16 @@ __device__ __forceinline__ void store_four(void* out, int64_t at, f32x4 v, int l
     }
 }
 
+// The tiles of two bfloat16 chunks fit into LDS side by side: four more waves load the next chunk's while these compute (issuing
+// its 77 KiB of loads by themselves kept the computing waves for 3000 of a chunk's 10000 cycles). float32 chunks are loaded one by one.
+template <typename T>
+constexpr int kMainThreads = sizeof(T) == 2 ? 512 : 256;
+
 // OUT: the outputs (and the last state); else the states before every chunk and the rows r, for the backward pass.
 template <typename T, int KD, bool OUT>
-__global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
+__global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_kernel(MainArgs p) {
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
-    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;   // float32 tiles of two chunks do not fit
+    constexpr bool kAhead = sizeof(T) == 2;
     constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
     constexpr int kN = kFragBytes<T> / 1024;
     constexpr int kBuf = (OUT ? 2 : 1) * kTile + kTileV + (OUT ? 2 : 1) * kFragBytes<T> + kFacBytes;
@@ -350,7 +421,8 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
     const int bh = blk / p.cols, cb = blk - bh * p.cols, b = bh / p.H, h = bh - b * p.H;
-    const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+    const bool loads = threadIdx.x >= 256;   // the waves that load ahead
+    const int tid = static_cast<int>(threadIdx.x) & 255, lane = static_cast<int>(lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
     const int c0 = 64 * cb, n0 = 16 * wave, vw = min(64, p.vd - c0);   // the block's columns, the wave's first among them
@@ -364,31 +436,40 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
     const int64_t one = static_cast<int64_t>(p.kd) * p.vd;
     const StateAt<KT> place(c0 + n0 + i16, qd, p.kd, p.vd);
 
-    f32x4 S[KT];
-#pragma unroll
-    for (int d = 0; d < KT; ++d) S[d] = f32x4{0, 0, 0, 0};
-    if (p.start != nullptr) place.read(p.start + bh * one, S);
-
     Stage<T, KD, 256> sq, sk;
     Stage<T, 64, 256> sv;
-    if (OUT) sq.init(p.q);
-    sk.init(p.k);
-    sv.init(vr);
     auto tiles = [&](int buf) { return lds + buf * kBuf; };
     auto fill = [&](int c, int buf) {
         const int64_t t0 = static_cast<int64_t>(c) * kL;
         const int left = len - c * kL;
         char* at = tiles(buf);
         sk.fill(p.k, kb_ + t0 * p.k.t, left, reinterpret_cast<T*>(at), wave, tid);
-        sv.fill(vr, vb + t0 * p.v.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
-        if (OUT) sq.fill(p.q, qb + t0 * p.q.t, left, reinterpret_cast<T*>(at + kTile + kTileV), wave, tid);
         record_fill(p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<T, !OUT>, (OUT ? 2 : 1) * kN,
                     kRecBytes<T, !OUT> - kFacBytes, at + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
+        sv.fill(vr, vb + t0 * p.v.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
+        if (OUT) sq.fill(p.q, qb + t0 * p.q.t, left, reinterpret_cast<T*>(at + kTile + kTileV), wave, tid);
     };
-    if (chunks > 0) fill(0, 0);
+    if (!kAhead || loads) {
+        if (OUT) sq.init(p.q, tid);
+        sk.init(p.k, tid);
+        sv.init(vr, tid);
+        if (chunks > 0) fill(0, 0);
+    }
+    if (kAhead && loads) {
+        for (int c = 0; c < chunks; ++c) {
+            tile_barrier();   // the chunk's tiles are complete, and the other buffer's are free
+            if (c + 1 < chunks) fill(c + 1, __builtin_amdgcn_readfirstlane((c + 1) & 1));
+        }
+        return;
+    }
+    f32x4 S[KT];
+#pragma unroll
+    for (int d = 0; d < KT; ++d) S[d] = f32x4{0, 0, 0, 0};
+    if (p.start != nullptr) place.read(p.start + bh * one, S);
+
 
     for (int c = 0; c < chunks; ++c) {
-        const int buf = kBufs == 2 ? __builtin_amdgcn_readfirstlane(c & 1) : 0, t0 = c * kL, left = len - t0;
+        const int buf = kAhead ? __builtin_amdgcn_readfirstlane(c & 1) : 0, t0 = c * kL, left = len - t0;
         char* const at = tiles(buf);
         T* const kt = reinterpret_cast<T*>(at);
         T* const vt = reinterpret_cast<T*>(at + kTile);
@@ -396,8 +477,8 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
         const char* const nf = at + (OUT ? 2 : 1) * kTile + kTileV;
         const char* const pf = nf + kFragBytes<T>;
         const Factors& fac = *reinterpret_cast<const Factors*>(nf + (OUT ? 2 : 1) * kFragBytes<T>);
-        tile_barrier();   // the chunk's tiles are complete, and the other buffer's are free
-        if (kBufs == 2 && c + 1 < chunks) fill(c + 1, buf ^ 1);
+        if (kAhead) lds_barrier();
+        else tile_barrier();
         if (!OUT) place.write(p.states + (static_cast<int64_t>(bh) * p.chunks + c) * one, S);
 
         // S^T k and S^T q
@@ -410,7 +491,7 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
             float s[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) { s[r] = S[2 * kb][r]; s[4 + r] = S[2 * kb + 1][r]; }
-            cut(s, sp);
+            split(s, sp);
             Frag<T> kf[4];
 #pragma unroll
             for (int it = 0; it < 4; ++it) kf[it] = row_frag<KD>(kt, 16 * it + i16, kb, qd);
@@ -450,14 +531,8 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
                 }
             }
             Parts<T, NP> yp;
-            cut(w, yp);
-#pragma unroll
-            for (int pr = 0; pr < 6; ++pr) {
-                if (Pairs<false>::kJb[pr] != jb) continue;
-                Parts<T, NP> np;
-                frag_read(nf, pr, lane, np);
-                mma_parts(np, yp, X[Pairs<false>::kIt[pr]]);
-            }
+            split(w, yp);
+            mma_triangle<false, false>(nf, jb, lane, yp, X);
         }
         float odd = 0.0f;
 #pragma unroll
@@ -527,7 +602,7 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
                 }
                 // The state takes the tokens' u
                 Parts<T, NP> zp;
-                cut(z, zp);
+                split(z, zp);
 #pragma unroll
                 for (int d = 0; d < KT; d += 4) {
                     Frag<T> kf[4];
@@ -541,14 +616,8 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
                 }
                 if constexpr (OUT) {
                     Parts<T, NP> up;
-                    cut(w, up);
-#pragma unroll
-                    for (int pr = 0; pr < 6; ++pr) {
-                        if (Pairs<false>::kJb[pr] != jb) continue;
-                        Parts<T, NP> pp;
-                        frag_read(pf, pr, lane, pp);
-                        mma_parts(up, pp, O[Pairs<false>::kIt[pr]]);
-                    }
+                    split(w, up);
+                    mma_triangle<false, true>(pf, jb, lane, up, O);
                 }
             }
             if constexpr (OUT) {
@@ -570,7 +639,7 @@ __global__ __launch_bounds__(256, 1) void gdr_kernel(MainArgs p) {
                 }
             }
         }
-        if (kBufs == 1) {
+        if (!kAhead) {
             lds_barrier();   // the tiles are free
             if (c + 1 < chunks) fill(c + 1, 0);
         }
@@ -611,9 +680,9 @@ struct BackArgs {
 };
 
 template <typename T, int KD>
-__global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
+__global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_back_kernel(BackArgs p) {
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
-    constexpr int kBufs = sizeof(T) == 2 ? 2 : 1;
+    constexpr bool kAhead = sizeof(T) == 2;
     constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
     constexpr int kN = kFragBytes<T> / 1024;
     constexpr int kBuf = 2 * kTile + kTileV + 2 * kFragBytes<T> + kFacBytes;
@@ -621,7 +690,8 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
     const int bh = blk / p.cols, cb = blk - bh * p.cols, b = bh / p.H, h = bh - b * p.H;
-    const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
+    const bool loads = threadIdx.x >= 256;   // the waves that load ahead
+    const int tid = static_cast<int>(threadIdx.x) & 255, lane = static_cast<int>(lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
     const int c0 = 64 * cb, n0 = 16 * wave, vw = min(64, p.vd - c0);
@@ -635,16 +705,8 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
     const int64_t one = static_cast<int64_t>(p.kd) * p.vd;
     const StateAt<KT> place(c0 + n0 + i16, qd, p.kd, p.vd);
 
-    f32x4 R[KT];
-#pragma unroll
-    for (int d = 0; d < KT; ++d) R[d] = f32x4{0, 0, 0, 0};
-    if (p.start != nullptr) place.read(p.start + bh * one, R);
-
     Stage<T, KD, 256> sq, sk;
     Stage<T, 64, 256> sd;
-    sq.init(p.q);
-    sk.init(p.k);
-    sd.init(dr);
     auto fill = [&](int c, int buf) {
         const int64_t t0 = static_cast<int64_t>(c) * kL;
         const int left = len - c * kL;
@@ -655,10 +717,27 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
         record_fill(p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<T, true> + kFragBytes<T>, 2 * kN, 2 * kFragBytes<T>,
                     at + 2 * kTile + kTileV, wave, lane);
     };
-    if (chunks > 0) fill(chunks - 1, 0);
+    if (!kAhead || loads) {
+        sq.init(p.q, tid);
+        sk.init(p.k, tid);
+        sd.init(dr, tid);
+        if (chunks > 0) fill(chunks - 1, 0);
+    }
+    if (kAhead && loads) {
+        for (int cc = 0; cc < chunks; ++cc) {
+            tile_barrier();
+            if (cc + 1 < chunks) fill(chunks - 2 - cc, __builtin_amdgcn_readfirstlane((cc + 1) & 1));
+        }
+        return;
+    }
+    f32x4 R[KT];
+#pragma unroll
+    for (int d = 0; d < KT; ++d) R[d] = f32x4{0, 0, 0, 0};
+    if (p.start != nullptr) place.read(p.start + bh * one, R);
+
 
     for (int cc = 0; cc < chunks; ++cc) {
-        const int c = chunks - 1 - cc, buf = kBufs == 2 ? __builtin_amdgcn_readfirstlane(cc & 1) : 0, t0 = c * kL, left = len - t0;
+        const int c = chunks - 1 - cc, buf = kAhead ? __builtin_amdgcn_readfirstlane(cc & 1) : 0, t0 = c * kL, left = len - t0;
         char* const at = lds + buf * kBuf;
         T* const kt = reinterpret_cast<T*>(at);
         T* const dt = reinterpret_cast<T*>(at + kTile);
@@ -666,8 +745,8 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
         const char* const nf = at + 2 * kTile + kTileV;
         const char* const pf = nf + kFragBytes<T>;
         const Factors& fac = *reinterpret_cast<const Factors*>(nf + 2 * kFragBytes<T>);
-        tile_barrier();
-        if (kBufs == 2 && c > 0) fill(c - 1, buf ^ 1);
+        if (kAhead) lds_barrier();
+        else tile_barrier();
         place.write(p.grads + (static_cast<int64_t>(bh) * p.chunks + c) * one, R);
 
         f32x4 Z[4];   // tile it: tokens 16 it + 4 quarter + r down, column n0 + lane % 16
@@ -679,7 +758,7 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
             float s[8];
 #pragma unroll
             for (int r = 0; r < 4; ++r) { s[r] = R[2 * kb][r]; s[4 + r] = R[2 * kb + 1][r]; }
-            cut(s, rp);
+            split(s, rp);
             Frag<T> kf[4];
 #pragma unroll
             for (int it = 0; it < 4; ++it) kf[it] = row_frag<KD>(kt, 16 * it + i16, kb, qd);
@@ -720,14 +799,8 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
                 for (int r = 0; r < 4; ++r) w[4 * s + r] = be[r] * Z[2 * jb + s][r];
             }
             Parts<T, NP> zp;
-            cut(w, zp);
-#pragma unroll
-            for (int pr = 0; pr < 6; ++pr) {
-                if (Pairs<true>::kJb[pr] != jb) continue;
-                Parts<T, NP> np;
-                frag_read(nf, pr, lane, np);
-                mma_parts(np, zp, X[Pairs<true>::kIt[pr]]);
-            }
+            split(w, zp);
+            mma_triangle<true, false>(nf, jb, lane, zp, X);
         }
         float odd = 0.0f;
 #pragma unroll
@@ -736,7 +809,6 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) odd = fmaf(Z[it][r], 0.0f, odd);
         }
-        float* const du = p.du + (static_cast<int64_t>(bh) * p.T + t0) * p.vd + c0 + n0 + i16;
         if (__builtin_expect(__ballot(odd != odd) != 0, 0)) {   // token by token, as forward
             for (int t = min(left, kL) - 1; t >= 0; --t) {
                 const float e = p.scale * tile_at(dt, t, n0 + i16), a = fac.one[t];
@@ -763,7 +835,7 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
                         R[2 * kb + (n >> 2)][n & 3] = sdm_decayed(a, s);
                     }
                 }
-                if (qd == 0 && n0 + i16 < vw) du[static_cast<int64_t>(t) * p.vd] = sum;
+                if (qd == 0 && n0 + i16 < vw) p.du[(static_cast<int64_t>(bh) * p.T + t0 + t) * p.vd + c0 + n0 + i16] = sum;
             }
         } else {
             const float all = fac.f[kL - 1];
@@ -784,8 +856,8 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
                     }
                 }
                 Parts<T, NP> ep, wp;
-                cut(e, ep);
-                cut(w, wp);
+                split(e, ep);
+                split(w, wp);
 #pragma unroll
                 for (int d = 0; d < KT; d += 4) {
                     Frag<T> qf[4], kf[4];
@@ -803,6 +875,7 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
                     }
                 }
             }
+            float* const du = p.du + (static_cast<int64_t>(bh) * p.T + t0) * p.vd + c0 + n0 + i16;
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
 #pragma unroll
@@ -812,7 +885,7 @@ __global__ __launch_bounds__(256, 1) void gdr_back_kernel(BackArgs p) {
                 }
             }
         }
-        if (kBufs == 1) {
+        if (!kAhead) {
             lds_barrier();
             if (c > 0) fill(c - 1, 0);
         }
@@ -1024,8 +1097,8 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
                 if (t < all) p.dbeta[row0 + static_cast<int64_t>(t) * p.H] = db_;
             }
             Parts<T, NP> up, wp;
-            cut(u, up);
-            cut(w, wp);
+            split(u, up);
+            split(w, wp);
 #pragma unroll
             for (int s = 0; s < NP; ++s) {
                 if constexpr (sizeof(T) == 2) {
@@ -1102,7 +1175,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
 #pragma unroll
     for (int kb = 0; kb < VB; ++kb) {
         Parts<T, NP> sp;
-        cut(S[kb], sp);
+        split(S[kb], sp);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
             const Frag<T> df = row_frag<VD>(dt, 16 * it + i16, kb, qd);
@@ -1166,7 +1239,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
 #pragma unroll
         for (int kb = 0; kb < VB; ++kb) {
             Parts<T, NP> rp;
-            cut(R[kb], rp);
+            split(R[kb], rp);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 Parts<T, NP> up;
@@ -1536,8 +1609,8 @@ hipError_t chunk_go(const sdm_gdr_io* io, char* rec, hipStream_t st) {
 template <typename T, bool OUT>
 hipError_t main_go(const sdm_gdr_io* io, const MainArgs& a, hipStream_t st) {
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(io->B) * io->H * a.cols);
-    if (padded(io->dk) == 64) gdr_kernel<T, 64, OUT><<<grid, 256, main_lds<T, 64>(OUT), st>>>(a);
-    else gdr_kernel<T, 128, OUT><<<grid, 256, main_lds<T, 128>(OUT), st>>>(a);
+    if (padded(io->dk) == 64) gdr_kernel<T, 64, OUT><<<grid, kMainThreads<T>, main_lds<T, 64>(OUT), st>>>(a);
+    else gdr_kernel<T, 128, OUT><<<grid, kMainThreads<T>, main_lds<T, 128>(OUT), st>>>(a);
     return hipGetLastError();
 }
 
@@ -1615,8 +1688,8 @@ hipError_t backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st)
     const BackArgs b{q, k, d, io->lens, io->T, io->H, chunks, cols, io->dk, io->dv, io->scale, ws + l.rec, g->d_last, g->d_state,
                      reinterpret_cast<float*>(ws + l.grads), reinterpret_cast<float*>(ws + l.du)};
     const unsigned grid = static_cast<unsigned>(bh * cols);
-    if (padded(io->dk) == 64) gdr_back_kernel<T, 64><<<grid, 256, main_lds<T, 64>(true), st>>>(b);
-    else gdr_back_kernel<T, 128><<<grid, 256, main_lds<T, 128>(true), st>>>(b);
+    if (padded(io->dk) == 64) gdr_back_kernel<T, 64><<<grid, kMainThreads<T>, main_lds<T, 64>(true), st>>>(b);
+    else gdr_back_kernel<T, 128><<<grid, kMainThreads<T>, main_lds<T, 128>(true), st>>>(b);
     if ((e = hipGetLastError()) != hipSuccess || io->T == 0) return e;
     const bool fold = per > 1;
     GradArgs a{q, k, v, d, io->g, io->beta, io->g_b, io->g_t, io->g_h, io->e_b, io->e_t, io->e_h, io->lens, io->T, io->H, chunks, io->dk, io->dv,

@@ -257,9 +257,10 @@ struct Stage {
     static_assert(kStep % 16 == 0 || (kStep % 8 == 0 && kPieces == 32), "a thread's rows have one twist");
     uint32_t off;      // of the thread's first piece from the chunk's first row, bytes; out of any range past the head's width
 
-    __device__ __forceinline__ void init(const Rows& s) {
-        const int row = static_cast<int>(threadIdx.x) / kPieces;
-        const int c = (static_cast<int>(threadIdx.x) % kPieces) ^ twist<T, W>(row);
+    __device__ __forceinline__ void init(const Rows& s) { init(s, static_cast<int>(threadIdx.x)); }
+    __device__ __forceinline__ void init(const Rows& s, int tid) {
+        const int row = tid / kPieces;
+        const int c = (tid % kPieces) ^ twist<T, W>(row);
         off = c * kElems < s.width ? (static_cast<uint32_t>(row) * static_cast<uint32_t>(s.t) * static_cast<uint32_t>(sizeof(T)) + c * 16) : 0xC0000000u;
     }
     // base: the chunk's first row; left: its tokens. Complete after a wait for vector memory and a barrier.
