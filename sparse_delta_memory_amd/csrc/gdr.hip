@@ -21,10 +21,13 @@ namespace {
 constexpr int kRow = 68;      // floats between the rows of a 64 x 64 matrix in LDS
 constexpr int kFacBytes = 4 * kL * 4;
 
-// Bytes of a chunk's score operands (Pairs) in all their parts.
+// A triangle of 64 x 64 token pairs as operands of matrix products. In a record: its ten 16 x 16 tiles that are not 0, float32,
+// a KiB each, the lane's four values together: row lane % 16 of tile row it, columns 4 (lane / 16) + r of tile column jt; lower
+// triangles (jt <= it) by rows of tiles, upper ones by columns. In LDS:
+// twelve halves of the six operands of Pairs, in parts.
+constexpr int kTriBytes = 10 * 1024;
 template <typename T>
-constexpr int kFragBytes = 6 * kParts<T> * kWave * 8 * static_cast<int>(sizeof(T));
-
+constexpr int kFragBytes = 12 * kParts<T> * kWave * 4 * static_cast<int>(sizeof(T));
 // A chunk's factors, in its record behind the operands.
 struct Factors {
     float f[kL];      // exp(G_i)
@@ -80,15 +83,35 @@ __device__ __forceinline__ void mma_parts(const Parts<T, NP>& a, const Parts<T, 
 }
 
 // Operand `pr` of a record's operands, as the lane holds it.
-template <typename T, int NP>
-__device__ __forceinline__ void frag_read(const char* at, int pr, int lane, Parts<T, NP>& o) {
+template <int NP>
+__device__ __forceinline__ void frag_read(const char* at, int pr, int lane, Parts<bf16_t, NP>& o) {
 #pragma unroll
-    for (int s = 0; s < NP; ++s) __builtin_memcpy(&o.p[s], at + ((pr * NP + s) * kWave + lane) * (8 * static_cast<int>(sizeof(T))), sizeof(Frag<T>));
+    for (int s = 0; s < NP; ++s) o.p[s].w = *reinterpret_cast<const u32x4*>(at + ((pr * NP + s) * kWave + lane) * 16);
 }
-template <typename T, int NP>
-__device__ __forceinline__ void frag_write(char* at, int pr, int lane, const Parts<T, NP>& o) {
+template <int NP>
+__device__ __forceinline__ void frag_read(const char* at, int pr, int lane, Parts<float, NP>& o) {
 #pragma unroll
-    for (int s = 0; s < NP; ++s) __builtin_memcpy(at + ((pr * NP + s) * kWave + lane) * (8 * static_cast<int>(sizeof(T))), &o.p[s], sizeof(Frag<T>));
+    for (int h = 0; h < 2; ++h) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(at + ((2 * pr + h) * kWave + lane) * 16);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o.p[0].v[4 * h + r] = x[r];
+    }
+}
+// Half of an operand: tokens 16 jt + 4 quarter + r (half jt % 2) of row 16 it + lane % 16.
+template <typename T>
+__device__ __forceinline__ void half_write(char* at, int pr, int half, int lane, f32x4 s) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            *reinterpret_cast<u32x2*>(at + ((pr * 3 + k) * kWave + lane) * 16 + 8 * half) =
+                u32x2{__builtin_amdgcn_perm(__float_as_uint(s[1]), __float_as_uint(s[0]), 0x07060302u),
+                      __builtin_amdgcn_perm(__float_as_uint(s[3]), __float_as_uint(s[2]), 0x07060302u)};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] -= __uint_as_float(__float_as_uint(s[r]) & 0xFFFF0000u);
+        }
+    } else {
+        *reinterpret_cast<f32x4*>(at + ((2 * pr + half) * kWave + lane) * 16) = s;
+    }
 }
 
 // x[it] += (the triangle's operand of token tile it) times y of the token pairs jb, for the pairs that there are (SWAP: transposed).
@@ -130,7 +153,7 @@ __device__ __forceinline__ int live_tokens(const int32_t* lens, int b, int T) {
 // ------------------------------------------------------------------------------------------ chunk records
 //
 // What of a chunk does not depend on the state, for every chunk at once: N, the scores of its tokens, and its factors,
-// as the operands that the kernels along the time axis take. Forward: N and D (q k^T). Backward: N, N^T and D (q k^T)
+// in the layout that the kernels along the time axis take. Forward: N and D (q k^T). Backward: N, N^T and D (q k^T)
 // transposed. A block of four waves per chunk. N's diagonal blocks of 16 come from substitution (a column of a
 // block per lane, all four blocks at once), the rest by block columns, a wave each, through float32 products.
 struct ChunkArgs {
@@ -143,12 +166,12 @@ struct ChunkArgs {
     char* rec;
 };
 
-template <typename T, bool BACK>
-constexpr int kRecBytes = (BACK ? 3 : 2) * kFragBytes<T> + kFacBytes;
+template <bool BACK>
+constexpr int kRecBytes = (BACK ? 3 : 2) * kTriBytes + kFacBytes;
 
 template <typename T, int KD, bool BACK>
 __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
-    constexpr int KB = KD / 32, NP = kParts<T>;
+    constexpr int KB = KD / 32;
     extern __shared__ __align__(16) char lds[];
     T* kt = reinterpret_cast<T*>(lds);
     T* qt = kt + kL * KD;
@@ -165,7 +188,7 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
     const int64_t t0 = static_cast<int64_t>(c) * kL;
-    char* rec = p.rec + static_cast<int64_t>(blk) * kRecBytes<T, BACK>;
+    char* rec = p.rec + static_cast<int64_t>(blk) * kRecBytes<BACK>;
 
     Stage<T, KD, 256> sq, sk;
     sk.init(p.k);
@@ -179,7 +202,7 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
         const float e = live ? p.beta[b * p.e_b + t * p.e_t + h * p.e_h] : 0.0f;
         gate_factors<false>(g, 1.0f, 1.0f, gates, lane);
         beta[lane] = e;
-        Factors* f = reinterpret_cast<Factors*>(rec + kRecBytes<T, BACK> - kFacBytes);
+        Factors* f = reinterpret_cast<Factors*>(rec + kRecBytes<BACK> - kFacBytes);
         f->f[lane] = gates.f[lane];
         f->u[lane] = gates.u[lane];
         f->beta[lane] = e;
@@ -187,65 +210,38 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
     }
     tile_barrier();
 
-    // Tiles of 16 x 16 tokens: twelve of the scores, dealt to the waves with the ten of A.
-    char* const scores = rec + (BACK ? 2 : 1) * kFragBytes<T>;
-    for (int e = wave; e < 22; e += 4) {
-        int it = 0, jt = 0;
-        const bool isA = e >= 12;
-        if (isA) {
-            const int n = e - 12;   // (it, jt), jt <= it, by rows
-            it = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0;
-            jt = n - it * (it + 1) / 2;
-        } else {
-#pragma unroll
-            for (int k = 0; k < 6; ++k) {
-                if (k == e >> 1) {
-                    it = Pairs<BACK>::kIt[k];
-                    jt = 2 * Pairs<BACK>::kJb[k] + (e & 1);
-                }
-            }
-        }
+    // Tiles of 16 x 16 tokens: ten of the scores, dealt to the waves with the ten of A.
+    char* const scores = rec + (BACK ? 2 : 1) * kTriBytes;
+    for (int e = wave; e < 20; e += 4) {
+        const bool isA = e >= 10;
+        const int n = isA ? e - 10 : e, hi = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0, lo = n - hi * (hi + 1) / 2;
+        const int it = BACK && !isA ? lo : hi, jt = BACK && !isA ? hi : lo;
         const bool rev = BACK && !isA;
         T* const x = !isA && !BACK ? qt : kt;
         T* const y = !isA && BACK ? qt : kt;
-        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // token 16 jt + 4 quarter + r down, token 16 it + lane % 16 across
-        if (rev ? jt >= it : jt <= it) {
-            f32x4 a = {0, 0, 0, 0};
+        f32x4 a = {0, 0, 0, 0}, s;   // token 16 jt + 4 quarter + r down, token 16 it + lane % 16 across
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) mma(row_frag<KD>(y, 16 * jt + i16, kb, qd), row_frag<KD>(x, 16 * it + i16, kb, qd), a);
-            const float m = isA ? 1.0f : p.scale;
-            if (jt == it) {
-                const float lhi = gates.lhi[16 * it + i16], llo = gates.llo[16 * it + i16];
-                const f32x4 jh = *reinterpret_cast<const f32x4*>(&gates.lhi[16 * jt + 4 * qd]);
-                const f32x4 jl = *reinterpret_cast<const f32x4*>(&gates.llo[16 * jt + 4 * qd]);
+        for (int kb = 0; kb < KB; ++kb) mma(row_frag<KD>(y, 16 * jt + i16, kb, qd), row_frag<KD>(x, 16 * it + i16, kb, qd), a);
+        const float m = isA ? 1.0f : p.scale;
+        if (jt == it) {
+            const float lhi = gates.lhi[16 * it + i16], llo = gates.llo[16 * it + i16];
+            const f32x4 jh = *reinterpret_cast<const f32x4*>(&gates.lhi[16 * jt + 4 * qd]);
+            const f32x4 jl = *reinterpret_cast<const f32x4*>(&gates.llo[16 * jt + 4 * qd]);
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int j = 4 * qd + r;
-                    const float d = (lhi - jh[r]) + (llo - jl[r]);
-                    const float w = __builtin_amdgcn_exp2f(rev ? -d : d);
-                    s[r] = (rev ? j >= i16 : isA ? j < i16 : j <= i16) ? sdm_decayed(w * m, a[r]) : 0.0f;
-                }
-            } else {
-                const float ot = (rev ? gates.down : gates.up)[16 * it + i16] * (m * gates.tau[4 * it + jt]);
-                const f32x4 d = *reinterpret_cast<const f32x4*>(&(rev ? gates.up : gates.down)[16 * jt + 4 * qd]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] = sdm_decayed(ot * d[r], a[r]);
-            }
-        }
-        if (isA) {
-            *reinterpret_cast<f32x4*>(A + (16 * it + i16) * kRow + 16 * jt + 4 * qd) = f32x4{s[0], s[1], s[2], s[3]};
-        } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int k = 0; k < NP; ++k) {
-                *reinterpret_cast<u32x2*>(scores + (((e >> 1) * NP + k) * kWave + lane) * 16 + 8 * (e & 1)) =
-                    u32x2{__builtin_amdgcn_perm(__float_as_uint(s[1]), __float_as_uint(s[0]), 0x07060302u),
-                          __builtin_amdgcn_perm(__float_as_uint(s[3]), __float_as_uint(s[2]), 0x07060302u)};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] -= __uint_as_float(__float_as_uint(s[r]) & 0xFFFF0000u);
+            for (int r = 0; r < 4; ++r) {
+                const int j = 4 * qd + r;
+                const float d = (lhi - jh[r]) + (llo - jl[r]);
+                const float w = __builtin_amdgcn_exp2f(rev ? -d : d);
+                s[r] = (rev ? j >= i16 : isA ? j < i16 : j <= i16) ? sdm_decayed(w * m, a[r]) : 0.0f;
             }
         } else {
-            *reinterpret_cast<f32x4*>(scores + ((e >> 1) * kWave + lane) * 32 + 16 * (e & 1)) = f32x4{s[0], s[1], s[2], s[3]};
+            const float ot = (rev ? gates.down : gates.up)[16 * it + i16] * (m * gates.tau[4 * it + jt]);
+            const f32x4 d = *reinterpret_cast<const f32x4*>(&(rev ? gates.up : gates.down)[16 * jt + 4 * qd]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) s[r] = sdm_decayed(ot * d[r], a[r]);
         }
+        if (isA) *reinterpret_cast<f32x4*>(A + (16 * it + i16) * kRow + 16 * jt + 4 * qd) = s;
+        else *reinterpret_cast<f32x4*>(scores + n * 1024 + lane * 16) = s;
     }
     lds_barrier();
 
@@ -293,30 +289,16 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
     }
     lds_barrier();
 
-    for (int e = wave; e < (BACK ? 12 : 6); e += 4) {
-        const bool tr = e >= 6;
-        const int pr = tr ? e - 6 : e;
-        int it = 0, jb = 0;
+    for (int e = wave; e < (BACK ? 20 : 10); e += 4) {
+        const int n = e >= 10 ? e - 10 : e, hi = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0, lo = n - hi * (hi + 1) / 2;
+        f32x4 x;
+        if (e < 10) {
+            x = *reinterpret_cast<const f32x4*>(N + (16 * hi + i16) * kRow + 16 * lo + 4 * qd);
+        } else {   // row 16 lo + lane % 16 of N^T
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
-            if (k == pr) {
-                it = tr ? Pairs<true>::kIt[k] : Pairs<false>::kIt[k];
-                jb = tr ? Pairs<true>::kJb[k] : Pairs<false>::kJb[k];
-            }
+            for (int r = 0; r < 4; ++r) x[r] = N[(16 * hi + 4 * qd + r) * kRow + 16 * lo + i16];
         }
-        float x[8];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int jt = 2 * jb + s;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                if (tr) x[4 * s + r] = jt >= it ? N[(16 * jt + 4 * qd + r) * kRow + 16 * it + i16] : 0.0f;
-                else x[4 * s + r] = jt <= it ? N[(16 * it + i16) * kRow + 16 * jt + 4 * qd + r] : 0.0f;
-            }
-        }
-        Parts<T, NP> o;
-        cut(x, o);
-        frag_write(rec + (tr ? kFragBytes<T> : 0), pr, lane, o);
+        *reinterpret_cast<f32x4*>(rec + e * 1024 + lane * 16) = x;
     }
 }
 
@@ -377,10 +359,36 @@ struct StateAt {
     }
 };
 
-// Copies KiB pieces of a record to LDS, dealt to four waves: the first n, then the factors.
-__device__ __forceinline__ void record_fill(const char* rec, int n, int fac_off, char* to, int wave, int lane) {
-    const u32x4 rsrc = buffer_of(rec, fac_off + kFacBytes);
-    for (int i = wave; i <= n; i += 4) to_lds16(rsrc, to + i * 1024, static_cast<uint32_t>((i < n ? i * 1024 : fac_off) + lane * 16));
+// M triangles of a record (`tri`: the first) to LDS as operands, by four waves, and the factors behind them. The operands' halves
+// that hold nothing are written once per buffer (record_zero).
+template <typename T, int M, bool REV>
+__device__ __forceinline__ void record_fill(const char* tri, const char* fac, char* to, int wave, int lane) {
+    f32x4 x[(M * 10 + 3) / 4], f;
+#pragma unroll
+    for (int u = 0; u < (M * 10 + 3) / 4; ++u) {
+        const int e = wave + 4 * u;
+        if (e < M * 10) x[u] = *reinterpret_cast<const f32x4*>(tri + e * 1024 + lane * 16);
+    }
+    if (wave == 3) f = *reinterpret_cast<const f32x4*>(fac + lane * 16);
+#pragma unroll
+    for (int u = 0; u < (M * 10 + 3) / 4; ++u) {
+        const int e = wave + 4 * u;
+        if (e >= M * 10) continue;
+        const int m = M > 1 && e >= 10 ? 1 : 0, n = e - 10 * m, hi = n >= 6 ? 3 : n >= 3 ? 2 : n >= 1 ? 1 : 0, lo = n - hi * (hi + 1) / 2;
+        const int it = REV ? lo : hi, jt = REV ? hi : lo;
+        // Pairs' place of (it, jt / 2)
+        const int pr = REV ? (it < 2 ? 2 * it + (jt >> 1) : it + 2) : (it < 2 ? it : 2 * it - 2 + (jt >> 1));
+        half_write<T>(to + m * kFragBytes<T>, pr, jt & 1, lane, x[u]);
+    }
+    if (wave == 3) *reinterpret_cast<f32x4*>(to + M * kFragBytes<T> + lane * 16) = f;
+}
+template <typename T, int M, bool REV>
+__device__ __forceinline__ void record_zero(char* to, int wave, int lane) {
+    // Forward the tiles (0, 1) and (2, 3), backwards (1, 0) and (3, 2).
+    for (int e = wave; e < 2 * M; e += 4) {
+        const int m = e >> 1, pr = REV ? (e & 1 ? 5 : 2) : (e & 1 ? 3 : 0);
+        half_write<T>(to + m * kFragBytes<T>, pr, REV ? 0 : 1, lane, f32x4{0, 0, 0, 0});
+    }
 }
 
 // 8 tokens' values at one column, as col_frag gives them.
@@ -415,7 +423,6 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
     constexpr bool kAhead = sizeof(T) == 2;
     constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
-    constexpr int kN = kFragBytes<T> / 1024;
     constexpr int kBuf = (OUT ? 2 : 1) * kTile + kTileV + (OUT ? 2 : 1) * kFragBytes<T> + kFacBytes;
     extern __shared__ __align__(16) char lds[];
 
@@ -444,15 +451,16 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
         const int left = len - c * kL;
         char* at = tiles(buf);
         sk.fill(p.k, kb_ + t0 * p.k.t, left, reinterpret_cast<T*>(at), wave, tid);
-        record_fill(p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<T, !OUT>, (OUT ? 2 : 1) * kN,
-                    kRecBytes<T, !OUT> - kFacBytes, at + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
         sv.fill(vr, vb + t0 * p.v.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
         if (OUT) sq.fill(p.q, qb + t0 * p.q.t, left, reinterpret_cast<T*>(at + kTile + kTileV), wave, tid);
+        const char* rec = p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<!OUT>;
+        record_fill<T, OUT ? 2 : 1, false>(rec, rec + kRecBytes<!OUT> - kFacBytes, at + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
     };
     if (!kAhead || loads) {
         if (OUT) sq.init(p.q, tid);
         sk.init(p.k, tid);
         sv.init(vr, tid);
+        for (int n = 0; n < (kAhead ? 2 : 1); ++n) record_zero<T, OUT ? 2 : 1, false>(tiles(n) + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
         if (chunks > 0) fill(0, 0);
     }
     if (kAhead && loads) {
@@ -684,7 +692,6 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
     constexpr bool kAhead = sizeof(T) == 2;
     constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
-    constexpr int kN = kFragBytes<T> / 1024;
     constexpr int kBuf = 2 * kTile + kTileV + 2 * kFragBytes<T> + kFacBytes;
     extern __shared__ __align__(16) char lds[];
 
@@ -714,13 +721,14 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
         sk.fill(p.k, kb_ + t0 * p.k.t, left, reinterpret_cast<T*>(at), wave, tid);
         sd.fill(dr, db + t0 * p.d.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
         sq.fill(p.q, qb + t0 * p.q.t, left, reinterpret_cast<T*>(at + kTile + kTileV), wave, tid);
-        record_fill(p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<T, true> + kFragBytes<T>, 2 * kN, 2 * kFragBytes<T>,
-                    at + 2 * kTile + kTileV, wave, lane);
+        const char* rec = p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<true>;
+        record_fill<T, 2, true>(rec + kTriBytes, rec + 3 * kTriBytes, at + 2 * kTile + kTileV, wave, lane);
     };
     if (!kAhead || loads) {
         sq.init(p.q, tid);
         sk.init(p.k, tid);
         sd.init(dr, tid);
+        for (int n = 0; n < (kAhead ? 2 : 1); ++n) record_zero<T, 2, true>(lds + n * kBuf + 2 * kTile + kTileV, wave, lane);
         if (chunks > 0) fill(chunks - 1, 0);
     }
     if (kAhead && loads) {
@@ -926,23 +934,6 @@ __device__ __forceinline__ f32x4 tile_four(bf16_t* tile, int row, int col) {
 template <int W>
 __device__ __forceinline__ f32x4 tile_four(float* tile, int row, int col) {
     return *reinterpret_cast<const f32x4*>(piece<float, W>(tile, row, col >> 2));
-}
-
-// Half of a score operand: tokens 16 jt + 4 quarter + r (half jt % 2) of row 16 it + lane % 16.
-template <typename T, int NP>
-__device__ __forceinline__ void score_write(char* at, int pr, int half, int lane, float (&s)[4]) {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            *reinterpret_cast<u32x2*>(at + ((pr * NP + k) * kWave + lane) * 16 + 8 * half) =
-                u32x2{__builtin_amdgcn_perm(__float_as_uint(s[1]), __float_as_uint(s[0]), 0x07060302u),
-                      __builtin_amdgcn_perm(__float_as_uint(s[3]), __float_as_uint(s[2]), 0x07060302u)};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) s[r] -= __uint_as_float(__float_as_uint(s[r]) & 0xFFFF0000u);
-        }
-    } else {
-        *reinterpret_cast<f32x4*>(at + (pr * kWave + lane) * 32 + 16 * half) = f32x4{s[0], s[1], s[2], s[3]};
-    }
 }
 
 // Scores a[r] (token 16 jt + 4 quarter + r, for row 16 it + lane % 16) times m and the decay between the two; REV: of later
@@ -1166,7 +1157,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
             }
             decay_scores<false, false>(gates, it, jt, i16, qd, p.scale, a, s);
         }
-        score_write<T, NP>(scores, pr, e & 1, lane, s);
+        half_write<T>(scores, pr, e & 1, lane, f32x4{s[0], s[1], s[2], s[3]});
     }
     // S E and S dv
     f32x4 Q[4], K[4];   // tile it: columns n0 + 4 quarter + r down, token 16 it + lane % 16
@@ -1226,7 +1217,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
             }
             decay_scores<true, false>(gates, it, jt, i16, qd, p.scale, a, s);
         }
-        score_write<T, NP>(scores, pr, e & 1, lane, s);
+        half_write<T>(scores, pr, e & 1, lane, f32x4{s[0], s[1], s[2], s[3]});
     }
     lds_barrier();   // complete, and d_o's tile is free
     sq.fill(p.q, static_cast<const T*>(p.q.p) + b * p.q.b + (h / p.q.per) * p.q.h + static_cast<int64_t>(t0) * p.q.t, left, qt, wave, tid);
@@ -1293,7 +1284,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
 #pragma unroll
             for (int r = 0; r < 4; ++r) s[r] += s2[r];   // one of the two is 0
         }
-        score_write<T, NP>(scores, e >> 1, e & 1, lane, s);
+        half_write<T>(scores, e >> 1, e & 1, lane, f32x4{s[0], s[1], s[2], s[3]});
     }
     lds_barrier();
 #pragma unroll
@@ -1570,7 +1561,6 @@ struct GdrLayout {
 };
 GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
     const size_t bh = static_cast<size_t>(io->B) * io->H, n = bh * chunks_of(io->T), rows = bh * io->T;
-    const bool bf = io->dtype == SDM_BF16;
     GdrLayout l{};
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -1579,7 +1569,7 @@ GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
         return o;
     };
     if (backward) {
-        l.rec = take(n * (bf ? kRecBytes<bf16_t, true> : kRecBytes<float, true>));
+        l.rec = take(n * kRecBytes<true>);
         l.states = take(n * io->dk * io->dv * 4);
         l.grads = take(n * io->dk * io->dv * 4);
         l.miss = take(rows * io->dv * 4);
@@ -1589,7 +1579,7 @@ GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
             l.fk = take(rows * io->dk * 4);
         }
     } else {
-        l.rec = take(n * (bf ? kRecBytes<bf16_t, false> : kRecBytes<float, false>));
+        l.rec = take(n * kRecBytes<false>);
     }
     l.total = at;
     return l;
