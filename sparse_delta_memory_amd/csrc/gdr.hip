@@ -145,6 +145,14 @@ __device__ __forceinline__ void mma_triangle(const char* at, int jb, int lane, c
     }
 }
 
+// The descriptor of a buffer that is the same for all lanes, in scalar registers (in vector registers every load is a loop).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void* p, int bytes) {
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(u)));
+    const uint32_t hi = static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(u >> 32)));
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((static_cast<uint64_t>(hi) << 32) | lo), 0, bytes, 0x00027000);
+}
+
 __device__ __forceinline__ int live_tokens(const int32_t* lens, int b, int T) {
     const int n = lens != nullptr ? lens[b] : T;
     return n < 0 ? 0 : n > T ? T : n;
@@ -313,13 +321,20 @@ struct MainArgs {
     int kd, vd;
     float scale;
     const char* rec;
+    int rec_bytes;
     const float* start;       // [B H] states [kd, vd] (NULL: zero)
     float* last;              // [B H] (NULL: not kept)
     void* out;                // [B, T, H, vd] (OUT)
     int64_t o_b, o_t, o_h;
     int out_wide;
-    float* states;            // the states before every chunk [B H, chunks] (!OUT), and r [B H, T, vd]
+    float* states;            // the states before every chunk [B H, chunks] (states pass), and r [B H, T, vd]
     float* miss;
+    // Segments of the time axis, `seg` chunks each. from: the states before every segment [B H, nseg] (NULL with one segment:
+    // start). Segments pass: own and move take every segment's own state, from nothing, and its transition [kd, kd], of which
+    // the first `made` are made; blocks past `cols` are the transition's.
+    int nseg, seg, made;
+    const float* from;
+    float *own, *move;
 };
 
 // A wave's part of a state: rows 32 (d / 2) + 8 quarter + 4 (d % 2) + r of tile d, one column per lane, read and written
@@ -417,8 +432,9 @@ __device__ __forceinline__ void store_four(void* out, int64_t at, f32x4 v, int l
 template <typename T>
 constexpr int kMainThreads = sizeof(T) == 2 ? 512 : 256;
 
-// OUT: the outputs (and the last state); else the states before every chunk and the rows r, for the backward pass.
-template <typename T, int KD, bool OUT>
+// OUT: the outputs (and the last state). Else the states before every chunk and the rows r, for the backward pass; or (SEG)
+// the segments' own states and transitions. The transition is the rule on the columns of the unit matrix, whose values are 0.
+template <typename T, int KD, bool OUT, bool SEG>
 __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_kernel(MainArgs p) {
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
     constexpr bool kAhead = sizeof(T) == 2;
@@ -427,21 +443,26 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
     extern __shared__ __align__(16) char lds[];
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    const int bh = blk / p.cols, cb = blk - bh * p.cols, b = bh / p.H, h = bh - b * p.H;
+    const int per = SEG ? p.cols + (p.kd + 63) / 64 : p.cols, nseg = SEG ? p.made : p.nseg;   // blocks of a segment, segments
+    const int bs = blk / per, bh = bs / nseg, si = bs - bh * nseg, b = bh / p.H, h = bh - b * p.H;
+    const bool unit = SEG && blk - bs * per >= p.cols;
+    const int cb = blk - bs * per - (unit ? p.cols : 0), vd = unit ? p.kd : p.vd;
     const bool loads = threadIdx.x >= 256;   // the waves that load ahead
     const int tid = static_cast<int>(threadIdx.x) & 255, lane = static_cast<int>(lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
-    const int c0 = 64 * cb, n0 = 16 * wave, vw = min(64, p.vd - c0);   // the block's columns, the wave's first among them
-    const int len = __builtin_amdgcn_readfirstlane(live_tokens(p.lens, b, p.T)), chunks = (len + kL - 1) / kL;
+    const int c0 = 64 * cb, n0 = 16 * wave, vw = min(64, vd - c0);   // the block's columns, the wave's first among them
+    const int len = __builtin_amdgcn_readfirstlane(live_tokens(p.lens, b, p.T));
+    // The segment's chunks.
+    const int first = si * p.seg, chunks = min((len + kL - 1) / kL, si + 1 == p.nseg ? p.chunks : first + p.seg);
 
     Rows vr = p.v;
     vr.width = vw;
     const T* qb = OUT ? static_cast<const T*>(p.q.p) + b * p.q.b + (h / p.q.per) * p.q.h : nullptr;
     const T* kb_ = static_cast<const T*>(p.k.p) + b * p.k.b + (h / p.k.per) * p.k.h;
     const T* vb = static_cast<const T*>(p.v.p) + b * p.v.b + h * p.v.h + c0;
-    const int64_t one = static_cast<int64_t>(p.kd) * p.vd;
-    const StateAt<KT> place(c0 + n0 + i16, qd, p.kd, p.vd);
+    const int64_t one = static_cast<int64_t>(p.kd) * vd;
+    const StateAt<KT> place(c0 + n0 + i16, qd, p.kd, vd);
 
     Stage<T, KD, 256> sq, sk;
     Stage<T, 64, 256> sv;
@@ -451,33 +472,50 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
         const int left = len - c * kL;
         char* at = tiles(buf);
         sk.fill(p.k, kb_ + t0 * p.k.t, left, reinterpret_cast<T*>(at), wave, tid);
-        sv.fill(vr, vb + t0 * p.v.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
+        if (!unit) sv.fill(vr, vb + t0 * p.v.t, left, reinterpret_cast<T*>(at + kTile), wave, tid);
         if (OUT) sq.fill(p.q, qb + t0 * p.q.t, left, reinterpret_cast<T*>(at + kTile + kTileV), wave, tid);
-        const char* rec = p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<!OUT>;
-        record_fill<T, OUT ? 2 : 1, false>(rec, rec + kRecBytes<!OUT> - kFacBytes, at + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
+        const char* rec = p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * p.rec_bytes;
+        record_fill<T, OUT ? 2 : 1, false>(rec, rec + p.rec_bytes - kFacBytes, at + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
     };
     if (!kAhead || loads) {
         if (OUT) sq.init(p.q, tid);
         sk.init(p.k, tid);
         sv.init(vr, tid);
-        for (int n = 0; n < (kAhead ? 2 : 1); ++n) record_zero<T, OUT ? 2 : 1, false>(tiles(n) + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
-        if (chunks > 0) fill(0, 0);
+        for (int n = 0; n < (kAhead ? 2 : 1); ++n) {
+            record_zero<T, OUT ? 2 : 1, false>(tiles(n) + (OUT ? 2 : 1) * kTile + kTileV, wave, lane);
+            if (unit) {   // no values
+                for (int e = tid; e < kTileV / 16; e += 256) *reinterpret_cast<u32x4*>(tiles(n) + kTile + 16 * e) = u32x4{0, 0, 0, 0};
+            }
+        }
+        if (chunks > first) fill(first, 0);
     }
     if (kAhead && loads) {
-        for (int c = 0; c < chunks; ++c) {
+        for (int c = first; c < chunks; ++c) {
             tile_barrier();   // the chunk's tiles are complete, and the other buffer's are free
-            if (c + 1 < chunks) fill(c + 1, __builtin_amdgcn_readfirstlane((c + 1) & 1));
+            if (c + 1 < chunks) fill(c + 1, __builtin_amdgcn_readfirstlane((c + 1 - first) & 1));
         }
         return;
     }
     f32x4 S[KT];
 #pragma unroll
     for (int d = 0; d < KT; ++d) S[d] = f32x4{0, 0, 0, 0};
-    if (p.start != nullptr) place.read(p.start + bh * one, S);
+    if constexpr (SEG) {
+        if (unit) {
+#pragma unroll
+            for (int d = 0; d < KT; ++d) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) S[d][r] = 32 * (d >> 1) + 8 * qd + 4 * (d & 1) + r == c0 + n0 + i16 ? 1.0f : 0.0f;
+            }
+        }
+    } else if (p.from != nullptr) {
+        place.read(p.from + (static_cast<int64_t>(bh) * p.nseg + si) * one, S);
+    } else if (p.start != nullptr) {
+        place.read(p.start + bh * one, S);
+    }
 
 
-    for (int c = 0; c < chunks; ++c) {
-        const int buf = kAhead ? __builtin_amdgcn_readfirstlane(c & 1) : 0, t0 = c * kL, left = len - t0;
+    for (int c = first; c < chunks; ++c) {
+        const int buf = kAhead ? __builtin_amdgcn_readfirstlane((c - first) & 1) : 0, t0 = c * kL, left = len - t0;
         char* const at = tiles(buf);
         T* const kt = reinterpret_cast<T*>(at);
         T* const vt = reinterpret_cast<T*>(at + kTile);
@@ -487,7 +525,7 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
         const Factors& fac = *reinterpret_cast<const Factors*>(nf + (OUT ? 2 : 1) * kFragBytes<T>);
         if (kAhead) lds_barrier();
         else tile_barrier();
-        if (!OUT) place.write(p.states + (static_cast<int64_t>(bh) * p.chunks + c) * one, S);
+        if (!OUT && !SEG) place.write(p.states + (static_cast<int64_t>(bh) * p.chunks + c) * one, S);
 
         // S^T k and S^T q
         f32x4 Y[4], O[4];   // Y, tile it: tokens 16 it + 4 quarter + r down, column n0 + lane % 16; O: transposed
@@ -582,7 +620,7 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
                 }
                 o += lane_xor_f<16>(o);
                 o += lane_xor_f<32>(o);
-                if (qd == 0 && col < p.vd) {
+                if (!SEG && qd == 0 && col < p.vd) {
                     if (OUT) static_cast<T*>(p.out)[b * p.o_b + h * p.o_h + static_cast<int64_t>(t0 + t) * p.o_t + col] = narrow<T>(p.scale * o);
                     else p.miss[(static_cast<int64_t>(bh) * p.T + t0 + t) * p.vd + col] = r;
                 }
@@ -635,7 +673,7 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
                     if (16 * it + i16 >= left || n >= p.vd) continue;
                     store_four<T>(p.out, b * p.o_b + h * p.o_h + static_cast<int64_t>(t0 + 16 * it + i16) * p.o_t + n, O[it], p.vd - n, p.out_wide);
                 }
-            } else {
+            } else if constexpr (!SEG) {
                 float* miss = p.miss + (static_cast<int64_t>(bh) * p.T + t0) * p.vd + c0 + n0 + i16;
 #pragma unroll
                 for (int it = 0; it < 4; ++it) {
@@ -653,13 +691,127 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ke
         }
     }
     if constexpr (OUT) {
-        // Tokens past the row's length.
-        for (int64_t e = tid; e < static_cast<int64_t>(p.T - len) * vw; e += 256) {
-            const int t = len + static_cast<int>(e / vw), col = c0 + static_cast<int>(e % vw);
+        // The segment's tokens past the row's length.
+        const int from = max(len, first * kL), to = si + 1 == p.nseg ? p.T : min(p.T, (first + p.seg) * kL);
+        for (int64_t e = tid; e < static_cast<int64_t>(to - from) * vw; e += 256) {
+            const int t = from + static_cast<int>(e / vw), col = c0 + static_cast<int>(e % vw);
             static_cast<T*>(p.out)[b * p.o_b + t * p.o_t + h * p.o_h + col] = narrow<T>(0.0f);
         }
     }
-    if (p.last != nullptr) place.write(p.last + bh * one, S);
+    if constexpr (SEG) place.write((unit ? p.move : p.own) + (static_cast<int64_t>(bh) * p.nseg + si) * one, S);
+    else if (p.last != nullptr && si + 1 == p.nseg) place.write(p.last + bh * one, S);
+}
+
+// The states before every segment (REV: the gradients behind every one) from the segments' own and their transitions,
+//     S_{n+1} = M_n S_n + own_n    (REV: R_{n-1} = M_n^T R_n + own_n),
+// one block per 16 columns of a (stream, head)'s state: each wave 16 rows, the columns in LDS between the steps, the next step's
+// matrices in flight. Both factors in three bfloat16 parts, whatever the inputs. A segment whose transition is 0 (a reset) leaves
+// nothing of what was before, finite or not.
+struct ChainArgs {
+    const float *move, *own;   // [B H, nseg]
+    const float* start;        // [B H] (NULL: zero)
+    float* to;                 // [B H, nseg]
+    int nseg, kd, vd, cols;    // cols: blocks of 16 columns
+};
+
+template <int KD, bool REV>
+__global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
+    constexpr int KB = KD / 32, kPad = KD + 4;
+    __shared__ __align__(16) float cols[2][16 * kPad];   // [column][row]
+    const int bh = static_cast<int>(blockIdx.x) / p.cols, cb = static_cast<int>(blockIdx.x) - bh * p.cols;
+    const int lane = static_cast<int>(lane_id()), wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    const int i16 = lane & 15, qd = lane >> 4, col = 16 * cb + i16, row = 16 * wave + i16, out = 16 * wave + 4 * qd;
+    const int64_t one = static_cast<int64_t>(p.kd) * p.vd, sq = static_cast<int64_t>(p.kd) * p.kd;
+    // Byte offsets of the lane's elements (row, 32 kb + 8 quarter + ..) of a transition, and of its part of a state; past any range
+    // where there are none. Every step's loads go by them.
+    uint32_t moff[KB], ooff[4];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+        const int j = 32 * kb + 8 * qd;
+        moff[kb] = row < p.kd && j < p.kd ? 4u * static_cast<uint32_t>(REV ? j * p.kd + row : row * p.kd + j) : 0xC0000000u;
+        __asm__ volatile("" : "+v"(moff[kb]));
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        ooff[r] = out + r < p.kd && col < p.vd ? 4u * static_cast<uint32_t>((out + r) * p.vd + col) : 0xC0000000u;
+        __asm__ volatile("" : "+v"(ooff[r]));
+    }
+    const bool four = !REV && p.kd % 4 == 0;
+    float m[KB][8];
+    f32x4 own;
+    auto part = [&](const float* from, f32x4& x) {
+        const auto b = uniform_buffer(from, static_cast<int>(one) * 4);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) x[r] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(ooff[r]), 0, 0));
+    };
+    auto load = [&](int n) {
+        const auto b = uniform_buffer(p.move + (static_cast<int64_t>(bh) * p.nseg + n) * sq, static_cast<int>(sq) * 4);
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            if (four) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const f32x4 w = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, static_cast<int>(moff[kb] + 16u * h), 0, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m[kb][4 * h + e] = w[e];
+                }
+            } else {
+                const uint32_t step = REV ? 4u * static_cast<uint32_t>(p.kd) : 4u;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) m[kb][e] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, static_cast<int>(moff[kb] + step * e), 0, 0));
+            }
+        }
+        part(p.own + (static_cast<int64_t>(bh) * p.nseg + n) * one, own);
+    };
+    auto keep = [&](int n, f32x4 s, float* at) {
+        float* to = p.to + (static_cast<int64_t>(bh) * p.nseg + n) * one;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (out + r < p.kd && col < p.vd) to[(out + r) * p.vd + col] = s[r];
+        }
+        *reinterpret_cast<f32x4*>(at + i16 * kPad + out) = s;
+    };
+    const int n0 = REV ? p.nseg - 1 : 0, n1 = REV ? 0 : p.nseg - 1, step = REV ? -1 : 1;
+    f32x4 s = {0, 0, 0, 0};
+    if (p.start != nullptr) {
+        part(p.start + bh * one, s);
+    }
+    keep(n0, s, cols[0]);
+    load(n0);
+    int buf = 0;
+    for (int n = n0; n != n1; n += step, buf ^= 1) {
+        Parts<bf16_t, 3> mp[KB];
+        bool some = false;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (32 * kb + 8 * qd + e >= p.kd) m[kb][e] = 0.0f;   // the next row's
+                some |= m[kb][e] != 0.0f;
+            }
+            split(m[kb], mp[kb]);
+        }
+        f32x4 x = {0, 0, 0, 0}, part_[KB];
+        const f32x4 add = own;
+        if (n + step != n1) load(n + step);
+        __syncthreads();   // the columns are complete
+        if (__ballot(some) != 0) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) {
+                const float* at = cols[buf] + i16 * kPad + 32 * kb + 8 * qd;
+                const f32x4 a = *reinterpret_cast<const f32x4*>(at), b = *reinterpret_cast<const f32x4*>(at + 4);
+                const float y[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                Parts<bf16_t, 3> yp;
+                split(y, yp);
+                part_[kb] = f32x4{0, 0, 0, 0};
+                mma_parts(mp[kb], yp, part_[kb]);
+            }
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) x += part_[kb];
+        }
+        x += add;
+        keep(n + step, x, cols[buf ^ 1]);
+    }
 }
 
 // ------------------------------------------------------------------------------------------ backward
@@ -685,9 +837,13 @@ struct BackArgs {
     float* first;             // [B H] gradients of the first states (NULL: not kept)
     float* grads;             // [B H, chunks] the gradients of the states behind every chunk
     float* du;                // [B H, T, vd]
+    // Segments as in MainArgs. from: the gradients behind every segment; own: the segments pass's, from nothing (all but the first's).
+    int nseg, seg;
+    const float* from;
+    float* own;
 };
 
-template <typename T, int KD>
+template <typename T, int KD, bool SEG>
 __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_back_kernel(BackArgs p) {
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
     constexpr bool kAhead = sizeof(T) == 2;
@@ -696,13 +852,15 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
     extern __shared__ __align__(16) char lds[];
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    const int bh = blk / p.cols, cb = blk - bh * p.cols, b = bh / p.H, h = bh - b * p.H;
+    const int bs = blk / p.cols, cb = blk - bs * p.cols, nseg = SEG ? p.nseg - 1 : p.nseg;
+    const int bh = bs / nseg, si = bs - bh * nseg + (SEG ? 1 : 0), b = bh / p.H, h = bh - b * p.H;
     const bool loads = threadIdx.x >= 256;   // the waves that load ahead
     const int tid = static_cast<int>(threadIdx.x) & 255, lane = static_cast<int>(lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
     const int c0 = 64 * cb, n0 = 16 * wave, vw = min(64, p.vd - c0);
-    const int len = __builtin_amdgcn_readfirstlane(live_tokens(p.lens, b, p.T)), chunks = (len + kL - 1) / kL;
+    const int len = __builtin_amdgcn_readfirstlane(live_tokens(p.lens, b, p.T));
+    const int first = si * p.seg, chunks = min((len + kL - 1) / kL, si + 1 == p.nseg ? p.chunks : first + p.seg);
 
     Rows dr = p.d;
     dr.width = vw;
@@ -729,23 +887,26 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
         sk.init(p.k, tid);
         sd.init(dr, tid);
         for (int n = 0; n < (kAhead ? 2 : 1); ++n) record_zero<T, 2, true>(lds + n * kBuf + 2 * kTile + kTileV, wave, lane);
-        if (chunks > 0) fill(chunks - 1, 0);
+        if (chunks > first) fill(chunks - 1, 0);
     }
     if (kAhead && loads) {
-        for (int cc = 0; cc < chunks; ++cc) {
+        for (int c = chunks - 1; c >= first; --c) {
             tile_barrier();
-            if (cc + 1 < chunks) fill(chunks - 2 - cc, __builtin_amdgcn_readfirstlane((cc + 1) & 1));
+            if (c > first) fill(c - 1, __builtin_amdgcn_readfirstlane((chunks - c) & 1));
         }
         return;
     }
     f32x4 R[KT];
 #pragma unroll
     for (int d = 0; d < KT; ++d) R[d] = f32x4{0, 0, 0, 0};
-    if (p.start != nullptr) place.read(p.start + bh * one, R);
+    if constexpr (!SEG) {
+        if (p.from != nullptr) place.read(p.from + (static_cast<int64_t>(bh) * p.nseg + si) * one, R);
+        else if (p.start != nullptr) place.read(p.start + bh * one, R);
+    }
 
 
-    for (int cc = 0; cc < chunks; ++cc) {
-        const int c = chunks - 1 - cc, buf = kAhead ? __builtin_amdgcn_readfirstlane(cc & 1) : 0, t0 = c * kL, left = len - t0;
+    for (int c = chunks - 1; c >= first; --c) {
+        const int buf = kAhead ? __builtin_amdgcn_readfirstlane((chunks - 1 - c) & 1) : 0, t0 = c * kL, left = len - t0;
         char* const at = lds + buf * kBuf;
         T* const kt = reinterpret_cast<T*>(at);
         T* const dt = reinterpret_cast<T*>(at + kTile);
@@ -755,7 +916,7 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
         const Factors& fac = *reinterpret_cast<const Factors*>(nf + 2 * kFragBytes<T>);
         if (kAhead) lds_barrier();
         else tile_barrier();
-        place.write(p.grads + (static_cast<int64_t>(bh) * p.chunks + c) * one, R);
+        if (!SEG) place.write(p.grads + (static_cast<int64_t>(bh) * p.chunks + c) * one, R);
 
         f32x4 Z[4];   // tile it: tokens 16 it + 4 quarter + r down, column n0 + lane % 16
 #pragma unroll
@@ -843,7 +1004,7 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
                         R[2 * kb + (n >> 2)][n & 3] = sdm_decayed(a, s);
                     }
                 }
-                if (qd == 0 && n0 + i16 < vw) p.du[(static_cast<int64_t>(bh) * p.T + t0 + t) * p.vd + c0 + n0 + i16] = sum;
+                if (!SEG && qd == 0 && n0 + i16 < vw) p.du[(static_cast<int64_t>(bh) * p.T + t0 + t) * p.vd + c0 + n0 + i16] = sum;
             }
         } else {
             const float all = fac.f[kL - 1];
@@ -889,16 +1050,17 @@ __global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_ba
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const int t = 16 * it + 4 * qd + r;
-                    if (t < left && n0 + i16 < vw) du[static_cast<int64_t>(t) * p.vd] = Z[it][r];
+                    if (!SEG && t < left && n0 + i16 < vw) du[static_cast<int64_t>(t) * p.vd] = Z[it][r];
                 }
             }
         }
         if (!kAhead) {
             lds_barrier();
-            if (c > 0) fill(c - 1, 0);
+            if (c > first) fill(c - 1, 0);
         }
     }
-    if (p.first != nullptr) place.write(p.first + bh * one, R);
+    if constexpr (SEG) place.write(p.own + (static_cast<int64_t>(bh) * p.nseg + si) * one, R);
+    else if (p.first != nullptr && si == 0) place.write(p.first + bh * one, R);
 }
 
 // What is local to a chunk: a block per chunk, 16 key columns for each of its waves.
@@ -1555,9 +1717,34 @@ size_t main_lds(bool out) {
 
 int chunks_of(int T) { return (T + kL - 1) / kL; }
 
+// Segments of the time axis. A block's way along it is most of the time where there are few blocks, so the axis is cut: a pass
+// makes every segment's own state and transition (as many columns again as the state has rows), a kernel chains them, and the main
+// pass runs on all segments at once. Rounds of blocks over the compute units times a segment's chunks, in units of a chunk (3.5 us,
+// 3 without outputs; a step of the chain is 1.5), say whether and how finely: 1 x 16384 tokens x 8 heads of 128, forward, 925 us whole
+// and 265 in 16 segments; 8 x 4096 x 16 stays whole.
+constexpr int kUnits = 256;
+struct SegPlan {
+    int nseg, seg;
+};
+SegPlan seg_plan(const sdm_gdr_io* io) {
+    const int64_t bh = static_cast<int64_t>(io->B) * io->H, chunks = chunks_of(io->T), cols = (io->dv + 63) / 64, kcols = (io->dk + 63) / 64;
+    auto rounds = [](int64_t blocks) { return static_cast<double>((blocks + kUnits - 1) / kUnits); };
+    SegPlan best{1, static_cast<int>(chunks > 0 ? chunks : 1)};
+    double cost = rounds(bh * cols) * chunks * 3.5;
+    for (int64_t per = (chunks + 1) / 2; per >= 2; per = per > 16 ? per * 3 / 4 : per - 1) {
+        const int64_t n = (chunks + per - 1) / per;
+        const double c = rounds(n * bh * (cols + kcols)) * per * 3.0 + 1.5 * n + 10.0 + rounds(n * bh * cols) * per * 3.5;
+        if (c < cost) {
+            cost = c;
+            best = SegPlan{static_cast<int>(n), static_cast<int>(per)};
+        }
+    }
+    return best;
+}
+
 // Byte offsets in the workspace.
 struct GdrLayout {
-    size_t rec, states, grads, miss, du, fq, fk, total;
+    size_t rec, move, own, from, rown, rfrom, states, grads, miss, du, fq, fk, total;
 };
 GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
     const size_t bh = static_cast<size_t>(io->B) * io->H, n = bh * chunks_of(io->T), rows = bh * io->T;
@@ -1568,6 +1755,17 @@ GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
         at += up256(bytes);
         return o;
     };
+    const SegPlan sp = seg_plan(io);
+    if (sp.nseg > 1) {
+        const size_t states = bh * sp.nseg * io->dk * io->dv * 4;
+        l.move = take(bh * sp.nseg * io->dk * io->dk * 4);
+        l.own = take(states);
+        l.from = take(states);
+        if (backward) {
+            l.rown = take(states);
+            l.rfrom = take(states);
+        }
+    }
     if (backward) {
         l.rec = take(n * kRecBytes<true>);
         l.states = take(n * io->dk * io->dv * 4);
@@ -1596,23 +1794,29 @@ hipError_t chunk_go(const sdm_gdr_io* io, char* rec, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename T, bool OUT>
+template <typename T, bool OUT, bool SEG>
 hipError_t main_go(const sdm_gdr_io* io, const MainArgs& a, hipStream_t st) {
-    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(io->B) * io->H * a.cols);
-    if (padded(io->dk) == 64) gdr_kernel<T, 64, OUT><<<grid, kMainThreads<T>, main_lds<T, 64>(OUT), st>>>(a);
-    else gdr_kernel<T, 128, OUT><<<grid, kMainThreads<T>, main_lds<T, 128>(OUT), st>>>(a);
+    const int64_t blocks = SEG ? static_cast<int64_t>(a.made) * (a.cols + (a.kd + 63) / 64) : static_cast<int64_t>(a.nseg) * a.cols;
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(io->B) * io->H * blocks);
+    if (padded(io->dk) == 64) gdr_kernel<T, 64, OUT, SEG><<<grid, kMainThreads<T>, main_lds<T, 64>(OUT), st>>>(a);
+    else gdr_kernel<T, 128, OUT, SEG><<<grid, kMainThreads<T>, main_lds<T, 128>(OUT), st>>>(a);
     return hipGetLastError();
 }
 
-template <typename T>
-hipError_t forward(const sdm_gdr_io* io, hipStream_t st) {
+template <bool REV>
+hipError_t chain_go(const sdm_gdr_io* io, const ChainArgs& a, hipStream_t st) {
+    const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(io->B) * io->H * a.cols);
+    if (padded(io->dk) == 64) gdr_chain_kernel<64, REV><<<grid, 256, 0, st>>>(a);
+    else gdr_chain_kernel<128, REV><<<grid, 512, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+// The call without outputs, and the states before its segments (`made` of whose transitions are needed), if it has some.
+template <typename T, bool BACK>
+hipError_t begin(const sdm_gdr_io* io, const GdrLayout& l, MainArgs& a, hipStream_t st) {
     const int per = io->H / io->Hk, es = sizeof(T);
-    char* rec = static_cast<char*>(io->workspace) + gdr_layout(io, false).rec;
-    if (io->T > 0) {
-        const hipError_t e = chunk_go<T, false>(io, rec, st);
-        if (e != hipSuccess) return e;
-    }
-    MainArgs a{};
+    char* ws = static_cast<char*>(io->workspace);
+    const SegPlan sp = seg_plan(io);
     a.q = rows_of(io->q, io->q_b, io->q_t, io->q_h, io->dk, per, es);
     a.k = rows_of(io->k, io->k_b, io->k_t, io->k_h, io->dk, per, es);
     a.v = rows_of(io->v, io->v_b, io->v_t, io->v_h, io->dv, 1, es);
@@ -1624,15 +1828,37 @@ hipError_t forward(const sdm_gdr_io* io, hipStream_t st) {
     a.kd = io->dk;
     a.vd = io->dv;
     a.scale = io->scale;
-    a.rec = rec;
+    a.rec = ws + l.rec;
+    a.rec_bytes = kRecBytes<BACK>;
     a.start = io->state;
+    a.nseg = sp.nseg;
+    a.seg = sp.seg;
+    if (io->T == 0) return hipSuccess;
+    hipError_t e = chunk_go<T, BACK>(io, ws + l.rec, st);
+    if (e != hipSuccess || sp.nseg == 1) return e;
+    a.made = BACK ? sp.nseg : sp.nseg - 1;   // what leaves the last one only the backward pass goes through
+    a.own = reinterpret_cast<float*>(ws + l.own);
+    a.move = reinterpret_cast<float*>(ws + l.move);
+    a.from = nullptr;
+    if ((e = main_go<T, false, true>(io, a, st)) != hipSuccess) return e;
+    float* from = reinterpret_cast<float*>(ws + l.from);
+    a.from = from;
+    return chain_go<false>(io, ChainArgs{a.move, a.own, a.start, from, sp.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st);
+}
+
+template <typename T>
+hipError_t forward(const sdm_gdr_io* io, hipStream_t st) {
+    const int es = sizeof(T);
+    MainArgs a{};
+    const hipError_t e = begin<T, false>(io, gdr_layout(io, false), a, st);
+    if (e != hipSuccess) return e;
     a.last = io->last;
     a.out = io->o;
     a.o_b = io->o_b;
     a.o_t = io->o_t;
     a.o_h = io->o_h;
     a.out_wide = reinterpret_cast<uintptr_t>(io->o) % (4 * es) == 0 && io->o_b % 4 == 0 && io->o_t % 4 == 0 && io->o_h % 4 == 0 && io->dv % 4 == 0;
-    return main_go<T, true>(io, a, st);
+    return main_go<T, true, false>(io, a, st);
 }
 
 template <typename T, int KD, bool FOLD>
@@ -1657,29 +1883,24 @@ hipError_t backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st)
     const int64_t bh = static_cast<int64_t>(io->B) * io->H;
     hipError_t e = hipSuccess;
     MainArgs m{};
-    m.k = k;
-    m.v = v;
-    m.lens = io->lens;
-    m.T = io->T;
-    m.H = io->H;
-    m.chunks = chunks;
-    m.cols = cols;
-    m.kd = io->dk;
-    m.vd = io->dv;
-    m.scale = io->scale;
-    m.rec = ws + l.rec;
-    m.start = io->state;
+    if ((e = begin<T, true>(io, l, m, st)) != hipSuccess) return e;
     m.states = reinterpret_cast<float*>(ws + l.states);
     m.miss = reinterpret_cast<float*>(ws + l.miss);
-    if (io->T > 0) {
-        if ((e = chunk_go<T, true>(io, ws + l.rec, st)) != hipSuccess) return e;
-        if ((e = main_go<T, false>(io, m, st)) != hipSuccess) return e;
+    if (io->T > 0 && (e = main_go<T, false, false>(io, m, st)) != hipSuccess) return e;
+    BackArgs b{q, k, d, io->lens, io->T, io->H, chunks, cols, io->dk, io->dv, io->scale, ws + l.rec, g->d_last, g->d_state,
+               reinterpret_cast<float*>(ws + l.grads), reinterpret_cast<float*>(ws + l.du), m.nseg, m.seg, nullptr, reinterpret_cast<float*>(ws + l.rown)};
+    if (m.nseg > 1) {
+        const unsigned grid = static_cast<unsigned>(bh * cols * (m.nseg - 1));
+        if (padded(io->dk) == 64) gdr_back_kernel<T, 64, true><<<grid, kMainThreads<T>, main_lds<T, 64>(true), st>>>(b);
+        else gdr_back_kernel<T, 128, true><<<grid, kMainThreads<T>, main_lds<T, 128>(true), st>>>(b);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        float* from = reinterpret_cast<float*>(ws + l.rfrom);
+        if ((e = chain_go<true>(io, ChainArgs{m.move, b.own, g->d_last, from, m.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st)) != hipSuccess) return e;
+        b.from = from;
     }
-    const BackArgs b{q, k, d, io->lens, io->T, io->H, chunks, cols, io->dk, io->dv, io->scale, ws + l.rec, g->d_last, g->d_state,
-                     reinterpret_cast<float*>(ws + l.grads), reinterpret_cast<float*>(ws + l.du)};
-    const unsigned grid = static_cast<unsigned>(bh * cols);
-    if (padded(io->dk) == 64) gdr_back_kernel<T, 64><<<grid, kMainThreads<T>, main_lds<T, 64>(true), st>>>(b);
-    else gdr_back_kernel<T, 128><<<grid, kMainThreads<T>, main_lds<T, 128>(true), st>>>(b);
+    const unsigned grid = static_cast<unsigned>(bh * cols * m.nseg);
+    if (padded(io->dk) == 64) gdr_back_kernel<T, 64, false><<<grid, kMainThreads<T>, main_lds<T, 64>(true), st>>>(b);
+    else gdr_back_kernel<T, 128, false><<<grid, kMainThreads<T>, main_lds<T, 128>(true), st>>>(b);
     if ((e = hipGetLastError()) != hipSuccess || io->T == 0) return e;
     const bool fold = per > 1;
     GradArgs a{q, k, v, d, io->g, io->beta, io->g_b, io->g_t, io->g_h, io->e_b, io->e_t, io->e_h, io->lens, io->T, io->H, chunks, io->dk, io->dv,
@@ -1702,20 +1923,21 @@ void list_grad(const void** all, int& n) {
     all[n++] = reinterpret_cast<const void*>(&gdr_grad_kernel<T, KD, 128, false>);
     all[n++] = reinterpret_cast<const void*>(&gdr_grad_kernel<T, KD, 128, true>);
 }
+template <typename T, int KD>
+void list_width(const void** all, int& n) {
+    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, KD, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, KD, true>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, KD, true, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, KD, false, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, KD, false, true>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_back_kernel<T, KD, false>);
+    all[n++] = reinterpret_cast<const void*>(&gdr_back_kernel<T, KD, true>);
+    list_grad<T, KD>(all, n);
+}
 template <typename T>
 void list(const void** all, int& n) {
-    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 64, true>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 128, true>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 64, false>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 128, false>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_back_kernel<T, 64>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_back_kernel<T, 128>);
-    list_grad<T, 64>(all, n);
-    list_grad<T, 128>(all, n);
-    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 64, false>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_chunk_kernel<T, 128, false>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 64, true>);
-    all[n++] = reinterpret_cast<const void*>(&gdr_kernel<T, 128, true>);
+    list_width<T, 64>(all, n);
+    list_width<T, 128>(all, n);
 }
 
 }  // namespace

@@ -182,3 +182,19 @@ def test_resets_and_strong_gates(dtype):
     assert not (r["dg"][0, 1:70] == 0).any() and not (r["dbeta"][0, 100:130] == 0).any()
     x["state"] = x["d_last"] = None
     assert (backward(x, dtype, 0.3)["dg"][0, 0] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,dk,dv,lens", [(700, 1, 48, 40, None), (1090, 2, 128, 128, None), (1600, 1, 100, 33, None), (900, 1, 64, 128, [900, 130, 0, 515])])
+def test_rows_cut_into_segments(dtype, T, H, dk, dv, lens):
+    say("gdr segments", dtype, T, H, dk, dv, lens)
+    B = 1 if lens is None else len(lens)
+    few, many = (sdm.gdr_workspace_bytes(n, T, H, 1, dk, dv, DT[dtype]) for n in (1, 1000))
+    assert few > many // 1000 + 4 * dk * dk   # the segments' transitions and states
+    x = make(B, T, H, 1, dk, dv, dtype, gate=5.0, lens=lens)
+    forward(x, dtype, 0.2)
+    backward(x, dtype, 0.2)
+    x = make(B, T, H, 1, dk, dv, dtype, gate=2.0, state=False, seed=5, lens=lens)
+    x["g"][0, 300] = x["g"][0, 511] = -INF
+    forward(x, dtype, 0.2)
+    backward(x, dtype, 0.2)
