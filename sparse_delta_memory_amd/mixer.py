@@ -12,13 +12,16 @@ One projection of the token rows x [P, T, model] gives everything:
 and the layer's output is the dense heads' outputs and the bank's reads, side by side. Streams are rows of
 the batch; the bank is worked through in chunks of C tokens (phase1 of all chunks at once, then read side and
 DW step by step), so prompts are whole chunks here. A single token of every stream is a chunk of one.
+
+DeltaBlock is a block of delta-rule heads with its norms, gate and residual, forward, for single tokens and backward.
 """
 
 from __future__ import annotations
 
 import torch
 
-from . import alloc_dw_workspace, dw_step, glr_forward, glr_step, make_shape, norm_rope, phase1, read_step, rope_table, slot_topk
+from . import (alloc_dw_workspace, dw_step, gate_norm, gate_norm_backward, gdr_backward, gdr_forward, gdr_step, glr_forward, glr_step, make_shape,
+               norm_rope, norm_rope_backward, phase1, read_step, residual_norm, residual_norm_backward, rope_table, slot_topk)
 
 
 class Mixer:
@@ -114,6 +117,87 @@ class Mixer:
         return torch.cat([o.flatten(1).float(), self.sparse(bank, P, 1, 1, *sparse)], 1)
 
 
+class DeltaBlock:
+    """A block of delta-rule heads as a stack of layers has it: from a residual x and its norm n, both [P, T, model],
+
+        n -> projection -> norm_rope (keys and queries of norm 1) -> gdr_forward / gdr_step -> gate_norm -> projection -> y
+        x, n = residual_norm(x, y)                       for the next block
+
+    with its backward pass. The output's norm weights and the residual's scale are parameters beside the two projections."""
+
+    def __init__(self, model=256, heads=4, key_heads=2, d=64, rot=32, positions=4096, norm_y=True, seed=0, device="cuda", dtype=torch.bfloat16):
+        gen = torch.Generator(device=device).manual_seed(seed)
+        rnd = lambda a, b: (torch.randn((a, b), generator=gen, device=device) * a ** -0.5).to(dtype)  # noqa: E731
+        self.heads, self.key_heads, self.d, self.norm_y = heads, key_heads, d, norm_y
+        # q, k, v, the output's gates z; then the state's gate and beta of every head. Every part starts on 16 bytes.
+        self.split = [key_heads * d, key_heads * d, heads * d, heads * d, 2 * heads]
+        unit = 16 // dtype.itemsize
+        self.padded = [-(-c // unit) * unit for c in self.split]
+        self.w = torch.cat([torch.nn.functional.pad(rnd(model, c), (0, wide - c)) for c, wide in zip(self.split, self.padded)], 1)
+        self.w_out = rnd(heads * d, model)
+        ones = lambda n: torch.ones(n, device=device)  # noqa: E731
+        self.unit, self.o_norm, self.y_norm, self.scale, self.next_norm = ones(d) * d ** -0.5, ones(d), ones(model) if norm_y else None, ones(model) * 0.5, ones(model)
+        self.table = rope_table(positions, rot, device=device)
+
+    def residual(self, x, y):
+        return residual_norm(x, y, self.next_norm, scale=self.scale, norm_y=self.norm_y, y_weight=self.y_norm)
+
+    def rows(self, n, pos):
+        """What the rule takes of the normed rows n [N, model]: raw and normed q and k, v, z [N, heads, d], and the gates' rows."""
+        if pos.numel() != n.shape[0]:
+            raise ValueError("DeltaBlock: %d positions for %d rows" % (pos.numel(), n.shape[0]))
+        q, k, v, z, g = (t[:, :c] for t, c in zip((n @ self.w).split(self.padded, 1), self.split))
+        q, k, v, z = (t.view(n.shape[0], -1, self.d) for t in (q, k, v, z))
+        return q, k, *norm_rope(q, k, self.unit, self.unit, pos, self.table, eps=1e-12), v, z, g.float()
+
+    def gates(self, g):
+        return torch.nn.functional.logsigmoid(g[:, :self.heads] + 3), g[:, self.heads:].sigmoid()
+
+    def prompt(self, x, n, state=None, start=0):
+        """(x, n) of the next block [P, T, model], the state [P, heads, d, d] and what backward needs."""
+        P, T = n.shape[:2]
+        if start < 0 or start + T > self.table.shape[0]:
+            raise ValueError("DeltaBlock.prompt: positions %d .. %d of a table of %d" % (start, start + T - 1, self.table.shape[0]))
+        pos = torch.arange(start, start + T, dtype=torch.int32, device=n.device).repeat(P)
+        q0, k0, q, k, v, z, g = self.rows(n.flatten(0, 1), pos)
+        gate, beta = self.gates(g)
+        seq = lambda t: t.unflatten(0, (P, T))  # noqa: E731
+        ins = [seq(t) for t in (q, k, v, gate, beta)]
+        o, last = gdr_forward(*ins, state=state)
+        o = o.flatten(0, 1)
+        y = (gate_norm(o, z, self.o_norm).flatten(1) @ self.w_out).view_as(x)
+        h, m = self.residual(x, y)
+        return h, m, last, (n, pos, q0, k0, ins, z, g, o, y, h, state)
+
+    def token(self, x, n, state, pos):
+        """One token of every stream: x, n [P, model]; the state is updated in place."""
+        if pos < 0 or pos >= self.table.shape[0]:
+            raise ValueError("DeltaBlock.token: position %d of a table of %d" % (pos, self.table.shape[0]))
+        _, _, q, k, v, z, g = self.rows(n, torch.full((n.shape[0],), pos, dtype=torch.int32, device=n.device))
+        o = gdr_step(q, k, v, *self.gates(g), state)
+        return self.residual(x, gate_norm(o, z, self.o_norm).flatten(1) @ self.w_out)
+
+    def backward(self, d_x, d_n, saved):
+        """Gradients from those of prompt's x and n: a dict of x, n, state and every parameter."""
+        n, pos, q0, k0, ins, z, g, o, y, h, state = saved
+        r = residual_norm_backward(d_x, d_n, h, y, self.next_norm, scale=self.scale, norm_y=self.norm_y, y_weight=self.y_norm)
+        dy = r["dy"].flatten(0, 1)
+        out = dict(x=r["dx"], next_norm=r["dw"], scale=r["dscale"], y_norm=r["dwy"])
+        gated = gate_norm(o, z, self.o_norm).flatten(1)
+        out["w_out"] = gated.t() @ dy
+        e = gate_norm_backward((dy @ self.w_out.t()).view_as(o), o, z, self.o_norm)
+        out["o_norm"] = e["dw"]
+        s = gdr_backward(e["dx"].unflatten(0, n.shape[:2]), *ins, state=state)
+        out["state"] = s["dstate"]
+        f = norm_rope_backward(s["dq"].flatten(0, 1), s["dk"].flatten(0, 1), q0, k0, self.unit, self.unit, pos, self.table, eps=1e-12)
+        beta = ins[4].flatten(0, 1)
+        dg = torch.cat([s["dg"].flatten(0, 1) * (-g[:, :self.heads] - 3).sigmoid(), s["dbeta"].flatten(0, 1) * beta * (1 - beta)], 1).to(n.dtype)
+        parts = [t.flatten(1) for t in (f["dq"], f["dk"], s["dv"].flatten(0, 1), e["dz"], dg)]
+        rows = torch.cat([torch.nn.functional.pad(t, (0, wide - t.shape[1])) for t, wide in zip(parts, self.padded)], 1)
+        out["w"], out["n"] = n.flatten(0, 1).t() @ rows, (rows @ self.w.t()).view_as(n)
+        return out
+
+
 def main():
     m = Mixer()
     P, T, more = 2, 4 * m.C, 8
@@ -125,6 +209,14 @@ def main():
         y = m.token(x[:, t], bank, state, t)
     print("%d more tokens: outputs %s, rms %.3f, %d slots written" % (more, tuple(y.shape), y.square().mean().sqrt(),
                                                                     int((bank != 0).any(1).sum())))
+    b = DeltaBlock(dtype=m.w.dtype)
+    n = residual_norm(x, torch.zeros_like(x))[1]
+    h, n2, state, saved = b.prompt(x[:, :T], n[:, :T])
+    grads = b.backward(torch.zeros_like(h), torch.ones_like(n2), saved)
+    for t in range(T, T + more):
+        h, n2 = b.token(x[:, t], n[:, t], state, t)
+    print("delta-rule block: next rows %s, rms %.3f; gradient of the projection, rms %.3g" % (
+        tuple(n2.shape), n2.float().square().mean().sqrt(), grads["w"].float().square().mean().sqrt()))
 
 
 if __name__ == "__main__":
