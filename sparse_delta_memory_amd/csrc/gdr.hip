@@ -189,14 +189,15 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
     Gates& gates = *reinterpret_cast<Gates*>(beta + kL);
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    const int bh = blk / p.chunks, c = blk - bh * p.chunks, b = bh / p.H, h = bh - b * p.H;
+    // Heads of the same tokens are neighbours: together they read and write whole rows.
+    const int bc = blk / p.H, h = blk - bc * p.H, b = bc / p.chunks, c = bc - b * p.chunks, bh = b * p.H + h;
     const int left = live_tokens(p.lens, b, p.T) - c * kL;
     if (left <= 0) return;
     const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4;
     const int64_t t0 = static_cast<int64_t>(c) * kL;
-    char* rec = p.rec + static_cast<int64_t>(blk) * kRecBytes<BACK>;
+    char* rec = p.rec + (static_cast<int64_t>(bh) * p.chunks + c) * kRecBytes<BACK>;
 
     Stage<T, KD, 256> sq, sk;
     sk.init(p.k);
@@ -1150,7 +1151,8 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
     float* const cross = dots + kWaves * kL;   // [waves]
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
-    const int bh = blk / p.chunks, c = blk - bh * p.chunks, b = bh / p.H, h = bh - b * p.H;
+    // Heads of the same tokens are neighbours: together they read and write whole rows.
+    const int bc = blk / p.H, h = blk - bc * p.H, b = bc / p.chunks, c = bc - b * p.chunks, bh = b * p.H + h;
     const int tid = static_cast<int>(threadIdx.x), lane = static_cast<int>(lane_id());
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int i16 = lane & 15, qd = lane >> 4, n0 = 16 * wave;

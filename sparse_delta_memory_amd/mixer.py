@@ -156,6 +156,7 @@ class DeltaBlock:
     def prompt(self, x, n, state=None, start=0):
         """(x, n) of the next block [P, T, model], the state [P, heads, d, d] and what backward needs."""
         P, T = n.shape[:2]
+        x, n = x.contiguous(), n.contiguous()   # parts of longer prompts: the norms take rows that are evenly spaced
         if start < 0 or start + T > self.table.shape[0]:
             raise ValueError("DeltaBlock.prompt: positions %d .. %d of a table of %d" % (start, start + T - 1, self.table.shape[0]))
         pos = torch.arange(start, start + T, dtype=torch.int32, device=n.device).repeat(P)
