@@ -474,8 +474,8 @@ size_t sdm_pa_workspace(const sdm_pa_io* io);
 sdm_status sdm_pa_step(const sdm_pa_io* io, int64_t ti, hipStream_t st);
 
 /* ------------------------------------------------------------------------------------------------
- * The mixer operators beside the bank: what makes a layer's slot ids, weights, keys and queries, and
- * the dense state that stands next to the sparse one. Same conventions as above; strides are in
+ * The mixer operators beside the bank: what makes a layer's slot ids, weights, keys and queries, the
+ * dense state that stands next to the sparse one, and the norms of its block. Same conventions as above; strides are in
  * elements and any multiple of one element is accepted (16-byte rows take wide accesses).
  * ------------------------------------------------------------------------------------------------ */
 
@@ -694,7 +694,11 @@ typedef struct sdm_gdr_grad {
                                `state`) */
 } sdm_gdr_grad;
 
-/* The backward of sdm_gdr_forward (io's o and last are not used; its workspace is of the backward size). */
+/* The backward of sdm_gdr_forward (io's o and last are not used; its workspace is of the backward size: two states, float32, per
+ * 64 tokens and head, and two float32 rows like v's). Heads that share a query and key head add their gradients in head order. No
+ * atomics: the bits are the same every run. A gate whose factor is 0 in float32 has a gradient of 0, and so has the first one when
+ * there is no `state`. Values that are not finite reach the gradients that they are part of, as forward; dg is a sum over the
+ * later tokens of its 64 (q . dq - v . dv, up to a reset), so it is NaN before such a value there as well. */
 sdm_status sdm_gdr_backward(const sdm_gdr_io* io, const sdm_gdr_grad* grad, hipStream_t st);
 
 /* One token of many requests. */

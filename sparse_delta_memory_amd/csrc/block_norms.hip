@@ -550,10 +550,12 @@ int team_width(int D, bool vec) {
 
 // Blocks: eight per compute unit, or as many as have rows.
 constexpr int64_t kBlocks = 2048;
-// Of a backward pass: partial sums of 16 MiB at most, one to four blocks per compute unit.
+// Of a backward pass: partial sums of 20 MiB at most, one block per compute unit to what is resident at once (by the kernels'
+// registers four blocks of a gate's, three of a residual's).
 int back_blocks(int64_t rows, int D, int M) {
-    int64_t most = (int64_t(16) << 20) / (int64_t(4) * M * D);
-    most = most < 256 ? 256 : most > 1024 ? 1024 : most;
+    const int64_t full = M == 1 ? 1024 : 768;
+    int64_t most = (int64_t(20) << 20) / (int64_t(4) * M * D);
+    most = most < 256 ? 256 : most > full ? full : most;
     return static_cast<int>(rows < most ? rows : most);
 }
 unsigned grid_of(int64_t rows, int per_block, int64_t most) {

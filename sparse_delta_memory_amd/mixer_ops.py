@@ -1,5 +1,5 @@
-"""The mixer operators beside the bank: head norms with rotation, slot selection and the gated linear
-recurrence. Argument marshalling only, as in the rest of the binding: torch provides device memory and
+"""The mixer operators beside the bank: head norms with rotation, slot selection, the gated linear recurrence
+and delta rule, and a block's norms. Argument marshalling only, as in the rest of the binding: torch provides device memory and
 the current stream, the HIP kernels of libsdm_amd.so do every step, and there is no CPU fallback.
 
 Heads are [.., heads, columns] device tensors with contiguous columns and any strides before them (views
@@ -491,7 +491,8 @@ def gdr_forward(q, k, v, g, beta, scale=None, state=None, lens=None, out=None, l
 def gdr_backward(d_out, q, k, v, g, beta, scale=None, state=None, d_last=None, lens=None, workspace=None, stream=None):
     """The backward of gdr_forward at its inputs, from the gradients d_out of out and d_last [B, H, dk, dv] float32 of the
     last state (None: zero): a dict of dq, dk, dv (contiguous, like q, k, v), dg and dbeta [B, T, H] float32 and dstate (the
-    gradient of the first state, [B, H, dk, dv] float32). Nothing of the forward is needed but its inputs."""
+    gradient of the first state, [B, H, dk, dv] float32). Nothing of the forward is needed but its inputs; the workspace holds a state
+    and its gradient, float32, per 64 tokens and head (1.9 GB for 8 x 4096 tokens of 16 heads of 128)."""
     fn = "gdr_backward"
     dev, io, keep = _gdr_io(fn, q, k, v, g, beta, scale, state, lens, None, None, 1, workspace, stream)
     _same(fn, q, d_out, d_last)
