@@ -454,17 +454,20 @@ __device__ __forceinline__ void store_four(void* out, int64_t at, f32x4 v, int l
     }
 }
 
-// The tiles of two bfloat16 chunks fit into LDS side by side: four more waves load the next chunk's while these compute (issuing
-// its 77 KiB of loads by themselves kept the computing waves for 3000 of a chunk's 10000 cycles). float32 chunks are loaded one by one.
-template <typename T>
-constexpr int kMainThreads = sizeof(T) == 2 ? 512 : 256;
+// Where the tiles of two chunks fit into LDS side by side, four more waves load the next chunk's while these compute (issuing
+// its 77 KiB of loads by themselves kept the computing waves for 3000 of a chunk's 10000 cycles). float32 chunks of keys past 64
+// columns are loaded one by one.
+template <typename T, int KD>
+constexpr bool kTwo = sizeof(T) == 2 || KD == 64;
+template <typename T, int KD>
+constexpr int kMainThreads = kTwo<T, KD> ? 512 : 256;
 
 // OUT: the outputs (and the last state). Else the states before every chunk and the rows r, for the backward pass; or (SEG)
 // the segments' own states and transitions. The transition is the rule on the columns of the unit matrix, whose values are 0.
 template <typename T, int KD, bool OUT, bool SEG>
-__global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_kernel(MainArgs p) {
+__global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256)) void gdr_kernel(MainArgs p) {
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
-    constexpr bool kAhead = sizeof(T) == 2;
+    constexpr bool kAhead = kTwo<T, KD>;
     constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
     constexpr int kBuf = (OUT ? 2 : 1) * kTile + kTileV + (OUT ? 2 : 1) * kFragBytes<T> + kFacBytes;
     extern __shared__ __align__(16) char lds[];
@@ -871,9 +874,9 @@ struct BackArgs {
 };
 
 template <typename T, int KD, bool SEG>
-__global__ __launch_bounds__(kMainThreads<T>, kMainThreads<T> / 256) void gdr_back_kernel(BackArgs p) {
+__global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256)) void gdr_back_kernel(BackArgs p) {
     constexpr int KB = KD / 32, KT = KD / 16, NP = kParts<T>;
-    constexpr bool kAhead = sizeof(T) == 2;
+    constexpr bool kAhead = kTwo<T, KD>;
     constexpr int kTile = kL * KD * static_cast<int>(sizeof(T)), kTileV = kL * 64 * static_cast<int>(sizeof(T));
     constexpr int kBuf = 2 * kTile + kTileV + 2 * kFragBytes<T> + kFacBytes;
     extern __shared__ __align__(16) char lds[];
@@ -1740,7 +1743,7 @@ size_t chunk_lds() { return 2 * kL * KD * sizeof(T) + 2 * kL * kRow * 4 + sizeof
 
 template <typename T, int KD>
 size_t main_lds(bool out) {
-    return (sizeof(T) == 2 ? 2 : 1) * (kL * ((out ? 2 : 1) * KD + 64) * sizeof(T) + (out ? 2 : 1) * kFragBytes<T> + kFacBytes);
+    return (kTwo<T, KD> ? 2 : 1) * (kL * ((out ? 2 : 1) * KD + 64) * sizeof(T) + (out ? 2 : 1) * kFragBytes<T> + kFacBytes);
 }
 
 int chunks_of(int T) { return (T + kL - 1) / kL; }
@@ -1826,8 +1829,8 @@ template <typename T, bool OUT, bool SEG>
 hipError_t main_go(const sdm_gdr_io* io, const MainArgs& a, hipStream_t st) {
     const int64_t blocks = SEG ? static_cast<int64_t>(a.made) * (a.cols + (a.kd + 63) / 64) : static_cast<int64_t>(a.nseg) * a.cols;
     const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(io->B) * io->H * blocks);
-    if (padded(io->dk) == 64) gdr_kernel<T, 64, OUT, SEG><<<grid, kMainThreads<T>, main_lds<T, 64>(OUT), st>>>(a);
-    else gdr_kernel<T, 128, OUT, SEG><<<grid, kMainThreads<T>, main_lds<T, 128>(OUT), st>>>(a);
+    if (padded(io->dk) == 64) gdr_kernel<T, 64, OUT, SEG><<<grid, kMainThreads<T, 64>, main_lds<T, 64>(OUT), st>>>(a);
+    else gdr_kernel<T, 128, OUT, SEG><<<grid, kMainThreads<T, 128>, main_lds<T, 128>(OUT), st>>>(a);
     return hipGetLastError();
 }
 
@@ -1919,16 +1922,16 @@ hipError_t backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st)
                reinterpret_cast<float*>(ws + l.grads), reinterpret_cast<float*>(ws + l.du), m.nseg, m.seg, nullptr, reinterpret_cast<float*>(ws + l.rown)};
     if (m.nseg > 1) {
         const unsigned grid = static_cast<unsigned>(bh * cols * (m.nseg - 1));
-        if (padded(io->dk) == 64) gdr_back_kernel<T, 64, true><<<grid, kMainThreads<T>, main_lds<T, 64>(true), st>>>(b);
-        else gdr_back_kernel<T, 128, true><<<grid, kMainThreads<T>, main_lds<T, 128>(true), st>>>(b);
+        if (padded(io->dk) == 64) gdr_back_kernel<T, 64, true><<<grid, kMainThreads<T, 64>, main_lds<T, 64>(true), st>>>(b);
+        else gdr_back_kernel<T, 128, true><<<grid, kMainThreads<T, 128>, main_lds<T, 128>(true), st>>>(b);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         float* from = reinterpret_cast<float*>(ws + l.rfrom);
         if ((e = chain_go<true>(io, ChainArgs{m.move, b.own, g->d_last, from, m.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st)) != hipSuccess) return e;
         b.from = from;
     }
     const unsigned grid = static_cast<unsigned>(bh * cols * m.nseg);
-    if (padded(io->dk) == 64) gdr_back_kernel<T, 64, false><<<grid, kMainThreads<T>, main_lds<T, 64>(true), st>>>(b);
-    else gdr_back_kernel<T, 128, false><<<grid, kMainThreads<T>, main_lds<T, 128>(true), st>>>(b);
+    if (padded(io->dk) == 64) gdr_back_kernel<T, 64, false><<<grid, kMainThreads<T, 64>, main_lds<T, 64>(true), st>>>(b);
+    else gdr_back_kernel<T, 128, false><<<grid, kMainThreads<T, 128>, main_lds<T, 128>(true), st>>>(b);
     if ((e = hipGetLastError()) != hipSuccess || io->T == 0) return e;
     const bool fold = per > 1;
     GradArgs a{q, k, v, d, io->g, io->beta, io->g_b, io->g_t, io->g_h, io->e_b, io->e_t, io->e_h, io->lens, io->T, io->H, chunks, io->dk, io->dv,
