@@ -203,15 +203,18 @@ struct ChunkArgs {
 template <bool BACK>
 constexpr int kRecBytes = (BACK ? 3 : 2) * kTriBytes + kFacBytes;
 
+template <typename T, int KD>
+constexpr int kChunkTiles = 2 * kL * KD * static_cast<int>(sizeof(T)) > kL * kRow * 4 ? 2 * kL * KD * static_cast<int>(sizeof(T)) : kL * kRow * 4;
+
 template <typename T, int KD, bool BACK>
 __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
     constexpr int KB = KD / 32;
     extern __shared__ __align__(16) char lds[];
     T* kt = reinterpret_cast<T*>(lds);
     T* qt = kt + kL * KD;
-    float* A = reinterpret_cast<float*>(qt + kL * KD);
-    float* N = A + kL * kRow;
-    float* beta = N + kL * kRow;
+    float* N = reinterpret_cast<float*>(lds);   // over the tiles, once the products of them are done: three blocks fit a compute unit
+    float* A = reinterpret_cast<float*>(lds + kChunkTiles<T, KD>);
+    float* beta = A + kL * kRow;
     Gates& gates = *reinterpret_cast<Gates*>(beta + kL);
 
     const int blk = xcd_block(static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
@@ -1739,7 +1742,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStep a) {
 // --------------------------------------------------------------------------------------------- plans
 
 template <typename T, int KD>
-size_t chunk_lds() { return 2 * kL * KD * sizeof(T) + 2 * kL * kRow * 4 + sizeof(Gates) + kL * 4; }
+size_t chunk_lds() { return kChunkTiles<T, KD> + kL * kRow * 4 + sizeof(Gates) + kL * 4; }
 
 template <typename T, int KD>
 size_t main_lds(bool out) {
