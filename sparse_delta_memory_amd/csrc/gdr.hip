@@ -26,13 +26,15 @@
 // whose r (backwards: du; in the last kernel: whose results) holds such a value goes over its columns of the chunk again token by
 // token, by the definition, where it reaches what it is part of and nothing else; a factor of 0 leaves nothing of it.
 //
-// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): forward 400 us, 115 of them the records (69 KiB a chunk and head
-// read and written, 4.5 TB/s) and 283 the way along 64 chunks: 4.4 us a chunk, where a wave's 216 matrix instructions keep its
-// SIMD's unit busy for 3456 of 8100 cycles; the steps of a chunk follow from each other, and with 16 columns a wave there is one
-// computing wave per SIMD to fill them. (More waves for the outputs, with the state's parts handed over in LDS: 430 us, their
-// loads of q and the two barriers a chunk; reads from LDS a step ahead by hand: 283, past 256 registers 650.) Backward 1.8 ms:
-// records 190, states 260, gradients 330, the rest 980: 272 KiB a chunk and head through memory at 2.3 TB/s, loads and
-// products of a block one after the other in its 152 KiB of LDS.
+// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): forward 365 us, some 95 of them the records (53 KiB a chunk and
+// head read and written) and 270 the way along 64 chunks: 4.2 us a chunk, where a wave's 216 matrix instructions keep its SIMD's
+// unit busy for 3456 of 8100 cycles; the steps of a chunk follow from each other, and with 16 columns a wave there is one
+// computing wave per SIMD to fill them. Not kept: more waves for the outputs, with the state's parts handed over in LDS (430 us:
+// loads of q in the operands' layout take 400 cycles each, and two barriers a chunk); reads from LDS a step ahead by hand (283
+// beside 283 for the kernel; past 256 registers 650); a chunk's results stored behind the next chunk's barrier (the same). Backward
+// 1.52 ms: records 135, states 260, gradients 350, the rest 980, whose 272 KiB a chunk and head come and go at 2.3 TB/s: a
+// block's loads and products follow each other, and its 157 KiB of LDS leave no room for a second block (all loads issued at
+// once, ahead of the gates: the same time).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -1755,7 +1757,7 @@ int chunks_of(int T) { return (T + kL - 1) / kL; }
 // makes every segment's own state and transition (as many columns again as the state has rows), a kernel chains them, and the main
 // pass runs on all segments at once. Rounds of blocks over the compute units times a segment's chunks, in units of a chunk (3.5 us,
 // 3 without outputs; a step of the chain is 1.5), say whether and how finely: 1 x 16384 tokens x 8 heads of 128, forward, 925 us whole
-// and 265 in 16 segments; 8 x 4096 x 16 stays whole.
+// and 226 in 16 segments; 8 x 4096 x 16 stays whole.
 constexpr int kUnits = 256;
 struct SegPlan {
     int nseg, seg;
