@@ -24,7 +24,9 @@
 //
 // What is not finite. A tile product takes a value that is not finite to other tokens of the chunk (0 times it is NaN). A wave
 // whose r (backwards: du; in the last kernel: whose results) holds such a value goes over its columns of the chunk again token by
-// token, by the definition, where it reaches what it is part of and nothing else; a factor of 0 leaves nothing of it.
+// token, by the definition, where it reaches what it is part of and nothing else; a factor of 0 leaves nothing of it. A key alone
+// in its sequence (a reset at it and behind it) shows in no r, but the state's product takes the whole tile of keys: N's diagonal, 0
+// otherwise, is NaN at a key that is not finite, and so is then some r of every column.
 //
 // What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): forward 365 us, some 95 of them the records (53 KiB a chunk and
 // head read and written) and 270 the way along 64 chunks: 4.2 us a chunk, where a wave's 216 matrix instructions keep its SIMD's
@@ -273,6 +275,7 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
                 const float d = (lhi - jh[r]) + (llo - jl[r]);
                 const float w = __builtin_amdgcn_exp2f(rev ? -d : d);
                 s[r] = (rev ? j >= i16 : isA ? j < i16 : j <= i16) ? sdm_decayed(w * m, a[r]) : 0.0f;
+                if (isA && j == i16) s[r] = 0.0f * a[r];   // NaN for a key that is not finite
             }
         } else {
             const float ot = (rev ? gates.down : gates.up)[16 * it + i16] * (m * gates.tau[4 * it + jt]);
