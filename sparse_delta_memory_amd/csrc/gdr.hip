@@ -370,6 +370,7 @@ struct MainArgs {
     int nseg, seg, made;
     const float* from;
     float *own, *move;
+    int32_t* resets;          // [B H, nseg] (segments pass): whether a gate of the segment resets
 };
 
 // A wave's part of a state: rows 32 (d / 2) + 8 quarter + 4 (d % 2) + r of tile d, one column per lane, read and written
@@ -552,6 +553,7 @@ __global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256))
     }
 
 
+    bool cut = false;   // a token of the lane's place resets
     for (int c = first; c < chunks; ++c) {
         const int buf = kAhead ? __builtin_amdgcn_readfirstlane((c - first) & 1) : 0, t0 = c * kL, left = len - t0;
         char* const at = tiles(buf);
@@ -564,6 +566,7 @@ __global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256))
         if (kAhead) lds_barrier();
         else tile_barrier();
         if (!OUT && !SEG) place.write(p.states + (static_cast<int64_t>(bh) * p.chunks + c) * one, S);
+        if (SEG) cut |= fac.one[lane] == 0.0f;
 
         // S^T k and S^T q
         f32x4 Y[4], O[4];   // Y, tile it: tokens 16 it + 4 quarter + r down, column n0 + lane % 16; O: transposed
@@ -736,17 +739,22 @@ __global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256))
             static_cast<T*>(p.out)[b * p.o_b + t * p.o_t + h * p.o_h + col] = narrow<T>(0.0f);
         }
     }
-    if constexpr (SEG) place.write((unit ? p.move : p.own) + (static_cast<int64_t>(bh) * p.nseg + si) * one, S);
-    else if (p.last != nullptr && si + 1 == p.nseg) place.write(p.last + bh * one, S);
+    if constexpr (SEG) {
+        place.write((unit ? p.move : p.own) + (static_cast<int64_t>(bh) * p.nseg + si) * one, S);
+        const bool any = __ballot(cut) != 0;
+        if (unit && cb == 0 && tid == 0) p.resets[static_cast<int64_t>(bh) * p.nseg + si] = any;
+    } else if (p.last != nullptr && si + 1 == p.nseg) place.write(p.last + bh * one, S);
 }
 
 // The states before every segment (REV: the gradients behind every one) from the segments' own and their transitions,
 //     S_{n+1} = M_n S_n + own_n    (REV: R_{n-1} = M_n^T R_n + own_n),
 // one block per 16 columns of a (stream, head)'s state: each wave 16 rows, the columns in LDS between the steps, the next step's
-// matrices in flight. Both factors in three bfloat16 parts, whatever the inputs. A segment whose transition is 0 (a reset) leaves
-// nothing of what was before, finite or not.
+// matrices in flight. Both factors in three bfloat16 parts, whatever the inputs. A segment with a reset leaves nothing of what was
+// before, finite or not. One without does, also where its transition is 0 in float32: by the rule every token takes a column's
+// infinity or NaN into the state again, as the product with it does.
 struct ChainArgs {
     const float *move, *own;   // [B H, nseg]
+    const int32_t* resets;     // [B H, nseg]
     const float* start;        // [B H] (NULL: zero)
     float* to;                 // [B H, nseg]
     int nseg, kd, vd, cols;    // cols: blocks of 16 columns
@@ -777,6 +785,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
     const bool four = !REV && p.kd % 4 == 0;
     float m[KB][8];
     f32x4 own;
+    int cleared = 0;
     auto part = [&](const float* from, f32x4& x) {
         const auto b = uniform_buffer(from, static_cast<int>(one) * 4);
 #pragma unroll
@@ -800,6 +809,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
             }
         }
         part(p.own + (static_cast<int64_t>(bh) * p.nseg + n) * one, own);
+        cleared = p.resets[static_cast<int64_t>(bh) * p.nseg + n];
     };
     auto keep = [&](int n, f32x4 s, float* at) {
         float* to = p.to + (static_cast<int64_t>(bh) * p.nseg + n) * one;
@@ -819,13 +829,12 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
     int buf = 0;
     for (int n = n0; n != n1; n += step, buf ^= 1) {
         Parts<bf16_t, 3> mp[KB];
-        bool some = false;
+        const bool some = cleared == 0;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (32 * kb + 8 * qd + e >= p.kd) m[kb][e] = 0.0f;   // the next row's
-                some |= m[kb][e] != 0.0f;
             }
             split(m[kb], mp[kb]);
         }
@@ -833,7 +842,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
         const f32x4 add = own;
         if (n + step != n1) load(n + step);
         __syncthreads();   // the columns are complete
-        if (__ballot(some) != 0) {
+        if (some) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 const float* at = cols[buf] + i16 * kPad + 32 * kb + 8 * qd;
@@ -1783,7 +1792,7 @@ SegPlan seg_plan(const sdm_gdr_io* io) {
 
 // Byte offsets in the workspace.
 struct GdrLayout {
-    size_t rec, move, own, from, rown, rfrom, states, grads, miss, du, fq, fk, total;
+    size_t rec, move, own, from, resets, rown, rfrom, states, grads, miss, du, fq, fk, total;
 };
 GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
     const size_t bh = static_cast<size_t>(io->B) * io->H, n = bh * chunks_of(io->T), rows = bh * io->T;
@@ -1800,6 +1809,7 @@ GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
         l.move = take(bh * sp.nseg * io->dk * io->dk * 4);
         l.own = take(states);
         l.from = take(states);
+        l.resets = take(bh * sp.nseg * 4);
         if (backward) {
             l.rown = take(states);
             l.rfrom = take(states);
@@ -1878,11 +1888,12 @@ hipError_t begin(const sdm_gdr_io* io, const GdrLayout& l, MainArgs& a, hipStrea
     a.made = BACK ? sp.nseg : sp.nseg - 1;   // what leaves the last one only the backward pass goes through
     a.own = reinterpret_cast<float*>(ws + l.own);
     a.move = reinterpret_cast<float*>(ws + l.move);
+    a.resets = reinterpret_cast<int32_t*>(ws + l.resets);
     a.from = nullptr;
     if ((e = main_go<T, false, true>(io, a, st)) != hipSuccess) return e;
     float* from = reinterpret_cast<float*>(ws + l.from);
     a.from = from;
-    return chain_go<false>(io, ChainArgs{a.move, a.own, a.start, from, sp.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st);
+    return chain_go<false>(io, ChainArgs{a.move, a.own, a.resets, a.start, from, sp.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st);
 }
 
 template <typename T>
@@ -1934,7 +1945,7 @@ hipError_t backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st)
         else gdr_back_kernel<T, 128, true><<<grid, kMainThreads<T, 128>, main_lds<T, 128>(true), st>>>(b);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         float* from = reinterpret_cast<float*>(ws + l.rfrom);
-        if ((e = chain_go<true>(io, ChainArgs{m.move, b.own, g->d_last, from, m.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st)) != hipSuccess) return e;
+        if ((e = chain_go<true>(io, ChainArgs{m.move, b.own, m.resets, g->d_last, from, m.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st)) != hipSuccess) return e;
         b.from = from;
     }
     const unsigned grid = static_cast<unsigned>(bh * cols * m.nseg);

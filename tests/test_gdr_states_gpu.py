@@ -1,0 +1,56 @@
+"""GPU: what gates and lengths do to states, the same for a whole row, for one whose time axis is cut into segments and for a token."""
+
+import os
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():
+    pytest.skip("no GPU", allow_module_level=True)
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
+import sparse_delta_memory_amd as sdm  # noqa: E402
+from test_gdr_gpu import DT, INF, NAN, make, say  # noqa: E402
+from test_gdr_more_gpu import close, run  # noqa: E402
+
+
+def cut_into_segments(B, T, H, dk, dv, dtype):
+    few, many = (sdm.gdr_workspace_bytes(n, T, H, H, dk, dv, DT[dtype]) for n in (B, 1000 * B))
+    return few > many // 1000 + 4 * dk * dk
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [200, 900])
+@pytest.mark.parametrize("value", [INF, NAN])
+def test_only_a_reset_stops_a_value_that_is_not_finite(dtype, T, value):
+    """Gates whose product is 0 in float32 (from 50 times e^-2 on) but none of which is by itself: every token's u takes what is not finite of its column
+    into the state again, so the column stays that way, in a whole row and in segments; so does a gradient's, back in time."""
+    say("gdr product of gates", dtype, T, value)
+    x = make(1, T, 1, 1, 32, 40, dtype)
+    assert cut_into_segments(1, T, 1, 32, 40, dtype) == (T == 900)
+    x["g"].fill_(-2.0)
+    clean = run(x)
+    y = {n: None if t is None else t.clone() for n, t in x.items()}
+    y["state"][0, 0, 3, 7] = value
+    y["d_last"][0, 0, 5, 11] = value
+    r = run(y)
+    cols = torch.arange(40)
+    for out in ("o", "last"):
+        assert not torch.isfinite(r[out][..., 7]).any(), out
+        close(out, r[out][..., cols != 7], clean[out][..., cols != 7])
+    for out in ("dv", "dstate"):
+        assert not torch.isfinite(r[out][..., 11]).any(), out
+    close("dv", r["dv"][..., (cols != 7) & (cols != 11)], clean["dv"][..., (cols != 7) & (cols != 11)])
+    assert not torch.isfinite(r["dk"]).any()
+    # A reset ends it.
+    for z in (y, x):
+        z["g"][0, T // 2] = -INF
+    r, clean = run(y), run(x)
+    close("o", r["o"][:, T // 2:], clean["o"][:, T // 2:])
+    close("last", r["last"], clean["last"])
+    close("dv", r["dv"][:, :T // 2, :, cols != 7], clean["dv"][:, :T // 2, :, cols != 7])
+    close("dstate", r["dstate"], clean["dstate"])
