@@ -345,6 +345,10 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
     }
 }
 
+// What a segment of the time axis does to the state before it: takes it through its transition, leaves nothing of it (a gate
+// resets), or nothing at all (past the row's length).
+enum Kind { kMoves, kClears, kIdle };
+
 // ---------------------------------------------------------------------------------------- along the time axis
 //
 // A block owns 64 columns of one (stream, head)'s state, 16 for each of its four waves, in registers over all chunks
@@ -370,7 +374,7 @@ struct MainArgs {
     int nseg, seg, made;
     const float* from;
     float *own, *move;
-    int32_t* resets;          // [B H, nseg] (segments pass): whether a gate of the segment resets
+    int32_t* kinds;           // [B H, nseg] (segments pass): what a segment does to a state before it (Kind)
 };
 
 // A wave's part of a state: rows 32 (d / 2) + 8 quarter + 4 (d % 2) + r of tile d, one column per lane, read and written
@@ -741,8 +745,8 @@ __global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256))
     }
     if constexpr (SEG) {
         place.write((unit ? p.move : p.own) + (static_cast<int64_t>(bh) * p.nseg + si) * one, S);
-        const bool any = __ballot(cut) != 0;
-        if (unit && cb == 0 && tid == 0) p.resets[static_cast<int64_t>(bh) * p.nseg + si] = any;
+        const int kind = chunks <= first ? kIdle : __ballot(cut) != 0 ? kClears : kMoves;
+        if (unit && cb == 0 && tid == 0) p.kinds[static_cast<int64_t>(bh) * p.nseg + si] = kind;
     } else if (p.last != nullptr && si + 1 == p.nseg) place.write(p.last + bh * one, S);
 }
 
@@ -751,10 +755,10 @@ __global__ __launch_bounds__((kMainThreads<T, KD>), (kMainThreads<T, KD> / 256))
 // one block per 16 columns of a (stream, head)'s state: each wave 16 rows, the columns in LDS between the steps, the next step's
 // matrices in flight. Both factors in three bfloat16 parts, whatever the inputs. A segment with a reset leaves nothing of what was
 // before, finite or not. One without does, also where its transition is 0 in float32: by the rule every token takes a column's
-// infinity or NaN into the state again, as the product with it does.
+// infinity or NaN into the state again, as the product with it does. One past the row's length leaves every bit of the state.
 struct ChainArgs {
     const float *move, *own;   // [B H, nseg]
-    const int32_t* resets;     // [B H, nseg]
+    const int32_t* kinds;      // [B H, nseg]
     const float* start;        // [B H] (NULL: zero)
     float* to;                 // [B H, nseg]
     int nseg, kd, vd, cols;    // cols: blocks of 16 columns
@@ -785,7 +789,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
     const bool four = !REV && p.kd % 4 == 0;
     float m[KB][8];
     f32x4 own;
-    int cleared = 0;
+    int kind = kMoves;
     auto part = [&](const float* from, f32x4& x) {
         const auto b = uniform_buffer(from, static_cast<int>(one) * 4);
 #pragma unroll
@@ -809,7 +813,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
             }
         }
         part(p.own + (static_cast<int64_t>(bh) * p.nseg + n) * one, own);
-        cleared = p.resets[static_cast<int64_t>(bh) * p.nseg + n];
+        kind = p.kinds[static_cast<int64_t>(bh) * p.nseg + n];
     };
     auto keep = [&](int n, f32x4 s, float* at) {
         float* to = p.to + (static_cast<int64_t>(bh) * p.nseg + n) * one;
@@ -829,7 +833,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
     int buf = 0;
     for (int n = n0; n != n1; n += step, buf ^= 1) {
         Parts<bf16_t, 3> mp[KB];
-        const bool some = cleared == 0;
+        const int now = kind;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
@@ -842,7 +846,7 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
         const f32x4 add = own;
         if (n + step != n1) load(n + step);
         __syncthreads();   // the columns are complete
-        if (some) {
+        if (now == kMoves) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
                 const float* at = cols[buf] + i16 * kPad + 32 * kb + 8 * qd;
@@ -856,8 +860,8 @@ __global__ __launch_bounds__(4 * KD) void gdr_chain_kernel(ChainArgs p) {
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) x += part_[kb];
         }
-        x += add;
-        keep(n + step, x, cols[buf ^ 1]);
+        s = now == kIdle ? s : x + add;
+        keep(n + step, s, cols[buf ^ 1]);
     }
 }
 
@@ -1792,7 +1796,7 @@ SegPlan seg_plan(const sdm_gdr_io* io) {
 
 // Byte offsets in the workspace.
 struct GdrLayout {
-    size_t rec, move, own, from, resets, rown, rfrom, states, grads, miss, du, fq, fk, total;
+    size_t rec, move, own, from, kinds, rown, rfrom, states, grads, miss, du, fq, fk, total;
 };
 GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
     const size_t bh = static_cast<size_t>(io->B) * io->H, n = bh * chunks_of(io->T), rows = bh * io->T;
@@ -1809,7 +1813,7 @@ GdrLayout gdr_layout(const sdm_gdr_io* io, bool backward) {
         l.move = take(bh * sp.nseg * io->dk * io->dk * 4);
         l.own = take(states);
         l.from = take(states);
-        l.resets = take(bh * sp.nseg * 4);
+        l.kinds = take(bh * sp.nseg * 4);
         if (backward) {
             l.rown = take(states);
             l.rfrom = take(states);
@@ -1888,12 +1892,12 @@ hipError_t begin(const sdm_gdr_io* io, const GdrLayout& l, MainArgs& a, hipStrea
     a.made = BACK ? sp.nseg : sp.nseg - 1;   // what leaves the last one only the backward pass goes through
     a.own = reinterpret_cast<float*>(ws + l.own);
     a.move = reinterpret_cast<float*>(ws + l.move);
-    a.resets = reinterpret_cast<int32_t*>(ws + l.resets);
+    a.kinds = reinterpret_cast<int32_t*>(ws + l.kinds);
     a.from = nullptr;
     if ((e = main_go<T, false, true>(io, a, st)) != hipSuccess) return e;
     float* from = reinterpret_cast<float*>(ws + l.from);
     a.from = from;
-    return chain_go<false>(io, ChainArgs{a.move, a.own, a.resets, a.start, from, sp.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st);
+    return chain_go<false>(io, ChainArgs{a.move, a.own, a.kinds, a.start, from, sp.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st);
 }
 
 template <typename T>
@@ -1945,7 +1949,7 @@ hipError_t backward(const sdm_gdr_io* io, const sdm_gdr_grad* g, hipStream_t st)
         else gdr_back_kernel<T, 128, true><<<grid, kMainThreads<T, 128>, main_lds<T, 128>(true), st>>>(b);
         if ((e = hipGetLastError()) != hipSuccess) return e;
         float* from = reinterpret_cast<float*>(ws + l.rfrom);
-        if ((e = chain_go<true>(io, ChainArgs{m.move, b.own, m.resets, g->d_last, from, m.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st)) != hipSuccess) return e;
+        if ((e = chain_go<true>(io, ChainArgs{m.move, b.own, m.kinds, g->d_last, from, m.nseg, io->dk, io->dv, (io->dv + 15) / 16}, st)) != hipSuccess) return e;
         b.from = from;
     }
     const unsigned grid = static_cast<unsigned>(bh * cols * m.nseg);

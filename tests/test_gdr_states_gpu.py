@@ -54,3 +54,21 @@ def test_only_a_reset_stops_a_value_that_is_not_finite(dtype, T, value):
     close("last", r["last"], clean["last"])
     close("dv", r["dv"][:, :T // 2, :, cols != 7], clean["dv"][:, :T // 2, :, cols != 7])
     close("dstate", r["dstate"], clean["dstate"])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,dk,dv", [(300, 24, 40), (1500, 32, 40), (1500, 128, 33)])
+def test_no_tokens_leave_every_bit_of_a_state(dtype, T, dk, dv):
+    """Infinities, subnormal values and zeros of either sign too: the state of a row without tokens, and its gradient."""
+    say("gdr rows without tokens", dtype, T, dk, dv)
+    lens = [0, T, -1]
+    x = make(3, T, 1, 1, dk, dv, dtype, gate=4.0, lens=lens)
+    assert cut_into_segments(3, T, 1, dk, dv, dtype) == (T == 1500)
+    for name in ("state", "d_last"):
+        for b in (0, 2):
+            x[name][b, 0, 1, 2], x[name][b, 0, 2, 3], x[name][b, 0, 3, 4], x[name][b, 0, 4, 5], x[name][b, 0, 5, 6] = INF, -INF, 1e-40, -0.0, 3e-38
+    r = run(x)
+    bits = lambda t: t.cpu().view(torch.int32)  # noqa: E731
+    for b in (0, 2):
+        assert torch.equal(bits(r["last"][b]), bits(x["state"][b])), b
+        assert torch.equal(bits(r["dstate"][b]), bits(x["d_last"][b])), b
