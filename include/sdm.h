@@ -572,7 +572,7 @@ typedef struct sdm_glr_io {
     const void* q;          /* [B, T, Hk, dk]: element (b, t, h) at q + b q_b + t q_t + h q_h, dk contiguous columns */
     const void* k;          /* [B, T, Hk, dk] */
     const void* v;          /* [B, T, H, dv] */
-    const float* g;         /* [B, T, H] log gates (<= 0; -infinity, or anything at or below -10000, resets the state) */
+    const float* g;         /* [B, T, H] log gates (<= 0; one whose factor exp(g) is below 2^-126 resets the state, as -infinity does) */
     int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, g_b, g_t, g_h;
     const float* state;     /* [B, H, dk, dv] contiguous, the state before the first token (NULL: zero). States are 16-byte
                                aligned, or 4-byte where dk dv is no multiple of 4 */
@@ -650,7 +650,7 @@ typedef struct sdm_gdr_io {
     const void* q;          /* [B, T, Hk, dk]: element (b, t, h) at q + b q_b + t q_t + h q_h, dk contiguous columns */
     const void* k;          /* [B, T, Hk, dk] */
     const void* v;          /* [B, T, H, dv] */
-    const float* g;         /* [B, T, H] log gates (<= 0; -infinity, or anything at or below -10000, resets the state) */
+    const float* g;         /* [B, T, H] log gates (<= 0; one whose factor exp(g) is below 2^-126 resets the state, as -infinity does) */
     const float* beta;      /* [B, T, H] what share of the missing part a token writes (0..1; up to 2 / |k|^2 is stable) */
     int64_t q_b, q_t, q_h, k_b, k_t, k_h, v_b, v_t, v_h, g_b, g_t, g_h, e_b, e_t, e_h;   /* e: of beta */
     const float* state;     /* [B, H, dk, dv] contiguous, the state before the first token (NULL: zero), aligned as in sdm_glr_io */

@@ -248,7 +248,7 @@ __global__ __launch_bounds__(256) void gdr_chunk_kernel(ChunkArgs p) {
         f->f[lane] = gates.f[lane];
         f->u[lane] = gates.u[lane];
         f->beta[lane] = e;
-        f->one[lane] = exp2_of(static_cast<double>(g < kGateMin ? kGateMin : g) * kLog2E);
+        f->one[lane] = gate_factor(g);
     }
     tile_barrier();
 
@@ -1527,7 +1527,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
             return widen(*reinterpret_cast<const T*>(piece<T, KD>(tile, t, col / kElems) + (col % kElems) * static_cast<int>(sizeof(T))));
         };
         for (int t = 0; t < n; ++t) {
-            const float a = exp2_of(static_cast<double>(one_gate[t] < kGateMin ? kGateMin : one_gate[t]) * kLog2E), be = beta[t], k = key(kt, t);
+            const float a = gate_factor(one_gate[t]), be = beta[t], k = key(kt, t);
             float sq_ = 0.0f, sk_ = 0.0f;
 #pragma unroll
             for (int kb = 0; kb < VB; ++kb) {
@@ -1562,7 +1562,7 @@ __global__ __launch_bounds__(4 * KD, KD == 128 ? 2 : 1) void gdr_grad_kernel(Gra
             }
         }
         for (int t = n - 1; t >= 0; --t) {
-            const float a = exp2_of(static_cast<double>(one_gate[t] < kGateMin ? kGateMin : one_gate[t]) * kLog2E), be = beta[t], k = key(kt, t),
+            const float a = gate_factor(one_gate[t]), be = beta[t], k = key(kt, t),
                         q = p.scale * key(qt, t);
             float sum = 0.0f;
 #pragma unroll
@@ -1704,7 +1704,7 @@ __global__ __launch_bounds__(256) void gdr_step_kernel(GdrStep a) {
     } else {
         qk[1][tid - 128] = tid - 128 < io.dk ? widen((static_cast<const T*>(io.k) + b * io.k_b + hk * io.k_h)[tid - 128]) : 0.0f;
     }
-    const float ga = expf(io.g[b * io.g_b + h * io.g_h]);
+    const float ga = token_factor(io.g[b * io.g_b + h * io.g_h]);
     const float v = tid < nc ? widen((static_cast<const T*>(io.v) + b * io.v_b + h * io.v_h)[n0 + tid]) : 0.0f;
     const float beta = io.beta[b * io.e_b + h * io.e_h];
     __syncthreads();

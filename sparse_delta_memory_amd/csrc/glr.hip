@@ -735,7 +735,7 @@ __global__ __launch_bounds__(256) void glr_step_kernel(GlrStep a) {
     } else if (tid >= 128 && tid - 128 < io.dk) {
         qk[1][tid - 128] = widen((static_cast<const T*>(io.k) + b * io.k_b + hk * io.k_h)[tid - 128]);
     }
-    const float ga = expf(io.g[b * io.g_b + h * io.g_h]);
+    const float ga = token_factor(io.g[b * io.g_b + h * io.g_h]);
     constexpr int kU = 8;   // rows in flight
     typedef float fv __attribute__((ext_vector_type(V)));
     for (int d0 = 0; d0 < io.dk; d0 += groups * kU) {   // the same trips for every lane: the barrier below is in it

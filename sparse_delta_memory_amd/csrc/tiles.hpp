@@ -379,8 +379,11 @@ __device__ __forceinline__ void pieces(uint64_t cuts, double x, int lane, F f) {
     }
 }
 
-// Whether a gate leaves nothing: its factor is 0 as the chunks and the step compute it.
-__device__ __forceinline__ bool resets(float g) { return __builtin_amdgcn_exp2f(g * static_cast<float>(kLog2E)) == 0.0f; }
+// exp(g) of one gate as the chunks take it: 0 below 2^-126 (the gate resets); NaN stays.
+__device__ __forceinline__ float gate_factor(float g) { return exp2_of(static_cast<double>(g < kGateMin ? kGateMin : g) * kLog2E); }
+__device__ __forceinline__ bool resets(float g) { return gate_factor(g) == 0.0f; }
+// The same for one token. expf goes on below 2^-126, where a state that is not finite would outlive the gate that resets it in a chunk.
+__device__ __forceinline__ float token_factor(float g) { return resets(g) ? 0.0f : expf(g); }
 
 // The score operands of a chunk, computed once and shared by the waves: pair n is (it, jb), the tiles of tokens
 // 16 it across and 32 jb down; its two halves are the score tiles jt = 2 jb and 2 jb + 1. Of the 16 tiles the

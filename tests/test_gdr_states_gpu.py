@@ -14,7 +14,7 @@ if not torch.cuda.is_available():
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 import sparse_delta_memory_amd as sdm  # noqa: E402
-from test_gdr_gpu import DT, INF, NAN, make, say  # noqa: E402
+from test_gdr_gpu import DT, INF, NAN, args, cuda, make, say  # noqa: E402
 from test_gdr_more_gpu import close, run  # noqa: E402
 
 
@@ -72,3 +72,29 @@ def test_no_tokens_leave_every_bit_of_a_state(dtype, T, dk, dv):
     for b in (0, 2):
         assert torch.equal(bits(r["last"][b]), bits(x["state"][b])), b
         assert torch.equal(bits(r["dstate"][b]), bits(x["d_last"][b])), b
+
+
+@pytest.mark.parametrize("op", ["gdr", "glr"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_token_clears_what_a_prompt_clears(op, dtype):
+    """Gates on both sides of where their factor is 0 (below 2^-126): a state that is not finite is gone after a prompt of one token if
+    and only if it is gone after the token."""
+    say("a token's gate", op, dtype)
+    gates = [-0.5, -80.0, -87.0, -87.3, -87.33, -87.34, -87.5, -88.0, -90.0, -95.0, -100.0, -103.0, -103.9, -104.0, -150.0, -1e4, -1e30, -INF]
+    border = torch.tensor(-126.0 / 1.4426950408889634)
+    gates += [float(border + n * 2.0 ** -17) for n in range(-3, 4)]   # the float32 values next to it
+    x = cuda(make(len(gates), 1, 2, 1, 16, 24, dtype))
+    x["g"][:] = torch.tensor(gates, device="cuda")[:, None, None]
+    ins = args(x) if op == "gdr" else args(x)[:4]
+    forward, step = (sdm.gdr_forward, sdm.gdr_step) if op == "gdr" else (sdm.glr_forward, sdm.glr_step)
+    for value in (INF, NAN, 1.0):
+        state = torch.full_like(x["state"], value)
+        o, last = forward(*ins, state=state)
+        s = state.clone()
+        p = step(*[t[:, 0] for t in ins], s)
+        assert torch.equal(torch.isfinite(s), torch.isfinite(last)), value
+        assert torch.equal(torch.isfinite(p), torch.isfinite(o[:, 0])), value
+        gone = torch.isfinite(last).flatten(1).all(1)
+        assert value == 1.0 or (not gone[:4].any() and gone[6:18].all())
+    x["g"].fill_(NAN)   # which is no reset
+    assert torch.isnan(step(*[t[:, 0] for t in ins], x["state"].clone())).all()
