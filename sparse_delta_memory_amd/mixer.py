@@ -178,9 +178,11 @@ class DeltaBlock:
         o = gdr_step(q, k, v, *self.gates(g), state)
         return self.residual(x, gate_norm(o, z, self.o_norm).flatten(1) @ self.w_out)
 
-    def backward(self, d_x, d_n, saved):
-        """Gradients from those of prompt's x and n: a dict of x, n, state and every parameter."""
+    def backward(self, d_x, d_n, saved, d_state=None):
+        """Gradients from those of prompt's x and n, and of the state that it returned (d_state [P, heads, d, d] float32; None: zero): a dict
+        of x, n, state and every parameter. Of a prompt run in parts the last part comes first, and its "state" is the d_state of the one before."""
         n, pos, q0, k0, ins, z, g, o, y, h, state = saved
+        d_x, d_n = d_x.contiguous(), d_n.contiguous()   # as prompt's rows
         r = residual_norm_backward(d_x, d_n, h, y, self.next_norm, scale=self.scale, norm_y=self.norm_y, y_weight=self.y_norm)
         dy = r["dy"].flatten(0, 1)
         out = dict(x=r["dx"], next_norm=r["dw"], scale=r["dscale"], y_norm=r["dwy"])
@@ -188,7 +190,7 @@ class DeltaBlock:
         out["w_out"] = gated.t() @ dy
         e = gate_norm_backward((dy @ self.w_out.t()).view_as(o), o, z, self.o_norm)
         out["o_norm"] = e["dw"]
-        s = gdr_backward(e["dx"].unflatten(0, n.shape[:2]), *ins, state=state)
+        s = gdr_backward(e["dx"].unflatten(0, n.shape[:2]), *ins, state=state, d_last=d_state)
         out["state"] = s["dstate"]
         f = norm_rope_backward(s["dq"].flatten(0, 1), s["dk"].flatten(0, 1), q0, k0, self.unit, self.unit, pos, self.table, eps=1e-12)
         beta = ins[4].flatten(0, 1)
