@@ -108,7 +108,7 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
     }
 }
 
-// 1 / (1 + exp(-z)). For float32 results the exponent's rounding, up to |z| / 2 units, is put back.
+// 1 / (1 + exp(-z)), for z >= kFarGate. For float32 results the exponent's rounding, up to |z| / 2 units, is put back.
 template <typename T>
 __device__ __forceinline__ float sigmoid_of(float z) {
     constexpr float kL2E = 1.44269504089f;
@@ -116,10 +116,26 @@ __device__ __forceinline__ float sigmoid_of(float z) {
     float e = __builtin_amdgcn_exp2f(t);
     if constexpr (sizeof(T) == 4) {
         const float lo = fmaf(-z, kL2E, -t) - z * 1.92596299e-8f;
-        if (fabsf(t) < 126.0f) e = fmaf(e, lo * 0.69314718056f, e);   // past it e is infinite or as good as 0
+        if (fabsf(t) < 126.0f) e = fmaf(e, lo * 0.69314718056f, e);   // past it e is as good as 0, or z is far out
     }
     return __builtin_amdgcn_rcpf(1.0f + e);
 }
+
+// Gates so far out that exp(-z) reaches 2^126, whose reciprocal is subnormal (and comes out as 0), while z exp(z) is a normal number down
+// to z = -91.9. There the sigmoid is exp(z), taken 2^64 times as large. Rows look for such gates (half an instruction a column) and
+// go over their columns a second time if there are any.
+constexpr float kFarGate = -87.3f;
+struct FarGate {
+    float silu, slope;   // z exp(z), (1 + z) exp(z)
+    __device__ __forceinline__ explicit FarGate(float z) {
+        constexpr float kL2E = 1.44269504089f, kDown = 5.421010862427522e-20f;   // 2^-64
+        const float c = fmaxf(z, -200.0f), t = c * kL2E, lo = fmaf(c, kL2E, -t) + c * 1.92596299e-8f;
+        float e = __builtin_amdgcn_exp2f(t + 64.0f);
+        e = fmaf(e, lo * 0.69314718056f, e);
+        silu = z * e * kDown;
+        slope = fmaf(z, e, e) * kDown;
+    }
+};
 
 // A team's rows: every `step`-th from its own, as (token, head).
 struct Walk {
@@ -177,13 +193,24 @@ __global__ __launch_bounds__(TW > 256 ? TW : 256) void gate_norm_kernel(sdm_gate
         }
         const float r = rsqrtf(fmaf(team_sum<TW>(ss, red[turn]), inv, io.eps));
         turn ^= 1;
-        float y[K][8];
+        float y[K][8], low = 0.0f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float g = zr[k].at(e);
+                low = fminf(low, g);
                 y[k][e] = xr[k].at(e) * r * wt[k][e] * (g * sigmoid_of<T>(g));
+            }
+        }
+        if (__builtin_expect(low < kFarGate, 0)) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float g = zr[k].at(e);
+                    if (g < kFarGate) y[k][e] = xr[k].at(e) * r * wt[k][e] * FarGate(g).silu;
+                }
             }
         }
         c.store(static_cast<T*>(io.out) + w.at(io.o_row, io.o_head), y);
@@ -266,16 +293,33 @@ __global__ __launch_bounds__(TW > 256 ? TW : 256) void gate_norm_back_kernel(Gat
             c.load(z + n.at(io.z_row, io.z_head), zn);
             c.load(d + n.at(p.d_row, p.d_head), dn_);
         }
-        float ss = 0.0f, dot = 0.0f, dy[K][8], oz[K][8];
+        float ss = 0.0f, dot = 0.0f, low = 0.0f, dy[K][8], oz[K][8];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float xe = xr[k].at(e), g = zr[k].at(e), de = dr[k].at(e), s = sigmoid_of<T>(g);
+                low = fminf(low, g);
                 dy[k][e] = de * (g * s);
                 oz[k][e] = de * wt[k][e] * xe * (s * fmaf(g, 1.0f - s, 1.0f));
                 ss = fmaf(xe, xe, ss);
                 dot = fmaf(dy[k][e] * wt[k][e], xe, dot);
+            }
+        }
+        if (__builtin_expect(low < kFarGate, 0)) {
+            dot = 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float xe = xr[k].at(e), g = zr[k].at(e), de = dr[k].at(e);
+                    if (g < kFarGate) {
+                        const FarGate far(g);
+                        dy[k][e] = de * far.silu;
+                        oz[k][e] = de * wt[k][e] * xe * far.slope;
+                    }
+                    dot = fmaf(dy[k][e] * wt[k][e], xe, dot);
+                }
             }
         }
         const float r = rsqrtf(fmaf(team_sum<TW>(ss, red[2 * turn]), inv, io.eps));
