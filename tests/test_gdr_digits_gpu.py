@@ -44,3 +44,26 @@ def test_a_token_keeps_them_too(dtype):
     got = sdm.gdr_step(*[t[:, 0].cuda() for t in args(x)], s, scale=0.3)
     D.check("o", got.float().cpu().numpy(), o[:, 0], 128, 120, dtype == "bf16")
     D.check("last", s.cpu().numpy(), last, 128, 120, False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("t0", [0, 40])
+def test_chunks_taken_token_by_token_keep_them(dtype, t0):
+    """A key that is not finite, alone between two resets: its chunk goes by the definition, and all other tokens' results are those
+    of finite keys."""
+    x = make(1, 64, 3, 3, 96, 72, dtype)
+    x["g"][0, t0] = x["g"][0, t0 + 1] = -float("inf")
+    h = {n: host(t) for n, t in x.items()}
+    o, last, _, _ = M.gdr_forward(*args(h), 0.3, h["state"])
+    want = dict(o=o, last=last, **M.gdr_backward(h["d_o"], *args(h), 0.3, h["state"], h["d_last"])[0])
+    x["k"] = x["k"].clone()
+    x["k"][0, t0, :, 5] = float("nan")
+    got = run(x)
+    others = [t for t in range(64) if t != t0]
+    for name in D.OUTPUTS:
+        if name == "dstate" and t0 == 0:
+            assert (got[name] == 0).all()   # cut off by the first token
+            continue
+        a, b = got[name].float().cpu().numpy(), want[name]
+        a, b = (a, b) if name in ("last", "dstate") else (a[:, others], b[:, others])
+        D.check(name, a, b, 96, 72, dtype == "bf16")
