@@ -586,25 +586,44 @@ void by_width(int D, bool vec, F f) {
     else if (D > 64) f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
     else f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
 }
-int team_width(int D, bool vec) {
-    int tw = 0;
-    by_width(D, vec, [&](auto t, auto) { tw = t; });
-    return tw;
-}
 
-// Blocks: eight per compute unit, or as many as have rows.
-constexpr int64_t kBlocks = 2048;
-// Of a backward pass: partial sums of 20 MiB at most, one block per compute unit to what is resident at once (by the kernels'
-// registers four blocks of a gate's, three of a residual's).
-int back_blocks(int64_t rows, int D, int M) {
-    const int64_t full = M == 1 ? 1024 : 768;
-    int64_t most = (int64_t(20) << 20) / (int64_t(4) * M * D);
-    most = most < 256 ? 256 : most > full ? full : most;
-    return static_cast<int>(rows < most ? rows : most);
-}
+// Blocks: as many as the kernel's own registers let be resident at once, or as many as have rows; each walks its share. (A few more would
+// run behind the others, alone: eight per compute unit for all, 2048 rows of 8192 float32 columns, took a residual 113 us, what fits
+// takes 54.)
+constexpr int64_t kUnits = 256;
 unsigned grid_of(int64_t rows, int per_block, int64_t most) {
     const int64_t n = (rows + per_block - 1) / per_block;
     return static_cast<unsigned>(n < most ? n : most);
+}
+
+// Of a backward pass each block leaves a row of partial sums, at most 24 MiB of them: the workspace has a row for every block that
+// the registers of such a pass may let be resident, for rows of one unit of columns a lane four per compute unit (a gate's, M 1) or
+// three (a residual's, M 3), for longer ones two blocks of 256 threads (a gate's) or one. 5461 bfloat16 rows of 6144 columns, a
+// gate's 108 us in 853 blocks, 87 in 256; a residual's 203 in 284 and 147 in 256.
+int back_blocks(int64_t rows, int D, int M) {
+    const int64_t most = kUnits * (D <= 2048 ? (M == 1 ? 4 : 3) : D <= 4096 && M == 1 ? 2 : 1);
+    return static_cast<int>(rows < most ? rows : most);
+}
+template <auto Kernel>
+int64_t resident(int threads) {
+    static const int per_unit = [threads] {
+        int n = 0;   // with the most LDS that its sums take: a block's teams hold 2048 columns
+        const hipError_t e = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, reinterpret_cast<const void*>(Kernel), threads, 2048 * sizeof(float));
+        return e == hipSuccess && n > 0 ? n : 1;
+    }();
+    return kUnits * per_unit;
+}
+template <auto Kernel, typename A>
+void forward_go(const A& io, int64_t rows, int TW, int threads, hipStream_t st) {
+    Kernel<<<grid_of(rows, threads / TW, resident<Kernel>(threads)), threads, 0, st>>>(io);
+}
+template <auto Kernel, typename A>
+unsigned back_go(const A& args, int64_t rows, int most, int TW, int threads, hipStream_t st) {
+    const int D = args.io.D, teams = threads / TW;
+    const int64_t fit = resident<Kernel>(threads);
+    const unsigned grid = grid_of(rows, teams, fit < most ? fit : most);
+    Kernel<<<grid, threads, teams > 1 ? static_cast<size_t>(teams) * D * 4 : 0, st>>>(args);
+    return grid;
 }
 
 bool wide(const void* p, int64_t a, int64_t b, int unit) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && a % unit == 0 && b % unit == 0; }
@@ -624,13 +643,13 @@ hipError_t gate_norm_launch(const sdm_gate_norm_io* io, hipStream_t st) {
                      wide(io->out, io->o_row, io->o_head, unit);
     by_width(io->D, vec, [&](auto tw, auto k) {
         constexpr int TW = tw, K = k, threads = TW > 256 ? TW : 256;
-        const unsigned grid = grid_of(io->N * io->H, threads / TW, kBlocks);
+        const int64_t rows = io->N * io->H;
         if (io->dtype == SDM_BF16) {
-            if (vec) gate_norm_kernel<bf16_t, TW, K, true><<<grid, threads, 0, st>>>(*io);
-            else if constexpr (TW >= 64) gate_norm_kernel<bf16_t, TW, K, false><<<grid, threads, 0, st>>>(*io);
+            if (vec) forward_go<gate_norm_kernel<bf16_t, TW, K, true>>(*io, rows, TW, threads, st);
+            else if constexpr (TW >= 64) forward_go<gate_norm_kernel<bf16_t, TW, K, false>>(*io, rows, TW, threads, st);
         } else {
-            if (vec) gate_norm_kernel<float, TW, K, true><<<grid, threads, 0, st>>>(*io);
-            else if constexpr (TW >= 64) gate_norm_kernel<float, TW, K, false><<<grid, threads, 0, st>>>(*io);
+            if (vec) forward_go<gate_norm_kernel<float, TW, K, true>>(*io, rows, TW, threads, st);
+            else if constexpr (TW >= 64) forward_go<gate_norm_kernel<float, TW, K, false>>(*io, rows, TW, threads, st);
         }
     });
     return hipGetLastError();
@@ -647,14 +666,14 @@ hipError_t gate_norm_back_launch(const sdm_gate_norm_io* io, const sdm_gate_norm
     if (io->N > 0) {
         by_width(io->D, vec, [&](auto tw, auto k) {
             constexpr int TW = tw, K = k, threads = TW > 256 ? TW : 256;
-            grid = grid_of(io->N * io->H, threads / TW, back_blocks(io->N * io->H, io->D, 1));
-            const size_t lds = threads > TW ? static_cast<size_t>(threads / TW) * io->D * 4 : 0;
+            const int64_t rows = io->N * io->H;
+            const int most = back_blocks(rows, io->D, 1);
             if (io->dtype == SDM_BF16) {
-                if (vec) gate_norm_back_kernel<bf16_t, TW, K, true><<<grid, threads, lds, st>>>(b);
-                else if constexpr (TW >= 64) gate_norm_back_kernel<bf16_t, TW, K, false><<<grid, threads, lds, st>>>(b);
+                if (vec) grid = back_go<gate_norm_back_kernel<bf16_t, TW, K, true>>(b, rows, most, TW, threads, st);
+                else if constexpr (TW >= 64) grid = back_go<gate_norm_back_kernel<bf16_t, TW, K, false>>(b, rows, most, TW, threads, st);
             } else {
-                if (vec) gate_norm_back_kernel<float, TW, K, true><<<grid, threads, lds, st>>>(b);
-                else if constexpr (TW >= 64) gate_norm_back_kernel<float, TW, K, false><<<grid, threads, lds, st>>>(b);
+                if (vec) grid = back_go<gate_norm_back_kernel<float, TW, K, true>>(b, rows, most, TW, threads, st);
+                else if constexpr (TW >= 64) grid = back_go<gate_norm_back_kernel<float, TW, K, false>>(b, rows, most, TW, threads, st);
             }
         });
         const hipError_t e = hipGetLastError();
@@ -669,13 +688,13 @@ hipError_t residual_norm_launch(const sdm_residual_norm_io* io, hipStream_t st) 
                      wide(io->n, io->n_row, 0, unit);
     by_width(io->D, vec, [&](auto tw, auto k) {
         constexpr int TW = tw, K = k, threads = TW > 256 ? TW : 256;
-        const unsigned grid = grid_of(io->N, threads / TW, kBlocks);
+        const int64_t rows = io->N;
         if (io->dtype == SDM_BF16) {
-            if (vec) residual_norm_kernel<bf16_t, TW, K, true><<<grid, threads, 0, st>>>(*io);
-            else if constexpr (TW >= 64) residual_norm_kernel<bf16_t, TW, K, false><<<grid, threads, 0, st>>>(*io);
+            if (vec) forward_go<residual_norm_kernel<bf16_t, TW, K, true>>(*io, rows, TW, threads, st);
+            else if constexpr (TW >= 64) forward_go<residual_norm_kernel<bf16_t, TW, K, false>>(*io, rows, TW, threads, st);
         } else {
-            if (vec) residual_norm_kernel<float, TW, K, true><<<grid, threads, 0, st>>>(*io);
-            else if constexpr (TW >= 64) residual_norm_kernel<float, TW, K, false><<<grid, threads, 0, st>>>(*io);
+            if (vec) forward_go<residual_norm_kernel<float, TW, K, true>>(*io, rows, TW, threads, st);
+            else if constexpr (TW >= 64) forward_go<residual_norm_kernel<float, TW, K, false>>(*io, rows, TW, threads, st);
         }
     });
     return hipGetLastError();
@@ -693,14 +712,13 @@ hipError_t residual_norm_back_launch(const sdm_residual_norm_io* io, const sdm_r
     if (io->N > 0) {
         by_width(io->D, vec, [&](auto tw, auto k) {
             constexpr int TW = tw, K = k, threads = TW > 256 ? TW : 256;
-            grid = grid_of(io->N, threads / TW, back_blocks(io->N, io->D, 3));
-            const size_t lds = threads > TW ? static_cast<size_t>(threads / TW) * io->D * 4 : 0;
+            const int most = back_blocks(io->N, io->D, 3);
             if (io->dtype == SDM_BF16) {
-                if (vec) residual_norm_back_kernel<bf16_t, TW, K, true><<<grid, threads, lds, st>>>(b);
-                else if constexpr (TW >= 64) residual_norm_back_kernel<bf16_t, TW, K, false><<<grid, threads, lds, st>>>(b);
+                if (vec) grid = back_go<residual_norm_back_kernel<bf16_t, TW, K, true>>(b, io->N, most, TW, threads, st);
+                else if constexpr (TW >= 64) grid = back_go<residual_norm_back_kernel<bf16_t, TW, K, false>>(b, io->N, most, TW, threads, st);
             } else {
-                if (vec) residual_norm_back_kernel<float, TW, K, true><<<grid, threads, lds, st>>>(b);
-                else if constexpr (TW >= 64) residual_norm_back_kernel<float, TW, K, false><<<grid, threads, lds, st>>>(b);
+                if (vec) grid = back_go<residual_norm_back_kernel<float, TW, K, true>>(b, io->N, most, TW, threads, st);
+                else if constexpr (TW >= 64) grid = back_go<residual_norm_back_kernel<float, TW, K, false>>(b, io->N, most, TW, threads, st);
             }
         });
         const hipError_t e = hipGetLastError();
