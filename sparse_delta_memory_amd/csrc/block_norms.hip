@@ -55,6 +55,9 @@ struct Cols {
     static constexpr int kRows = (TW > 256 ? TW : 256) / TW, kThreads = TW * kRows;
     int l, D;
     __device__ __forceinline__ int col(int k, int e) const { return VEC ? (k * TW + l) * 8 + e : (k * 8 + e) * TW + l; }
+    // Whether the lane has columns in unit k. Waves past the row's end skip it (half of them at 1024 columns: 88 to 80 us of a gate's
+    // backward pass of 32768 bfloat16 rows).
+    __device__ __forceinline__ bool some(int k) const { return col(k, 0) < D; }
     __device__ __forceinline__ void load(const T* p, Eight<T> (&x)[K]) const {
 #pragma unroll
         for (int k = 0; k < K; ++k) {
@@ -108,6 +111,27 @@ __device__ __forceinline__ float team_sum(float x, float* red) {
     }
 }
 
+// Two of them at once, given each wave's own sums (of the team's lanes, for teams of a wave or less).
+template <int TW>
+__device__ __forceinline__ float wave_sum(float x) { return group_sum<(TW < kWave ? TW : kWave)>(x); }
+template <int TW>
+__device__ __forceinline__ void team_sums(float& a, float& b, float* red_a, float* red_b) {
+    if constexpr (TW > kWave) {
+        if (lane_id() == 0) {
+            red_a[threadIdx.x / kWave] = a;
+            red_b[threadIdx.x / kWave] = b;
+        }
+        __syncthreads();
+        a = red_a[0];
+        b = red_b[0];
+#pragma unroll
+        for (int w = 1; w < TW / kWave; ++w) {
+            a += red_a[w];
+            b += red_b[w];
+        }
+    }
+}
+
 // 1 / (1 + exp(-z)), for z >= kFarGate. For float32 results the exponent's rounding, up to |z| / 2 units, is put back.
 template <typename T>
 __device__ __forceinline__ float sigmoid_of(float z) {
@@ -122,9 +146,10 @@ __device__ __forceinline__ float sigmoid_of(float z) {
 }
 
 // Gates so far out that exp(-z) reaches 2^126, whose reciprocal is subnormal (and comes out as 0), while z exp(z) is a normal number down
-// to z = -91.9. There the sigmoid is exp(z), taken 2^64 times as large. Rows look for such gates (half an instruction a column) and
-// go over their columns a second time if there are any.
+// to z = -91.9. There the sigmoid is exp(z), taken 2^64 times as large. Lanes look for such gates (by the largest of their bits) and
+// go over their columns a second time if there are any: 1 to 2 % of the time of a norm whose rows have none.
 constexpr float kFarGate = -87.3f;
+__device__ __forceinline__ bool far_out(uint32_t bits) { return __builtin_expect(bits > __float_as_uint(kFarGate), 0); }   // or NaN
 struct FarGate {
     float silu, slope;   // z exp(z), (1 + z) exp(z)
     __device__ __forceinline__ explicit FarGate(float z) {
@@ -193,19 +218,18 @@ __global__ __launch_bounds__(TW > 256 ? TW : 256) void gate_norm_kernel(sdm_gate
         }
         const float r = rsqrtf(fmaf(team_sum<TW>(ss, red[turn]), inv, io.eps));
         turn ^= 1;
-        float y[K][8], low = 0.0f;
+        float y[K][8];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
+            if (!c.some(k)) continue;
+            uint32_t low = 0;   // the lowest gate's bits: negative floats order as their bits do
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float g = zr[k].at(e);
-                low = fminf(low, g);
+                low = max(low, __float_as_uint(g));
                 y[k][e] = xr[k].at(e) * r * wt[k][e] * (g * sigmoid_of<T>(g));
             }
-        }
-        if (__builtin_expect(low < kFarGate, 0)) {
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
+            if (far_out(low)) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float g = zr[k].at(e);
@@ -293,23 +317,30 @@ __global__ __launch_bounds__(TW > 256 ? TW : 256) void gate_norm_back_kernel(Gat
             c.load(z + n.at(io.z_row, io.z_head), zn);
             c.load(d + n.at(p.d_row, p.d_head), dn_);
         }
-        float ss = 0.0f, dot = 0.0f, low = 0.0f, dy[K][8], oz[K][8];
+        float ss = 0.0f, dot = 0.0f, dy[K][8], oz[K][8];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
 #pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(xr[k].at(e), xr[k].at(e), ss);
+        }
+        ss = wave_sum<TW>(ss);   // its steps wait for each other: under the gates' work, not behind the branch
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dy[k][e] = oz[k][e] = 0.0f;
+            if (!c.some(k)) continue;
+            uint32_t low = 0;
+            const float before = dot;
+#pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float xe = xr[k].at(e), g = zr[k].at(e), de = dr[k].at(e), s = sigmoid_of<T>(g);
-                low = fminf(low, g);
+                low = max(low, __float_as_uint(g));
                 dy[k][e] = de * (g * s);
                 oz[k][e] = de * wt[k][e] * xe * (s * fmaf(g, 1.0f - s, 1.0f));
-                ss = fmaf(xe, xe, ss);
                 dot = fmaf(dy[k][e] * wt[k][e], xe, dot);
             }
-        }
-        if (__builtin_expect(low < kFarGate, 0)) {
-            dot = 0.0f;
-#pragma unroll
-            for (int k = 0; k < K; ++k) {
+            if (far_out(low)) {
+                dot = before;
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float xe = xr[k].at(e), g = zr[k].at(e), de = dr[k].at(e);
@@ -322,9 +353,10 @@ __global__ __launch_bounds__(TW > 256 ? TW : 256) void gate_norm_back_kernel(Gat
                 }
             }
         }
-        const float r = rsqrtf(fmaf(team_sum<TW>(ss, red[2 * turn]), inv, io.eps));
-        const float m = team_sum<TW>(dot, red[2 * turn + 1]) * r * inv;
+        dot = wave_sum<TW>(dot);
+        team_sums<TW>(ss, dot, red[2 * turn], red[2 * turn + 1]);
         turn ^= 1;
+        const float r = rsqrtf(fmaf(ss, inv, io.eps)), m = dot * r * inv;
         float ox[K][8];
 #pragma unroll
         for (int k = 0; k < K; ++k) {
