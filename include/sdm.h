@@ -673,10 +673,10 @@ typedef struct sdm_gdr_io {
  * Per stream and head, from S = state:
  *   u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),  S_t = exp(g_t) S_{t-1} + k_t u_t^T,  o_t = scale S_t^T q_t.
  * States and sums are float32; of bfloat16 inputs every product is exact, and a float32 factor enters a matrix product as
- * three bfloat16 parts, all its 24 bits. A gate that resets leaves nothing of the state before it, finite or not. Gates none of
- * which resets do not clear a state that is not finite, however small their product: every token's u takes such a column into the
- * state again. A value that is not finite makes what the rule takes it into infinity or NaN and nothing else: no earlier token,
- * stream or head, nothing past a reset.
+ * three bfloat16 parts, all its 24 bits (of values from 2^-100 up: parts below 2^-126 are dropped). A gate that resets leaves
+ * nothing of the state before it, finite or not. Gates none of which resets do not clear a state that is not finite, however
+ * small their product: every token's u takes such a column into the state again. A value that is not finite makes what the rule
+ * takes it into infinity or NaN and nothing else: no earlier token, stream or head, nothing past a reset.
  * Requires B * H <= 2^20, T <= 2^30, B * T * H <= 2^31 - 1.
  */
 sdm_status sdm_gdr_forward(const sdm_gdr_io* io, hipStream_t st);

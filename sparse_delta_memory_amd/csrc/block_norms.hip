@@ -5,10 +5,16 @@
 // silu' = s (1 + z (1 - s)), s the sigmoid. The gradient of h is that of the residual and of its norm together; it is x's, and
 // times a that of y (or of y's norm).
 //
-// All of it is bound by the bytes of the rows, each read once and written once. A team of lanes owns a row: 8 to 64 lanes of
-// a wave for rows of up to 512 columns, a block of 256 or 512 threads for longer ones, 8 or 16 columns a lane. Teams walk rows with a
-// stride, their columns' weights and weight gradients in registers and the next row's loads in flight; the blocks' weight
-// gradients are added in a fixed order by a second kernel (no atomics: the bits are the same every run).
+// The rows' bytes bound it, each read once and written once. A team of lanes owns a row: 8 to 64 lanes of a wave for rows of up to 512
+// columns, a block of 256 or 512 threads for longer ones, 8 or 16 columns a lane. Teams walk rows with a stride, their columns' weights
+// and weight gradients in registers. The next row's loads stand ahead of a row's work, but being conditional most of them are waited for
+// there; what fills the wait is the other waves. The blocks' weight gradients are added in a fixed order by a second kernel (no
+// atomics: the bits are the same every run).
+//
+// Of bfloat16 rows, 64 MiB a tensor, TB/s of these bytes at 64 / 512 / 1024 / 2048 / 4096 / 8192 columns: gate_norm 6.0, 5.5,
+// 5.3, 5.4, 5.5, 5.5 and its backward 4.8, 4.7, 4.2, 4.4, 4.5, 4.4; residual_norm 6.0, 5.4, 5.4, 5.4, 4.8, 4.6. Its backward (4.6, 4.5,
+// 3.9, 4.0, 3.5, 2.8) holds six arrays of weights and sums: past 2048 columns that is one wave per SIMD, past 4096 two with 46 to 201
+// registers spilled (float32 there: 1.9), and rows of 513 to 1024 columns leave half of its waves without columns of their own.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>

@@ -28,15 +28,15 @@
 // in its sequence (a reset at it and behind it) shows in no r, but the state's product takes the whole tile of keys: N's diagonal, 0
 // otherwise, is NaN at a key that is not finite, and so is then some r of every column.
 //
-// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): forward 365 us, some 95 of them the records (53 KiB a chunk and
-// head read and written) and 270 the way along 64 chunks: 4.2 us a chunk, where a wave's 216 matrix instructions keep its SIMD's
-// unit busy for 3456 of 8100 cycles; the steps of a chunk follow from each other, and with 16 columns a wave there is one
-// computing wave per SIMD to fill them. Not kept: more waves for the outputs, with the state's parts handed over in LDS (430 us:
-// loads of q in the operands' layout take 400 cycles each, and two barriers a chunk); reads from LDS a step ahead by hand (283
-// beside 283 for the kernel; past 256 registers 650); a chunk's results stored behind the next chunk's barrier (the same). Backward
-// 1.52 ms: records 135, states 260, gradients 350, the rest 980, whose 272 KiB a chunk and head come and go at 2.3 TB/s: a
-// block's loads and products follow each other, and its 157 KiB of LDS leave no room for a second block (all loads issued at
-// once, ahead of the gates: the same time).
+// What bounds it, 8 x 4096 tokens x 16 heads of 128 (bfloat16): forward 370 us, by the profile (whose kernels add up to a little more) 113 of
+// them the records (53 KiB a chunk and head read and written) and 273 the way along 64 chunks: 4.2 us a chunk, where a wave's 216
+// matrix instructions keep its SIMD's unit busy for 3456 of 8100 cycles; the steps of a chunk follow from each other, and with 16 columns
+// a wave there is one computing wave per SIMD to fill them. Not kept: more waves for the outputs, with the state's parts handed over in LDS
+// (430 us: loads of q in the operands' layout take 400 cycles each, and two barriers a chunk); reads from LDS a step ahead by hand
+// (283 beside 283 for the kernel; past 256 registers 650); a chunk's results stored behind the next chunk's barrier (the same). Backward
+// 1530 us: records 122, states 227, gradients 300, the rest 893, whose 304 KiB a chunk and head (192 of them float32 states, gradients, r and
+// du) come and go at 2.9 TB/s: a block's loads and products follow each other, and its 157 KiB of LDS leave no room for a second block
+// (all loads issued at once, ahead of the gates: the same time).
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -469,7 +469,8 @@ __device__ __forceinline__ void store_four(void* out, int64_t at, f32x4 v, int l
 
 // Where the tiles of two chunks fit into LDS side by side, four more waves load the next chunk's while these compute (issuing
 // its 77 KiB of loads by themselves kept the computing waves for 3000 of a chunk's 10000 cycles). float32 chunks of keys past 64
-// columns are loaded one by one.
+// columns do not fit twice and are loaded one by one (8 x 4096 x 16 heads, float32, 64 / 128 columns: forward 520 / 1240 us, backward
+// 1505 / 3290).
 template <typename T, int KD>
 constexpr bool kTwo = sizeof(T) == 2 || KD == 64;
 template <typename T, int KD>
@@ -1771,9 +1772,10 @@ int chunks_of(int T) { return (T + kL - 1) / kL; }
 
 // Segments of the time axis. A block's way along it is most of the time where there are few blocks, so the axis is cut: a pass
 // makes every segment's own state and transition (as many columns again as the state has rows), a kernel chains them, and the main
-// pass runs on all segments at once. Rounds of blocks over the compute units times a segment's chunks, in units of a chunk (3.5 us,
-// 3 without outputs; a step of the chain is 1.5), say whether and how finely: 1 x 16384 tokens x 8 heads of 128, forward, 925 us whole
-// and 226 in 16 segments; 8 x 4096 x 16 stays whole.
+// pass runs on all segments at once. Rounds of blocks over the compute units times a segment's chunks, at 3.5 us a chunk, 3 without
+// outputs, and 1.5 a step of the chain, say whether and how finely: 1 x 16384 tokens x 8 heads of 128, forward, 925 us whole and 230 in
+// 16 segments; 8 x 4096 x 16 stays whole. The prices are those of bfloat16 forward at 128 columns; the backward pass, float32 (about twice
+// as much) and narrower heads (half) are cut by them too. The same tokens and heads: backward 670, float32 595 and 1435, 64 columns 126 and 370.
 constexpr int kUnits = 256;
 struct SegPlan {
     int nseg, seg;
