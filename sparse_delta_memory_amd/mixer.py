@@ -179,10 +179,10 @@ class DeltaBlock:
         return self.residual(x, gate_norm(o, z, self.o_norm).flatten(1) @ self.w_out)
 
     def backward(self, d_x, d_n, saved, d_state=None):
-        """Gradients from those of prompt's x and n, and of the state that it returned (d_state [P, heads, d, d] float32; None: zero): a dict
+        """Gradients from those of prompt's x (None: zero) and n, and of the state that it returned (d_state [P, heads, d, d] float32; None: zero): a dict
         of x, n, state and every parameter. Of a prompt run in parts the last part comes first, and its "state" is the d_state of the one before."""
         n, pos, q0, k0, ins, z, g, o, y, h, state = saved
-        d_x, d_n = d_x.contiguous(), d_n.contiguous()   # as prompt's rows
+        d_x, d_n = None if d_x is None else d_x.contiguous(), d_n.contiguous()   # as prompt's rows
         r = residual_norm_backward(d_x, d_n, h, y, self.next_norm, scale=self.scale, norm_y=self.norm_y, y_weight=self.y_norm)
         dy = r["dy"].flatten(0, 1)
         out = dict(x=r["dx"], next_norm=r["dw"], scale=r["dscale"], y_norm=r["dwy"])

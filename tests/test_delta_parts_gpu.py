@@ -46,6 +46,9 @@ def test_parts_have_the_gradients_of_the_whole(norm_y):
     none, zero = b.backward(d_x, d_n, saved), b.backward(d_x, d_n, saved, d_state=torch.zeros_like(d_state))
     assert torch.equal(none["state"], zero["state"]) and torch.equal(none["w"], zero["w"])
     assert not torch.equal(none["w"], want["w"])
+    # So is x's.
+    none, zero = b.backward(None, d_n, saved), b.backward(torch.zeros_like(d_x), d_n, saved)
+    assert all(none[k] is zero[k] is None or torch.equal(none[k], zero[k]) for k in zero)
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
